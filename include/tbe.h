@@ -21,6 +21,11 @@
  *                        kimbodo.com/?p=28372, "What Happened" and "Kimbodo
  *                        Engineering Perspective".
  *
+ * Without a handle it also has three layers that work on looked-up rows, with
+ * their gradients: dropout (tbe_dropout), a gated linear recurrence over jagged
+ * sequences (tbe_scan_*) and a linear layer for each of several ragged row
+ * groups (tbe_grouped_linear*).
+ *
  * The batch format (flat ids + CSR offsets whose last entry is the id count)
  * follows the example call in "Optimizing Recommendation Systems with FBTriton
  * Table Batched Embeddings" (explore.n1n.ai), "Implementation Guide:
@@ -345,6 +350,115 @@ tbe_status tbe_set_option(tbe_handle* handle, int32_t option, int64_t value);
  * events are then dropped. */
 tbe_status tbe_stage_times(tbe_handle* handle, float* ms, const char** names, int32_t capacity,
                            int32_t* count);
+
+/* ---------------------------------------------------------------------------
+ * Layers on looked-up rows.  They need no handle: every call takes its sizes,
+ * row strides (elements between the starts of rows; the elements of a row are
+ * adjacent) and buffers, enqueues kernels on `stream` and returns.  The
+ * argument checks run on the host first: on any error nothing is enqueued.
+ * They neither allocate nor clear memory by copies, so they may be captured
+ * into a HIP graph.  Rows are fp32, fp16 or bf16 (tbe_dtype); sums and states
+ * are fp32 and a result is rounded once, to nearest even.  Buffers are aligned
+ * to their elements (workspaces to 256 bytes) and outputs do not overlap
+ * inputs unless stated.  Offsets are int32 or int64 (tbe_index_dtype) on the
+ * device and are not checked there beyond being clamped to the row count, so
+ * bad ones give wrong values, never accesses out of range.
+ * ------------------------------------------------------------------------- */
+
+/* Dropout with a mask that is computed, never stored: element n of the
+ * row-major [rows, cols] matrix is kept where word n % 4 of the 7-round
+ * Philox4x32 block with counter offset + n / 4 (mod 2^64; the counter's upper
+ * 64 bits are 0) and key `seed` is at least floor(p 2^32), and then scaled by
+ * 1 / (1 - p).  y = kept ? x / (1 - p) : 0, plus residual where given.  A
+ * dropped element is 0 whatever x holds.  p = 1 drops everything.  The
+ * gradient with respect to x is the same call on the output's gradient,
+ * without the residual, with the same p, seed and offset (the residual's
+ * gradient is the output's).  The call uses ceil(rows cols / 4) counters: the
+ * next call's offset under the same seed should be that much larger.  y may be
+ * x or residual itself (same strides).  rows * cols <= 2^35. */
+tbe_status tbe_dropout(const void* x, int64_t x_stride, const void* residual,
+                       int64_t residual_stride, void* y, int64_t y_stride, int64_t rows,
+                       int64_t cols, int32_t dtype, double p, uint64_t seed, uint64_t offset,
+                       void* stream);
+
+/* Gates of the recurrence h_t = a_t h_{t-1} + b_t x_t, per channel. */
+typedef enum {
+  TBE_GATE_SIGMOID = 0,  /* a = sigmoid(gate), b = 1 - a */
+  TBE_GATE_DECAY = 1     /* a = gate, b = 1 */
+} tbe_gate;
+
+/* The recurrence for one new token of each sequence: next_state = a state +
+ * b x (fp32 [seqs, dim]) and h, the same rounded to `dtype` ([seqs, dim]).
+ * state NULL: zeros; next_state may be state itself (with stride dim). */
+tbe_status tbe_scan_step(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride,
+                         const float* state, int64_t state_stride, void* h, float* next_state,
+                         int64_t seqs, int64_t dim, int32_t dtype, int32_t gate_kind,
+                         void* stream);
+
+/* A batch of jagged sequences: sequence s holds the tokens offsets[s] ..
+ * offsets[s+1] of x and gate ([tokens, dim]); offsets [seqs + 1] start at 0
+ * and end at tokens.  initial: fp32 [seqs, dim], the state before each first
+ * token (NULL: zeros; stride 0: one row for all).  tokens, seqs and dim are
+ * below 2^31 - 1. */
+typedef struct {
+  int64_t tokens, seqs, dim;
+  int32_t dtype, gate_kind, index_dtype;
+  const void* x;
+  int64_t x_stride;
+  const void* gate;
+  int64_t gate_stride;
+  const void* offsets;
+  const float* initial;
+  int64_t initial_stride;
+} tbe_scan_input;
+
+/* Bytes of the carry that a forward call leaves for the backward pass, and of
+ * the workspace either call needs (0: none). */
+tbe_status tbe_scan_sizes(int64_t tokens, int64_t seqs, int64_t dim, int32_t dtype,
+                          size_t* carry_bytes, size_t* workspace_bytes);
+
+/* h [tokens, dim] (contiguous, the rows' type): every state; final: fp32
+ * [seqs, dim], each sequence's last state (its initial one where it is empty);
+ * carry: 16-byte aligned, tbe_scan_sizes bytes, or NULL where no backward pass
+ * follows. */
+tbe_status tbe_scan_forward(const tbe_scan_input* input, void* h, float* final, float* carry,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of the forward call with the same input, whose carry this is:
+ * grad_h [tokens, dim] (the rows' type) and grad_final (fp32 [seqs, dim]) are
+ * the outputs' (NULL: zeros); dx and dgate [tokens, dim] get the rows' type,
+ * dinitial fp32 [seqs, dim] (NULL: not wanted). */
+tbe_status tbe_scan_backward(const tbe_scan_input* input, const float* carry, const void* grad_h,
+                             int64_t grad_h_stride, const float* grad_final,
+                             int64_t grad_final_stride, void* dx, int64_t dx_stride, void* dgate,
+                             int64_t dgate_stride, float* dinitial, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace of the grouped linear layer's two calls (0: none). */
+tbe_status tbe_grouped_linear_sizes(int64_t rows, int64_t groups, int64_t in_features,
+                                    int64_t out_features, int32_t dtype, size_t* forward_bytes,
+                                    size_t* backward_bytes);
+
+/* A linear layer for each group of consecutive rows: group g holds the rows
+ * offsets[g] .. offsets[g+1] of x [rows, in_features] and y [rows,
+ * out_features], y_n = weight[g] x_n + bias[g].  weight [groups, out_features,
+ * in_features] and bias [groups, out_features] (NULL: none) are contiguous;
+ * offsets [groups + 1] start at 0 and end at rows.  Groups may be empty. */
+tbe_status tbe_grouped_linear(const void* x, int64_t x_stride, const void* weight, const void* bias,
+                              const void* offsets, int32_t index_dtype, void* y, int64_t y_stride,
+                              int64_t rows, int64_t groups, int64_t in_features,
+                              int64_t out_features, int32_t dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Its gradients: dx [rows, in_features], dweight and dbias (contiguous; empty
+ * groups get zeros) from grad [rows, out_features].  Each of the three may be
+ * NULL (not wanted). */
+tbe_status tbe_grouped_linear_backward(const void* x, int64_t x_stride, const void* weight,
+                                       const void* offsets, int32_t index_dtype, const void* grad,
+                                       int64_t grad_stride, void* dx, int64_t dx_stride,
+                                       void* dweight, void* dbias, int64_t rows, int64_t groups,
+                                       int64_t in_features, int64_t out_features, int32_t dtype,
+                                       void* workspace, size_t workspace_bytes, void* stream);
 
 const char* tbe_status_string(tbe_status status);
 int32_t tbe_abi_version(void);

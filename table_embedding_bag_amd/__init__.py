@@ -28,7 +28,9 @@ __all__ = [
     "FLAG_SPLIT_BAGS", "FLAG_COUNT_BACKWARD",
     "OPTION_LONG_RUN_THRESHOLD", "OPTION_PROFILE", "OPTION_SORT", "OPTION_SPIN_LIMIT",
     "OPTION_LDS_FORWARD",
-    "EXPORTED_SYMBOLS",
+    "EXPORTED_SYMBOLS", "GATE_SIGMOID", "GATE_DECAY",
+    "dropout", "dropout_backward", "scan_step", "scan_forward", "scan_backward",
+    "grouped_linear", "grouped_linear_backward",
 ]
 
 F32, F16, BF16 = 0, 1, 2
@@ -40,6 +42,7 @@ FLAG_SPLIT_BAGS = 16
 FLAG_COUNT_BACKWARD = 32
 OPTION_LONG_RUN_THRESHOLD, OPTION_PROFILE, OPTION_SORT, OPTION_SPIN_LIMIT = 1, 2, 3, 4
 OPTION_LDS_FORWARD = 5
+GATE_SIGMOID, GATE_DECAY = 0, 1
 STATIC_SCRATCH_BYTES = 64 << 20   # TBE_STATIC_SCRATCH_BYTES
 
 STATUS = {
@@ -53,7 +56,9 @@ EXPORTED_SYMBOLS = (
     "tbe_backward_update", "tbe_forward_group", "tbe_backward_update_grouped", "tbe_psw_grad",
     "tbe_set_option", "tbe_stage_times", "tbe_status_string", "tbe_abi_version",
     "tbe_check_device_status", "tbe_backward_update_no_alloc", "tbe_forward_scratch_size",
-    "tbe_set_forward_scratch",
+    "tbe_set_forward_scratch", "tbe_dropout", "tbe_scan_step", "tbe_scan_sizes",
+    "tbe_scan_forward", "tbe_scan_backward", "tbe_grouped_linear_sizes", "tbe_grouped_linear",
+    "tbe_grouped_linear_backward",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -79,6 +84,15 @@ class _Config(ctypes.Structure):
 class _Runs(ctypes.Structure):
     _fields_ = [("unique_ids", ctypes.c_void_p), ("run_lengths", ctypes.c_void_p),
                 ("num_unique", ctypes.c_void_p)]
+
+
+class _ScanInput(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("gate_kind", ctypes.c_int32),
+                ("index_dtype", ctypes.c_int32), ("x", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64), ("gate", ctypes.c_void_p),
+                ("gate_stride", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+                ("initial", ctypes.c_void_p), ("initial_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -114,13 +128,27 @@ def load():
     lib.tbe_status_string.restype = ctypes.c_char_p
     lib.tbe_forward_scratch_size.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
     lib.tbe_set_forward_scratch.argtypes = [P, P, ctypes.c_size_t]
+    size_p, scan_p, z = ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(_ScanInput), ctypes.c_size_t
+    lib.tbe_dropout.argtypes = [P, i64, P, i64, P, i64, i64, i64, i32, ctypes.c_double,
+                                ctypes.c_uint64, ctypes.c_uint64, P]
+    lib.tbe_scan_step.argtypes = [P, i64, P, i64, P, i64, P, P, i64, i64, i32, i32, P]
+    lib.tbe_scan_sizes.argtypes = [i64, i64, i64, i32, size_p, size_p]
+    lib.tbe_scan_forward.argtypes = [scan_p, P, P, P, P, z, P]
+    lib.tbe_scan_backward.argtypes = [scan_p, P, P, i64, P, i64, P, i64, P, i64, P, P, z, P]
+    lib.tbe_grouped_linear_sizes.argtypes = [i64, i64, i64, i64, i32, size_p, size_p]
+    lib.tbe_grouped_linear.argtypes = [P, i64, P, P, P, i32, P, i64, i64, i64, i64, i64, i32, P, z,
+                                       P]
+    lib.tbe_grouped_linear_backward.argtypes = [P, i64, P, P, i32, P, i64, P, i64, P, P, i64, i64,
+                                                i64, i64, i32, P, z, P]
     lib.tbe_abi_version.argtypes = []
     lib.tbe_abi_version.restype = i32
     for name in ("tbe_create", "tbe_forward", "tbe_backward_workspace_size", "tbe_backward_update",
                  "tbe_forward_group", "tbe_backward_update_grouped", "tbe_psw_grad",
                  "tbe_set_option", "tbe_stage_times", "tbe_check_device_status",
                  "tbe_backward_update_no_alloc", "tbe_forward_scratch_size",
-                 "tbe_set_forward_scratch"):
+                 "tbe_set_forward_scratch", "tbe_dropout", "tbe_scan_step", "tbe_scan_sizes",
+                 "tbe_scan_forward", "tbe_scan_backward", "tbe_grouped_linear_sizes",
+                 "tbe_grouped_linear", "tbe_grouped_linear_backward"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -390,3 +418,16 @@ class TBE:
             self.close()
         except Exception:
             pass
+
+
+_LAYERS = ("dropout", "dropout_backward", "scan_step", "scan_forward", "scan_backward",
+           "grouped_linear", "grouped_linear_backward")
+
+
+def __getattr__(name):
+    """The layers on first use: their module needs torch, this one alone does not."""
+    if name in _LAYERS:
+        from . import layers
+        globals()[name] = value = getattr(layers, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
