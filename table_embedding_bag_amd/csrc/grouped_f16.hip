@@ -1,0 +1,11 @@
+// grouped_f16.hip -- the grouped linear layer's kernels for f16 rows.
+#include <hip/hip_runtime.h>
+
+#define TBE_GROUPED_KERNELS
+#include "grouped.hpp"
+
+namespace tbe {
+hipError_t launch_grouped_f16(const GroupedArgs& a, bool backward, hipStream_t s) {
+  return launch_grouped<kF16>(a, backward, s);
+}
+}  // namespace tbe
