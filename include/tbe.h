@@ -399,7 +399,8 @@ tbe_status tbe_scan_step(const void* x, int64_t x_stride, const void* gate, int6
  * offsets[s+1] of x and gate ([tokens, dim]); offsets [seqs + 1] start at 0
  * and end at tokens.  initial: fp32 [seqs, dim], the state before each first
  * token (NULL: zeros; stride 0: one row for all).  tokens, seqs and dim are
- * below 2^31 - 1. */
+ * below 2^31 - 1, tokens rounded up to 128 times dim rounded up to 64 below
+ * 2^36. */
 typedef struct {
   int64_t tokens, seqs, dim;
   int32_t dtype, gate_kind, index_dtype;

@@ -10,6 +10,8 @@
 // h, dx and dg are rounded once, to the rows' type.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "layers.hpp"
 
 using namespace tbe;
@@ -75,6 +77,7 @@ struct ScanArgs {
   const void* x;
   const void* gate;
   const void* offsets;
+  int32_t index64;
   const float* initial;  // null: zeros
   int64_t x_stride, gate_stride, initial_stride;
   // forward
@@ -92,90 +95,544 @@ struct ScanArgs {
   float* dinitial;            // null: not asked for
 };
 
-template <typename IT>
+// Offsets are clamped to the tokens, so that bad ones read and write nothing out of range.
 __device__ __forceinline__ int64_t offset_at(const ScanArgs& a, int64_t s) {
-  const int64_t o = static_cast<const IT*>(a.offsets)[s];
+  const int64_t o = a.index64 ? static_cast<const int64_t*>(a.offsets)[s]
+                              : static_cast<const int32_t*>(a.offsets)[s];
   return o < 0 ? 0 : (o > a.tokens ? a.tokens : o);
 }
 
-// A thread walks one channel of one sequence.
-template <int ST, bool SIGMOID, typename IT>
-__global__ __launch_bounds__(kBlock) void scan_walk(ScanArgs a) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
-  const int64_t s = i / a.dim, c = i - s * a.dim;
-  if (s >= a.seqs) return;
-  const int64_t lo = offset_at<IT>(a, s), hi = offset_at<IT>(a, s + 1);
-  float v = a.initial ? a.initial[s * a.initial_stride + c] : 0.0f;
-  for (int64_t t = lo; t < hi; ++t) {
-    if (a.carry) a.carry[t * a.dim + c] = v;
-    const Gates k = gates<SIGMOID>(load_one<ST>(a.gate, t * a.gate_stride + c));
-    v = k.a * v + k.b * load_one<ST>(a.x, t * a.x_stride + c);
-    store_one<ST>(a.h, t * a.dim + c, v);
-  }
-  a.final[s * a.dim + c] = v;
+// The token axis is cut into tiles whatever the sequences: W waves of kSpan
+// tokens each, and 64 V channels, V neighbours a lane.  Within its span a wave
+// reduces the recurrence to "state out = A state in + B" per channel, the waves'
+// pairs join in LDS, and the tiles' in the workspace: a tile publishes its own
+// (A, B), or, where a sequence starts inside, the state it ends with, which
+// depends on no earlier tile; it then looks back for the nearest tile whose end
+// state is known and folds the pairs between, first tile first, into its own
+// start state and the end state it publishes.  Every state is the same sequence
+// of operations whichever tile was found, so results do not depend on timing.
+// The waves then run their tokens from their start states.  One pass: inputs are
+// read once and stay in registers in between.
+//
+// What passes between tiles is written and read with 8- and 4-byte device-scope
+// atomics; a value is there once it differs from all ones (a NaN that canonical()
+// never lets through).  Tiles are numbered by a ticket taken at a workgroup's
+// start, so every tile waited for is running or done.
+constexpr int kSpan = 16;                  // tokens a wave; also of a carry row
+constexpr uint64_t kNoPair = ~uint64_t{0};
+constexpr uint32_t kNoState = ~uint32_t{0};
+constexpr uint32_t kSpinLimit = 1u << 22;  // polls before a wait gives up (states turn NaN)
+
+struct ScanWork {
+  uint32_t* ticket;
+  int32_t* lo;       // [tiles + 1]: first offset at or past the tile's first token
+  uint64_t* pairs;   // [tiles, dim]
+  uint32_t* states;  // [tiles, dim]
+  int64_t tiles;
+  int32_t channel_blocks;
+};
+
+__device__ __forceinline__ float canonical(float v) {
+  return v != v ? __uint_as_float(0x7FC00000u) : v;
+}
+__device__ __forceinline__ uint64_t ld_pair(const uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint32_t ld_state(const uint32_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void st_pair(uint64_t* p, float A, float B) {
+  const uint64_t v = static_cast<uint64_t>(__float_as_uint(canonical(B))) << 32 |
+                     __float_as_uint(canonical(A));
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void st_state(uint32_t* p, float v) {
+  __hip_atomic_store(p, __float_as_uint(canonical(v)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <int ST, bool SIGMOID, typename IT>
-__global__ __launch_bounds__(kBlock) void scan_walk_back(ScanArgs a) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
-  const int64_t s = i / a.dim, c = i - s * a.dim;
-  if (s >= a.seqs) return;
-  const int64_t lo = offset_at<IT>(a, s), hi = offset_at<IT>(a, s + 1);
-  float mu = a.grad_final ? a.grad_final[s * a.grad_final_stride + c] : 0.0f;
-  for (int64_t t = hi - 1; t >= lo; --t) {
-    const Gates k = gates<SIGMOID>(load_one<ST>(a.gate, t * a.gate_stride + c));
-    const float before = a.carried[t * a.dim + c];
-    const float lam = (a.grad_h ? load_one<ST>(a.grad_h, t * a.grad_h_stride + c) : 0.0f) + mu;
-    store_one<ST>(a.dx, t * a.dx_stride + c, k.b * lam);
-    float dg = lam * before;
-    if constexpr (SIGMOID)
-      dg = lam * (before - load_one<ST>(a.x, t * a.x_stride + c)) * (k.a * k.b);
-    store_one<ST>(a.dgate, t * a.dgate_stride + c, dg);
-    mu = k.a * lam;
+// Before the tiles: nothing published, the tiles' first offsets found, and the
+// empty sequences' outputs, which belong to no token (copied from `from`).
+__global__ __launch_bounds__(kBlock) void scan_prepare(ScanArgs a, ScanWork w, int32_t tile_tokens,
+                                                       const float* from, int64_t from_stride,
+                                                       float* to) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+  const int64_t all = static_cast<int64_t>(gridDim.x) * kBlock;
+  if (id == 0) *w.ticket = 0u;
+  const int64_t words = w.tiles * a.dim;
+  for (int64_t i = id; i < words; i += all) {
+    w.pairs[i] = kNoPair;
+    w.states[i] = kNoState;
   }
-  if (a.dinitial) a.dinitial[s * a.dim + c] = mu;
+  if (w.tiles > 0)
+    for (int64_t k = id; k <= w.tiles; k += all) {
+      const int64_t token = k * tile_tokens;
+      int64_t lo = 0, hi = a.seqs + 1;
+      while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (offset_at(a, mid) < token) lo = mid + 1;
+        else hi = mid;
+      }
+      w.lo[k] = static_cast<int32_t>(lo);
+    }
+  if (!to) return;
+  const int lane = lane_id();
+  for (int64_t s0 = id - lane; s0 < a.seqs; s0 += all) {
+    const int64_t s = s0 + lane;
+    uint64_t empty = __ballot(s < a.seqs && offset_at(a, s) >= offset_at(a, s + 1));
+    for (; empty; empty &= empty - 1) {
+      const int64_t e = s0 + __builtin_ctzll(empty);
+      for (int64_t c = lane; c < a.dim; c += 64)
+        to[e * a.dim + c] = from ? from[e * from_stride + c] : 0.0f;
+    }
+  }
 }
 
-template <int ST, bool SIGMOID, typename IT>
-hipError_t launch_scan(const ScanArgs& a, bool back, hipStream_t s) {
-  const int64_t blocks = (a.seqs * a.dim + kBlock - 1) / kBlock;
+// What the waves of a tile share.
+template <int V, int W>
+struct TileShared {
+  static constexpr int kWindow = 2 * W;  // tiles looked back on at a time
+  uint32_t ticket;
+  int32_t lists[2][W * kSpan];           // sequence that starts at / ends with a token, or -1
+  uint32_t resets[W];                    // the wave's span holds a reset
+  float A[W][64 * V], B[W][64 * V];
+  float pair_a[kWindow][64 * V], pair_b[kWindow][64 * V];
+  uint32_t state[kWindow][64 * V];
+};
+
+// Which sequences start in and end with the tile's tokens.
+template <int V, int W>
+__device__ __forceinline__ void list_sequences(const ScanArgs& a, const ScanWork& w, int64_t tile,
+                                               TileShared<V, W>& sh) {
+  constexpr int kTokens = W * kSpan;
+  const int64_t t0 = tile * kTokens;
+  const int64_t lo = w.lo[tile], hi = w.lo[tile + 1];
+  for (int64_t i = lo + threadIdx.x; i <= hi && i <= a.seqs; i += 64 * W) {
+    const int64_t o = offset_at(a, i);
+    const int64_t at = o - t0;
+    if (i < a.seqs && at >= 0 && at < kTokens && offset_at(a, i + 1) > o)
+      sh.lists[0][at] = static_cast<int32_t>(i);
+    if (i > 0 && at >= 1 && at <= kTokens && offset_at(a, i - 1) < o)
+      sh.lists[1][at - 1] = static_cast<int32_t>(i - 1);
+  }
+}
+
+// A tile's start state per channel (the state after its predecessor in scan
+// order), the tile's own pair, and the end state published.  STEP: +1 where
+// tile k follows tile k - 1, -1 where it follows tile k + 1.
+template <int V, int W, int STEP>
+__device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w, int64_t tile,
+                                           int64_t c0, int nv, TileShared<V, W>& sh,
+                                           float (&start)[V]) {
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  // the tile's pair: wave by wave in scan order
+  float A[V], B[V];
+  bool reset = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+#pragma unroll
+  for (int q = 0; q < W; ++q) {
+    const int i = STEP > 0 ? q : W - 1 - q;
+    const bool r = sh.resets[i];
+    reset |= r;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float wa = sh.A[i][lane * V + v], wb = sh.B[i][lane * V + v];
+      B[v] = r ? wb : fmaf(wa, B[v], wb);
+      A[v] *= wa;
+    }
+  }
+  const bool first = STEP > 0 ? tile == 0 : tile == w.tiles - 1;
+  const int64_t mine = tile * a.dim + c0;
+  if (wave == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v < nv) {
+        if (reset || first) st_state(w.states + mine + v, B[v]);
+        else st_pair(w.pairs + mine + v, A[v], B[v]);
+      }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) start[v] = 0.0f;
+  // no state comes in where the tile's first token (in scan order) starts afresh
+  if (first || sh.lists[STEP > 0 ? 0 : 1][STEP > 0 ? 0 : W * kSpan - 1] >= 0) return;
+  constexpr int kWindow = TileShared<V, W>::kWindow;
+  uint32_t spins = 0;
+  for (int round = 0;; ++round) {
+    // The first look is at the nearest tile alone (with short sequences it knows
+    // its end state by itself), the later ones at the whole window.
+    const int n = round == 0 ? 1 : kWindow;
+    __syncthreads();
+    for (int e = wave; e < n; e += W) {
+      const int64_t k = tile - static_cast<int64_t>(STEP) * (e + 1);
+      const bool real = k >= 0 && k < w.tiles;
+      uint64_t pair[V];
+      uint32_t state[V];
+      bool there;
+      do {
+        there = true;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          pair[v] = 0;
+          state[v] = 0;
+          if (real && v < nv) {
+            state[v] = ld_state(w.states + k * a.dim + c0 + v);
+            pair[v] = ld_pair(w.pairs + k * a.dim + c0 + v);
+            there = there && (state[v] != kNoState || pair[v] != kNoPair);
+          }
+        }
+        if (__all(there)) break;
+        if (++spins > kSpinLimit) break;
+        __builtin_amdgcn_s_sleep(1);
+      } while (true);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        sh.pair_a[e][lane * V + v] = __uint_as_float(static_cast<uint32_t>(pair[v]));
+        sh.pair_b[e][lane * V + v] = __uint_as_float(static_cast<uint32_t>(pair[v] >> 32));
+        sh.state[e][lane * V + v] = state[v];
+      }
+    }
+    __syncthreads();
+    // from the nearest tile whose end state is there, through the pairs of those
+    // after it (a tile without a state has its pair)
+    bool have[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) have[v] = false;
+    for (int e = n - 1; e >= 0; --e)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint32_t s = sh.state[e][lane * V + v];
+        const float on = fmaf(sh.pair_a[e][lane * V + v], start[v], sh.pair_b[e][lane * V + v]);
+        start[v] = s != kNoState ? __uint_as_float(s) : on;
+        have[v] = have[v] || s != kNoState;
+      }
+    bool all = true;
+#pragma unroll
+    for (int v = 0; v < V; ++v) all = all && have[v];
+    if (__all(all)) break;
+    if (round > static_cast<int>(kSpinLimit >> 4)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) start[v] = __uint_as_float(0x7FC00000u);
+      break;
+    }
+  }
+  if (wave == 0 && !reset) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v < nv) st_state(w.states + mine + v, fmaf(A[v], start[v], B[v]));
+  }
+}
+
+// The state a wave starts from: the tile's, taken through the waves before it.
+template <int V, int W, int STEP>
+__device__ __forceinline__ void wave_start(const TileShared<V, W>& sh, int wave, int lane,
+                                           float (&state)[V]) {
+#pragma unroll
+  for (int q = 0; q < W; ++q) {
+    const int i = STEP > 0 ? q : W - 1 - q;
+    if (STEP > 0 ? i < wave : i > wave) {
+      const bool r = sh.resets[i];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float wb = sh.B[i][lane * V + v];
+        state[v] = r ? wb : fmaf(sh.A[i][lane * V + v], state[v], wb);
+      }
+    }
+  }
+}
+
+// V channels of a row for each token of a span: those that exist (tokens below
+// `tokens`, nv channels), the others 0.
+template <int ST, int V>
+__device__ __forceinline__ void load_span(const void* base, int64_t stride, int64_t t0, int tokens,
+                                          int64_t c0, int nv, StoredVec<ST, V> (&out)[kSpan]) {
+#pragma unroll
+  for (int i = 0; i < kSpan; ++i) {
+    out[i] = StoredVec<ST, V>{};
+    if (i < tokens) {
+      const int64_t at = (t0 + i) * stride + c0;
+      if (nv == V) out[i] = load_vec<ST, V>(base, at);
+      else if (nv > 0) out[i][0] = static_cast<const typename Stored<ST>::type*>(base)[at];
+    }
+  }
+}
+// The rows of `base` of the sequences whose bits are set in mask (list: lane i
+// holds the sequence of token i), 0 for the others.
+template <int V>
+__device__ __forceinline__ void load_marked(const float* base, int64_t stride, uint32_t mask,
+                                            int32_t list, int64_t c0, int nv,
+                                            float (&out)[kSpan][V]) {
+#pragma unroll
+  for (int i = 0; i < kSpan; ++i) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) out[i][v] = 0.0f;
+    if (base && (mask >> i & 1u)) {
+      const int64_t at = static_cast<int64_t>(__builtin_amdgcn_readlane(list, i)) * stride + c0;
+      if (nv == V) {
+        const auto r = load_vec<kF32, V>(base, at);
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[i][v] = r[v];
+      } else if (nv > 0) {
+        out[i][0] = base[at];
+      }
+    }
+  }
+}
+template <int ST, int V>
+__device__ __forceinline__ void store_row(void* base, int64_t at, int nv, const float (&f)[V]) {
+  if (nv == V) {
+    StoredVec<ST, V> o;
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = static_cast<typename Stored<ST>::type>(f[v]);
+    store_vec<ST, V>(base, at, o);
+  } else if (nv > 0) {
+    store_one<ST>(base, at, f[0]);
+  }
+}
+
+// Tile and channels of a workgroup, in the order of the tickets, and the lists cleared.
+template <int V, int W>
+__device__ __forceinline__ uint32_t take_ticket(const ScanWork& w, TileShared<V, W>& sh) {
+  if (threadIdx.x == 0) sh.ticket = atomicAdd(w.ticket, 1u);
+  for (int i = threadIdx.x; i < 2 * W * kSpan; i += 64 * W) (&sh.lists[0][0])[i] = -1;
+  __syncthreads();
+  return sh.ticket;
+}
+
+template <int ST, int V, bool SIGMOID, int W>
+__global__ __launch_bounds__(64 * W) void scan_tiles(ScanArgs a, ScanWork w) {
+  __shared__ TileShared<V, W> sh;
+  const uint32_t ticket = take_ticket(w, sh);
+  const int64_t tile = ticket / w.channel_blocks;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t c0 = static_cast<int64_t>(ticket % w.channel_blocks) * (64 * V) + lane * V;
+  const int nv = c0 >= a.dim ? 0 : c0 + V <= a.dim ? V : static_cast<int>(a.dim - c0);
+  const int64_t t0 = tile * (W * kSpan) + wave * kSpan;
+  const int tokens = static_cast<int>(a.tokens - t0 < 0 ? 0 : a.tokens - t0 < kSpan ? a.tokens - t0
+                                                                                     : kSpan);
+  StoredVec<ST, V> x[kSpan], g[kSpan];
+  load_span<ST, V>(a.x, a.x_stride, t0, tokens, c0, nv, x);
+  load_span<ST, V>(a.gate, a.gate_stride, t0, tokens, c0, nv, g);
+  list_sequences<V, W>(a, w, tile, sh);
+  __syncthreads();
+  const int32_t starts = lane < kSpan ? sh.lists[0][wave * kSpan + lane] : -1;
+  const int32_t ends = lane < kSpan ? sh.lists[1][wave * kSpan + lane] : -1;
+  const uint32_t first = static_cast<uint32_t>(__ballot(starts >= 0));
+  const uint32_t last = static_cast<uint32_t>(__ballot(ends >= 0));
+  float init[kSpan][V];
+  load_marked<V>(a.initial, a.initial_stride, first, starts, c0, nv, init);
+
+  // state_i = first ? u_i : k_i state_{i-1} + u_i, the state before a first token being in its u
+  float k[kSpan][V], u[kSpan][V], A[V], B[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSpan; ++i) {
+    const bool f = first >> i & 1u;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const Gates t = gates<SIGMOID>(static_cast<float>(g[i][v]));
+      const bool in = i < tokens;
+      k[i][v] = in ? t.a : 1.0f;
+      const float in_x = t.b * static_cast<float>(x[i][v]);
+      u[i][v] = f ? fmaf(t.a, init[i][v], in_x) : in ? in_x : 0.0f;
+      B[v] = f ? u[i][v] : fmaf(k[i][v], B[v], u[i][v]);
+      A[v] *= k[i][v];
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    sh.A[wave][lane * V + v] = A[v];
+    sh.B[wave][lane * V + v] = B[v];
+  }
+  if (lane == 0) sh.resets[wave] = first;
+  __syncthreads();
+  float state[V];
+  join_tiles<V, W, 1>(a, w, tile, c0, nv, sh, state);
+  wave_start<V, W, 1>(sh, wave, lane, state);
+  if (a.carry && tokens > 0) store_row<kF32, V>(a.carry, t0 / kSpan * a.dim + c0, nv, state);
+#pragma unroll
+  for (int i = 0; i < kSpan; ++i) {
+    const bool f = first >> i & 1u;
+#pragma unroll
+    for (int v = 0; v < V; ++v) state[v] = f ? u[i][v] : fmaf(k[i][v], state[v], u[i][v]);
+    if (i < tokens) store_row<ST, V>(a.h, (t0 + i) * a.dim + c0, nv, state);
+    if (last >> i & 1u) {
+      const int64_t s = __builtin_amdgcn_readlane(ends, i);
+      store_row<kF32, V>(a.final, s * a.dim + c0, nv, state);
+    }
+  }
+}
+
+template <int ST, int V, bool SIGMOID, int W>
+__global__ __launch_bounds__(64 * W) void scan_tiles_back(ScanArgs a, ScanWork w) {
+  __shared__ TileShared<V, W> sh;
+  const uint32_t ticket = take_ticket(w, sh);
+  const int64_t tile = w.tiles - 1 - ticket / w.channel_blocks;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t c0 = static_cast<int64_t>(ticket % w.channel_blocks) * (64 * V) + lane * V;
+  const int nv = c0 >= a.dim ? 0 : c0 + V <= a.dim ? V : static_cast<int>(a.dim - c0);
+  const int64_t t0 = tile * (W * kSpan) + wave * kSpan;
+  const int tokens = static_cast<int>(a.tokens - t0 < 0 ? 0 : a.tokens - t0 < kSpan ? a.tokens - t0
+                                                                                     : kSpan);
+  StoredVec<ST, V> x[kSpan], g[kSpan], dh[kSpan];
+  load_span<ST, V>(a.gate, a.gate_stride, t0, tokens, c0, nv, g);
+  load_span<ST, V>(a.x, a.x_stride, t0, tokens, c0, nv, x);
+  load_span<ST, V>(a.grad_h, a.grad_h_stride, t0, a.grad_h ? tokens : 0, c0, nv, dh);
+  float state[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    state[v] = tokens > 0 && v < nv ? a.carried[t0 / kSpan * a.dim + c0 + v] : 0.0f;
+  list_sequences<V, W>(a, w, tile, sh);
+  __syncthreads();
+  const int32_t starts = lane < kSpan ? sh.lists[0][wave * kSpan + lane] : -1;
+  const int32_t ends = lane < kSpan ? sh.lists[1][wave * kSpan + lane] : -1;
+  const uint32_t first = static_cast<uint32_t>(__ballot(starts >= 0));
+  const uint32_t last = static_cast<uint32_t>(__ballot(ends >= 0));
+  // before[i]: the state before token i; lam_i = up_i + (last ? 0 : mu_{i+1}), mu_i = a_i lam_i,
+  // the gradient of a final state being in its up
+  float before[kSpan][V], up[kSpan][V], A[V], B[V];
+  load_marked<V>(a.initial, a.initial_stride, first, starts, c0, nv, before);
+  load_marked<V>(a.grad_final, a.grad_final_stride, last, ends, c0, nv, up);
+#pragma unroll
+  for (int i = 0; i < kSpan; ++i) {
+    const bool f = first >> i & 1u;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const Gates t = gates<SIGMOID>(static_cast<float>(g[i][v]));
+      before[i][v] = f ? before[i][v] : state[v];
+      const float u = t.b * static_cast<float>(x[i][v]);
+      // as the forward pass rounds it
+      state[v] = f ? fmaf(t.a, before[i][v], u) : fmaf(t.a, state[v], u);
+      up[i][v] += static_cast<float>(dh[i][v]);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+#pragma unroll
+  for (int i = kSpan - 1; i >= 0; --i) {
+    const bool l = last >> i & 1u;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float k = i < tokens ? gates<SIGMOID>(static_cast<float>(g[i][v])).a : 1.0f;
+      B[v] = k * (l ? up[i][v] : up[i][v] + B[v]);
+      A[v] *= k;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    sh.A[wave][lane * V + v] = A[v];
+    sh.B[wave][lane * V + v] = B[v];
+  }
+  if (lane == 0) sh.resets[wave] = last;
+  __syncthreads();
+  float mu[V];
+  join_tiles<V, W, -1>(a, w, tile, c0, nv, sh, mu);
+  wave_start<V, W, -1>(sh, wave, lane, mu);
+#pragma unroll
+  for (int i = kSpan - 1; i >= 0; --i) {
+    const bool l = last >> i & 1u;
+    float dx[V], dg[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const Gates t = gates<SIGMOID>(static_cast<float>(g[i][v]));
+      const float lam = l ? up[i][v] : up[i][v] + mu[v];
+      dx[v] = t.b * lam;
+      dg[v] = SIGMOID ? lam * (before[i][v] - static_cast<float>(x[i][v])) * (t.a * t.b)
+                      : lam * before[i][v];
+      mu[v] = i < tokens ? t.a * lam : mu[v];
+    }
+    if (i < tokens) {
+      store_row<ST, V>(a.dx, (t0 + i) * a.dx_stride + c0, nv, dx);
+      store_row<ST, V>(a.dgate, (t0 + i) * a.dgate_stride + c0, nv, dg);
+    }
+    if (a.dinitial && (first >> i & 1u)) {
+      const int64_t s = __builtin_amdgcn_readlane(starts, i);
+      store_row<kF32, V>(a.dinitial, s * a.dim + c0, nv, mu);
+    }
+  }
+}
+
+// Waves in a tile.
+constexpr int kForwardWaves = 8, kBackWaves = 4;
+
+template <int ST, int V, bool SIGMOID>
+hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, bool back, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(w.tiles * w.channel_blocks));
   if (back)
-    hipLaunchKernelGGL((scan_walk_back<ST, SIGMOID, IT>), dim3(static_cast<unsigned>(blocks)),
-                       dim3(kBlock), 0, s, a);
+    hipLaunchKernelGGL((scan_tiles_back<ST, V, SIGMOID, kBackWaves>), grid, dim3(64 * kBackWaves), 0,
+                       s, a, w);
   else
-    hipLaunchKernelGGL((scan_walk<ST, SIGMOID, IT>), dim3(static_cast<unsigned>(blocks)),
-                       dim3(kBlock), 0, s, a);
+    hipLaunchKernelGGL((scan_tiles<ST, V, SIGMOID, kForwardWaves>), grid, dim3(64 * kForwardWaves),
+                       0, s, a, w);
   return hipGetLastError();
 }
 
-template <int ST>
-hipError_t launch_scan(const ScanArgs& a, int32_t kind, int32_t index, bool back, hipStream_t s) {
-  if (kind == TBE_GATE_SIGMOID)
-    return index == TBE_I64 ? launch_scan<ST, true, int64_t>(a, back, s)
-                            : launch_scan<ST, true, int32_t>(a, back, s);
-  return index == TBE_I64 ? launch_scan<ST, false, int64_t>(a, back, s)
-                          : launch_scan<ST, false, int32_t>(a, back, s);
+template <int ST, int V>
+hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, int32_t kind, bool back,
+                        hipStream_t s) {
+  return kind == TBE_GATE_SIGMOID ? launch_tiles<ST, V, true>(a, w, back, s)
+                                  : launch_tiles<ST, V, false>(a, w, back, s);
 }
 
-hipError_t launch_scan(const ScanArgs& a, const tbe_scan_input* in, bool back, hipStream_t s) {
-  return in->dtype == TBE_F32   ? launch_scan<kF32>(a, in->gate_kind, in->index_dtype, back, s)
-         : in->dtype == TBE_F16 ? launch_scan<kF16>(a, in->gate_kind, in->index_dtype, back, s)
-                                : launch_scan<kBF16>(a, in->gate_kind, in->index_dtype, back, s);
+// Channels a lane: a wave covers 64 or 128.
+int lane_channels(int32_t dtype, int64_t dim) { return dtype != TBE_F32 && dim > 64 ? 2 : 1; }
+
+int64_t tiles_of(int64_t tokens, bool back) {
+  const int64_t n = (back ? kBackWaves : kForwardWaves) * kSpan;
+  return (tokens + n - 1) / n;
 }
 
-constexpr int64_t kMaxElements = int64_t{1} << 38;
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Sizes a call can take: 31-bit tokens, sequences and channels.
+// The workspace: ticket, first offsets, pairs, states.
+size_t workspace_bytes_of(int64_t tokens, int64_t dim) {
+  const size_t tiles = static_cast<size_t>(tiles_of(tokens, kBackWaves < kForwardWaves));
+  return 256 + up256((tiles + 1) * 4) + up256(tiles * dim * 8) + up256(tiles * dim * 4);
+}
+
+hipError_t launch_scan(const ScanArgs& a, const tbe_scan_input* in, bool back, void* workspace,
+                       hipStream_t s) {
+  ScanWork w{};
+  w.tiles = tiles_of(a.tokens, back);
+  const int v = lane_channels(in->dtype, a.dim);
+  w.channel_blocks = static_cast<int32_t>((a.dim + 64 * v - 1) / (64 * v));
+  char* p = static_cast<char*>(workspace);
+  w.ticket = reinterpret_cast<uint32_t*>(p);
+  p += 256;
+  w.lo = reinterpret_cast<int32_t*>(p);
+  p += up256(static_cast<size_t>(w.tiles + 1) * 4);
+  w.pairs = reinterpret_cast<uint64_t*>(p);
+  p += up256(static_cast<size_t>(w.tiles) * a.dim * 8);
+  w.states = reinterpret_cast<uint32_t*>(p);
+  const int64_t work = std::max(w.tiles * a.dim, a.seqs);
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((work + kBlock - 1) / kBlock, 1024));
+  hipLaunchKernelGGL(scan_prepare, dim3(static_cast<unsigned>(blocks)), dim3(kBlock), 0, s, a, w,
+                     static_cast<int32_t>((back ? kBackWaves : kForwardWaves) * kSpan),
+                     back ? a.grad_final : a.initial,
+                     back ? a.grad_final_stride : a.initial_stride, back ? a.dinitial : a.final);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || w.tiles == 0) return e;
+  if (in->dtype == TBE_F32) return launch_tiles<kF32, 1>(a, w, in->gate_kind, back, s);
+  if (in->dtype == TBE_F16)
+    return v == 2 ? launch_tiles<kF16, 2>(a, w, in->gate_kind, back, s)
+                  : launch_tiles<kF16, 1>(a, w, in->gate_kind, back, s);
+  return v == 2 ? launch_tiles<kBF16, 2>(a, w, in->gate_kind, back, s)
+                : launch_tiles<kBF16, 1>(a, w, in->gate_kind, back, s);
+}
+
+// Sizes a call can take: 31-bit tokens, sequences and channels, 2^32 threads in a launch.
 tbe_status check_sizes(int64_t tokens, int64_t seqs, int64_t dim, int32_t dtype) {
+  constexpr int64_t kMax = 0x7FFFFFFF;
   if (tokens < 0 || seqs < 0 || dim < 1 || !known_dtype(dtype)) return TBE_ERR_INVALID_ARGUMENT;
   if (seqs == 0 && tokens > 0) return TBE_ERR_INVALID_ARGUMENT;
-  if (tokens >= 0x7FFFFFFF || seqs >= 0x7FFFFFFF || dim >= 0x7FFFFFFF) return TBE_ERR_UNSUPPORTED;
-  if (tokens > kMaxElements / dim || seqs > kMaxElements / dim) return TBE_ERR_UNSUPPORTED;
+  if (tokens >= kMax || seqs >= kMax || dim >= kMax) return TBE_ERR_UNSUPPORTED;
+  // 256 threads for 64 tokens of 64 channels, in tiles of up to 128 tokens
+  if ((tokens + 127) / 128 * 2 * ((dim + 63) / 64) >= (int64_t{1} << 24)) return TBE_ERR_UNSUPPORTED;
   return TBE_OK;
 }
 
 size_t carry_bytes_of(int64_t tokens, int64_t dim) {
-  return static_cast<size_t>(tokens) * static_cast<size_t>(dim) * sizeof(float);
+  return static_cast<size_t>((tokens + kSpan - 1) / kSpan) * static_cast<size_t>(dim) * sizeof(float);
 }
 
 tbe_status check_input(const tbe_scan_input* in) {
@@ -196,6 +653,11 @@ tbe_status check_input(const tbe_scan_input* in) {
   return TBE_OK;
 }
 
+tbe_status check_workspace(const tbe_scan_input* in, const void* workspace, size_t bytes) {
+  if (!workspace || !aligned_to(workspace, 256)) return TBE_ERR_INVALID_ARGUMENT;
+  return bytes < workspace_bytes_of(in->tokens, in->dim) ? TBE_ERR_WORKSPACE_TOO_SMALL : TBE_OK;
+}
+
 ScanArgs scan_args(const tbe_scan_input* in) {
   ScanArgs a{};
   a.tokens = in->tokens;
@@ -204,6 +666,7 @@ ScanArgs scan_args(const tbe_scan_input* in) {
   a.x = in->x;
   a.gate = in->gate;
   a.offsets = in->offsets;
+  a.index64 = in->index_dtype == TBE_I64;
   a.initial = in->initial;
   a.x_stride = in->x_stride;
   a.gate_stride = in->gate_stride;
@@ -251,15 +714,17 @@ tbe_status tbe_scan_sizes(int64_t tokens, int64_t seqs, int64_t dim, int32_t dty
   const tbe_status st = check_sizes(tokens, seqs, dim, dtype);
   if (st != TBE_OK) return st;
   *carry_bytes = carry_bytes_of(tokens, dim);
-  *workspace_bytes = 0;
+  *workspace_bytes = seqs > 0 ? workspace_bytes_of(tokens, dim) : 0;
   return TBE_OK;
 }
 
 tbe_status tbe_scan_forward(const tbe_scan_input* in, void* h, float* final, float* carry,
                             void* workspace, size_t workspace_bytes, void* stream) {
-  const tbe_status st = check_input(in);
+  tbe_status st = check_input(in);
   if (st != TBE_OK) return st;
   if (in->seqs == 0) return TBE_OK;
+  st = check_workspace(in, workspace, workspace_bytes);
+  if (st != TBE_OK) return st;
   if (!final || !aligned_to(final, 4) || !aligned_to(carry, 16) ||
       (in->tokens > 0 && (!h || !aligned_to(h, dtype_bytes(in->dtype)))))
     return TBE_ERR_INVALID_ARGUMENT;
@@ -267,8 +732,9 @@ tbe_status tbe_scan_forward(const tbe_scan_input* in, void* h, float* final, flo
   a.h = h;
   a.final = final;
   a.carry = carry;
-  return launch_scan(a, in, false, static_cast<hipStream_t>(stream)) == hipSuccess ? TBE_OK
-                                                                                   : TBE_ERR_HIP;
+  return launch_scan(a, in, false, workspace, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? TBE_OK
+             : TBE_ERR_HIP;
 }
 
 tbe_status tbe_scan_backward(const tbe_scan_input* in, const float* carry, const void* grad_h,
@@ -276,9 +742,11 @@ tbe_status tbe_scan_backward(const tbe_scan_input* in, const float* carry, const
                              int64_t grad_final_stride, void* dx, int64_t dx_stride, void* dgate,
                              int64_t dgate_stride, float* dinitial, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  const tbe_status st = check_input(in);
+  tbe_status st = check_input(in);
   if (st != TBE_OK) return st;
   if (in->seqs == 0) return TBE_OK;
+  st = check_workspace(in, workspace, workspace_bytes);
+  if (st != TBE_OK) return st;
   const size_t e = dtype_bytes(in->dtype);
   if (grad_h_stride < 0 || grad_final_stride < 0 || !aligned_to(grad_h, e) ||
       !aligned_to(grad_final, 4) || !aligned_to(dinitial, 4))
@@ -299,8 +767,9 @@ tbe_status tbe_scan_backward(const tbe_scan_input* in, const float* carry, const
   a.dgate = dgate;
   a.dgate_stride = dgate_stride;
   a.dinitial = dinitial;
-  return launch_scan(a, in, true, static_cast<hipStream_t>(stream)) == hipSuccess ? TBE_OK
-                                                                                  : TBE_ERR_HIP;
+  return launch_scan(a, in, true, workspace, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? TBE_OK
+             : TBE_ERR_HIP;
 }
 
 }  // extern "C"
