@@ -398,9 +398,9 @@ tbe_status tbe_scan_step(const void* x, int64_t x_stride, const void* gate, int6
 /* A batch of jagged sequences: sequence s holds the tokens offsets[s] ..
  * offsets[s+1] of x and gate ([tokens, dim]); offsets [seqs + 1] start at 0
  * and end at tokens.  initial: fp32 [seqs, dim], the state before each first
- * token (NULL: zeros; stride 0: one row for all).  tokens, seqs and dim are
- * below 2^31 - 1, tokens rounded up to 128 times dim rounded up to 64 below
- * 2^36. */
+ * token (NULL: zeros; stride 0: one row for all).  tokens and seqs are
+ * below 2^31 - 1, dim and the strides of rows at most 2^24, tokens and dim
+ * each rounded up to 64 have a product below 2^35. */
 typedef struct {
   int64_t tokens, seqs, dim;
   int32_t dtype, gate_kind, index_dtype;

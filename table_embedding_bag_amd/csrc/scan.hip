@@ -23,12 +23,25 @@ struct Gates {
 };
 
 // sigmoid(g) and sigmoid(-g) from one exponential of -|g|: neither overflows
-// nor loses the smaller one to cancellation.
+// nor loses the smaller one to cancellation.  exp(-|g|) = 2^t (1 + r ln 2) with
+// t + r = -|g| log2 e, r what the product's rounding left out; the reciprocal
+// gets one Newton step.  Both are good to some 2^-23 relative; expf and two
+// divisions cost three times as much and made the backward pass wait for them.
 template <bool SIGMOID>
 __device__ __forceinline__ Gates gates(float g) {
   if constexpr (!SIGMOID) return {g, 1.0f};
-  const float z = expf(-fabsf(g));
-  const float hi = 1.0f / (1.0f + z), lo = z / (1.0f + z);
+  constexpr double kLog2e = 1.4426950408889634074;
+  constexpr float kHigh = static_cast<float>(kLog2e);
+  constexpr float kLow = static_cast<float>(kLog2e - static_cast<double>(kHigh));
+  const float m = fabsf(g) > 128.0f ? -128.0f : -fabsf(g);  // infinities stay out of r, NaN passes
+  const float t = m * kHigh;
+  const float r = fmaf(m, kLow, fmaf(m, kHigh, -t));
+  const float p = __builtin_amdgcn_exp2f(t);
+  const float z = fmaf(p, r * 0.69314718f, p);
+  const float d = 1.0f + z;
+  float hi = __builtin_amdgcn_rcpf(d);
+  hi = fmaf(fmaf(-d, hi, 1.0f), hi, hi);
+  const float lo = z * hi;
   return g >= 0.0f ? Gates{hi, lo} : Gates{lo, hi};
 }
 
@@ -102,8 +115,8 @@ __device__ __forceinline__ int64_t offset_at(const ScanArgs& a, int64_t s) {
   return o < 0 ? 0 : (o > a.tokens ? a.tokens : o);
 }
 
-// The token axis is cut into tiles whatever the sequences: W waves of kSpan
-// tokens each, and 64 V channels, V neighbours a lane.  Within its span a wave
+// The token axis is cut into tiles whatever the sequences: W waves of T tokens
+// each (a span), and 64 V channels, V neighbours a lane.  Within its span a wave
 // reduces the recurrence to "state out = A state in + B" per channel, the waves'
 // pairs join in LDS, and the tiles' in the workspace: a tile publishes its own
 // (A, B), or, where a sequence starts inside, the state it ends with, which
@@ -118,7 +131,7 @@ __device__ __forceinline__ int64_t offset_at(const ScanArgs& a, int64_t s) {
 // atomics; a value is there once it differs from all ones (a NaN that canonical()
 // never lets through).  Tiles are numbered by a ticket taken at a workgroup's
 // start, so every tile waited for is running or done.
-constexpr int kSpan = 16;                  // tokens a wave; also of a carry row
+constexpr int kCarry = 8;                  // tokens between the states that are carried
 constexpr uint64_t kNoPair = ~uint64_t{0};
 constexpr uint32_t kNoState = ~uint32_t{0};
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls before a wait gives up (states turn NaN)
@@ -188,11 +201,11 @@ __global__ __launch_bounds__(kBlock) void scan_prepare(ScanArgs a, ScanWork w, i
 }
 
 // What the waves of a tile share.
-template <int V, int W>
+template <int V, int W, int T>
 struct TileShared {
   static constexpr int kWindow = 2 * W;  // tiles looked back on at a time
   uint32_t ticket;
-  int32_t lists[2][W * kSpan];           // sequence that starts at / ends with a token, or -1
+  int32_t lists[2][W * T];               // sequence that starts at / ends with a token, or -1
   uint32_t resets[W];                    // the wave's span holds a reset
   float A[W][64 * V], B[W][64 * V];
   float pair_a[kWindow][64 * V], pair_b[kWindow][64 * V];
@@ -200,10 +213,10 @@ struct TileShared {
 };
 
 // Which sequences start in and end with the tile's tokens.
-template <int V, int W>
+template <int V, int W, int T>
 __device__ __forceinline__ void list_sequences(const ScanArgs& a, const ScanWork& w, int64_t tile,
-                                               TileShared<V, W>& sh) {
-  constexpr int kTokens = W * kSpan;
+                                               TileShared<V, W, T>& sh) {
+  constexpr int kTokens = W * T;
   const int64_t t0 = tile * kTokens;
   const int64_t lo = w.lo[tile], hi = w.lo[tile + 1];
   for (int64_t i = lo + threadIdx.x; i <= hi && i <= a.seqs; i += 64 * W) {
@@ -219,9 +232,9 @@ __device__ __forceinline__ void list_sequences(const ScanArgs& a, const ScanWork
 // A tile's start state per channel (the state after its predecessor in scan
 // order), the tile's own pair, and the end state published.  STEP: +1 where
 // tile k follows tile k - 1, -1 where it follows tile k + 1.
-template <int V, int W, int STEP>
+template <int V, int W, int T, int STEP>
 __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w, int64_t tile,
-                                           int64_t c0, int nv, TileShared<V, W>& sh,
+                                           int64_t c0, bool mine, TileShared<V, W, T>& sh,
                                            float (&start)[V]) {
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   // the tile's pair: wave by wave in scan order
@@ -242,20 +255,20 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
     }
   }
   const bool first = STEP > 0 ? tile == 0 : tile == w.tiles - 1;
-  const int64_t mine = tile * a.dim + c0;
+  const int64_t here = tile * a.dim + c0;
   if (wave == 0) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (v < nv) {
-        if (reset || first) st_state(w.states + mine + v, B[v]);
-        else st_pair(w.pairs + mine + v, A[v], B[v]);
+      if (mine) {
+        if (reset || first) st_state(w.states + here + v, B[v]);
+        else st_pair(w.pairs + here + v, A[v], B[v]);
       }
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) start[v] = 0.0f;
   // no state comes in where the tile's first token (in scan order) starts afresh
-  if (first || sh.lists[STEP > 0 ? 0 : 1][STEP > 0 ? 0 : W * kSpan - 1] >= 0) return;
-  constexpr int kWindow = TileShared<V, W>::kWindow;
+  if (first || sh.lists[STEP > 0 ? 0 : 1][STEP > 0 ? 0 : W * T - 1] >= 0) return;
+  constexpr int kWindow = TileShared<V, W, T>::kWindow;
   uint32_t spins = 0;
   for (int round = 0;; ++round) {
     // The first look is at the nearest tile alone (with short sequences it knows
@@ -274,7 +287,7 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
         for (int v = 0; v < V; ++v) {
           pair[v] = 0;
           state[v] = 0;
-          if (real && v < nv) {
+          if (real && mine) {
             state[v] = ld_state(w.states + k * a.dim + c0 + v);
             pair[v] = ld_pair(w.pairs + k * a.dim + c0 + v);
             there = there && (state[v] != kNoState || pair[v] != kNoPair);
@@ -318,13 +331,13 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
   if (wave == 0 && !reset) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (v < nv) st_state(w.states + mine + v, fmaf(A[v], start[v], B[v]));
+      if (mine) st_state(w.states + here + v, fmaf(A[v], start[v], B[v]));
   }
 }
 
 // The state a wave starts from: the tile's, taken through the waves before it.
-template <int V, int W, int STEP>
-__device__ __forceinline__ void wave_start(const TileShared<V, W>& sh, int wave, int lane,
+template <int V, int W, int T, int STEP>
+__device__ __forceinline__ void wave_start(const TileShared<V, W, T>& sh, int wave, int lane,
                                            float (&state)[V]) {
 #pragma unroll
   for (int q = 0; q < W; ++q) {
@@ -340,93 +353,137 @@ __device__ __forceinline__ void wave_start(const TileShared<V, W>& sh, int wave,
   }
 }
 
-// V channels of a row for each token of a span: those that exist (tokens below
-// `tokens`, nv channels), the others 0.
-template <int ST, int V>
-__device__ __forceinline__ void load_span(const void* base, int64_t stride, int64_t t0, int tokens,
-                                          int64_t c0, int nv, StoredVec<ST, V> (&out)[kSpan]) {
-#pragma unroll
-  for (int i = 0; i < kSpan; ++i) {
-    out[i] = StoredVec<ST, V>{};
-    if (i < tokens) {
-      const int64_t at = (t0 + i) * stride + c0;
-      if (nv == V) out[i] = load_vec<ST, V>(base, at);
-      else if (nv > 0) out[i][0] = static_cast<const typename Stored<ST>::type*>(base)[at];
-    }
+// A buffer descriptor: loads past `bytes` give 0, stores there are dropped.  The
+// spans' loads and stores go through these, so that no branch parts them and all
+// of a wave's loads are in flight together.
+__device__ __forceinline__ auto buffer(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0,
+                                           static_cast<int>(bytes > 0 ? bytes : 0), 0x00020000);
+}
+using Buffer = decltype(buffer(nullptr, 0));
+constexpr uint32_t kOutside = 0x80000000u;  // past every descriptor's end
+
+// One lane's V channels: 2, 4 or 8 bytes.
+template <int BYTES>
+struct Word;
+template <>
+struct Word<2> {
+  using type = uint16_t;
+  static __device__ __forceinline__ type load(Buffer b, uint32_t o) {
+    return __builtin_amdgcn_raw_buffer_load_b16(b, o, 0, 0);
   }
+  static __device__ __forceinline__ void store(type v, Buffer b, uint32_t o) {
+    __builtin_amdgcn_raw_buffer_store_b16(v, b, o, 0, 0);
+  }
+};
+template <>
+struct Word<4> {
+  using type = uint32_t;
+  static __device__ __forceinline__ type load(Buffer b, uint32_t o) {
+    return __builtin_amdgcn_raw_buffer_load_b32(b, o, 0, 0);
+  }
+  static __device__ __forceinline__ void store(type v, Buffer b, uint32_t o) {
+    __builtin_amdgcn_raw_buffer_store_b32(v, b, o, 0, 0);
+  }
+};
+template <>
+struct Word<8> {
+  using type = uint32_t __attribute__((ext_vector_type(2)));
+  static __device__ __forceinline__ type load(Buffer b, uint32_t o) {
+    return __builtin_amdgcn_raw_buffer_load_b64(b, o, 0, 0);
+  }
+  static __device__ __forceinline__ void store(type v, Buffer b, uint32_t o) {
+    __builtin_amdgcn_raw_buffer_store_b64(v, b, o, 0, 0);
+  }
+};
+template <int ST, int V>
+using RowWord = Word<StorageTraits<ST>::bytes * V>;
+
+// The span's rows from column `c` (the workgroup's first) of `base`; a lane's V
+// channels are at byte `lane_off` (kOutside: none).
+template <int ST>
+__device__ __forceinline__ Buffer span_buffer(const void* base, int64_t stride, int64_t t0,
+                                              int tokens, int64_t c, int64_t dim) {
+  constexpr int b = StorageTraits<ST>::bytes;
+  return buffer(static_cast<const char*>(base) + (t0 * stride + c) * b,
+                tokens > 0 && base ? ((tokens - 1) * stride + dim - c) * b : 0);
+}
+template <int ST, int V, int T>
+__device__ __forceinline__ void load_span(Buffer rows, int64_t stride, uint32_t lane_off,
+                                          StoredVec<ST, V> (&out)[T]) {
+  const uint32_t step = static_cast<uint32_t>(stride) * StorageTraits<ST>::bytes;
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+    out[i] = __builtin_bit_cast(StoredVec<ST, V>, RowWord<ST, V>::load(rows, lane_off + i * step));
 }
 // The rows of `base` of the sequences whose bits are set in mask (list: lane i
 // holds the sequence of token i), 0 for the others.
-template <int V>
+template <int V, int T>
 __device__ __forceinline__ void load_marked(const float* base, int64_t stride, uint32_t mask,
-                                            int32_t list, int64_t c0, int nv,
-                                            float (&out)[kSpan][V]) {
+                                            int32_t list, int64_t c, int64_t dim, uint32_t lane_off,
+                                            float (&out)[T][V]) {
 #pragma unroll
-  for (int i = 0; i < kSpan; ++i) {
+  for (int i = 0; i < T; ++i)
 #pragma unroll
     for (int v = 0; v < V; ++v) out[i][v] = 0.0f;
-    if (base && (mask >> i & 1u)) {
-      const int64_t at = static_cast<int64_t>(__builtin_amdgcn_readlane(list, i)) * stride + c0;
-      if (nv == V) {
-        const auto r = load_vec<kF32, V>(base, at);
+  if (!base || !mask) return;
 #pragma unroll
-        for (int v = 0; v < V; ++v) out[i][v] = r[v];
-      } else if (nv > 0) {
-        out[i][0] = base[at];
-      }
-    }
+  for (int i = 0; i < T; ++i) {
+    const int64_t s = __builtin_amdgcn_readlane(list, i);
+    const Buffer row = buffer(base + (s < 0 ? 0 : s * stride) + c, s < 0 ? 0 : (dim - c) * 4);
+    const auto r = __builtin_bit_cast(StoredVec<kF32, V>, RowWord<kF32, V>::load(row, lane_off));
+#pragma unroll
+    for (int v = 0; v < V; ++v) out[i][v] = r[v];
   }
 }
 template <int ST, int V>
-__device__ __forceinline__ void store_row(void* base, int64_t at, int nv, const float (&f)[V]) {
-  if (nv == V) {
-    StoredVec<ST, V> o;
+__device__ __forceinline__ void store_row(Buffer rows, uint32_t off, const float (&f)[V]) {
+  StoredVec<ST, V> o;
 #pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = static_cast<typename Stored<ST>::type>(f[v]);
-    store_vec<ST, V>(base, at, o);
-  } else if (nv > 0) {
-    store_one<ST>(base, at, f[0]);
-  }
+  for (int v = 0; v < V; ++v) o[v] = static_cast<typename Stored<ST>::type>(f[v]);
+  RowWord<ST, V>::store(__builtin_bit_cast(typename RowWord<ST, V>::type, o), rows, off);
 }
 
 // Tile and channels of a workgroup, in the order of the tickets, and the lists cleared.
-template <int V, int W>
-__device__ __forceinline__ uint32_t take_ticket(const ScanWork& w, TileShared<V, W>& sh) {
+template <int V, int W, int T>
+__device__ __forceinline__ uint32_t take_ticket(const ScanWork& w, TileShared<V, W, T>& sh) {
   if (threadIdx.x == 0) sh.ticket = atomicAdd(w.ticket, 1u);
-  for (int i = threadIdx.x; i < 2 * W * kSpan; i += 64 * W) (&sh.lists[0][0])[i] = -1;
+  for (int i = threadIdx.x; i < 2 * W * T; i += 64 * W) (&sh.lists[0][0])[i] = -1;
   __syncthreads();
   return sh.ticket;
 }
 
-template <int ST, int V, bool SIGMOID, int W>
-__global__ __launch_bounds__(64 * W) void scan_tiles(ScanArgs a, ScanWork w) {
-  __shared__ TileShared<V, W> sh;
+template <int ST, int V, bool SIGMOID, int W, int T>
+__global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) {
+  __shared__ TileShared<V, W, T> sh;
   const uint32_t ticket = take_ticket(w, sh);
   const int64_t tile = ticket / w.channel_blocks;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c0 = static_cast<int64_t>(ticket % w.channel_blocks) * (64 * V) + lane * V;
-  const int nv = c0 >= a.dim ? 0 : c0 + V <= a.dim ? V : static_cast<int>(a.dim - c0);
-  const int64_t t0 = tile * (W * kSpan) + wave * kSpan;
-  const int tokens = static_cast<int>(a.tokens - t0 < 0 ? 0 : a.tokens - t0 < kSpan ? a.tokens - t0
-                                                                                     : kSpan);
-  StoredVec<ST, V> x[kSpan], g[kSpan];
-  load_span<ST, V>(a.x, a.x_stride, t0, tokens, c0, nv, x);
-  load_span<ST, V>(a.gate, a.gate_stride, t0, tokens, c0, nv, g);
-  list_sequences<V, W>(a, w, tile, sh);
+  const int64_t c = static_cast<int64_t>(ticket % w.channel_blocks) * (64 * V), c0 = c + lane * V;
+  const bool mine = c0 < a.dim;  // V divides dim
+  constexpr int bytes = StorageTraits<ST>::bytes;
+  const uint32_t at = mine ? lane * V * bytes : kOutside, at32 = mine ? lane * V * 4 : kOutside;
+  const int64_t t0 = tile * (W * T) + wave * T;
+  const int tokens = static_cast<int>(a.tokens - t0 < 0 ? 0 : a.tokens - t0 < T ? a.tokens - t0
+                                                                                     : T);
+  StoredVec<ST, V> x[T], g[T];
+  load_span<ST, V, T>(span_buffer<ST>(a.gate, a.gate_stride, t0, tokens, c, a.dim), a.gate_stride, at, g);
+  load_span<ST, V, T>(span_buffer<ST>(a.x, a.x_stride, t0, tokens, c, a.dim), a.x_stride, at, x);
+  list_sequences<V, W, T>(a, w, tile, sh);
   __syncthreads();
-  const int32_t starts = lane < kSpan ? sh.lists[0][wave * kSpan + lane] : -1;
-  const int32_t ends = lane < kSpan ? sh.lists[1][wave * kSpan + lane] : -1;
+  const int32_t starts = lane < T ? sh.lists[0][wave * T + lane] : -1;
+  const int32_t ends = lane < T ? sh.lists[1][wave * T + lane] : -1;
   const uint32_t first = static_cast<uint32_t>(__ballot(starts >= 0));
   const uint32_t last = static_cast<uint32_t>(__ballot(ends >= 0));
-  float init[kSpan][V];
-  load_marked<V>(a.initial, a.initial_stride, first, starts, c0, nv, init);
+  float init[T][V];
+  load_marked<V, T>(a.initial, a.initial_stride, first, starts, c, a.dim, at32, init);
 
   // state_i = first ? u_i : k_i state_{i-1} + u_i, the state before a first token being in its u
-  float k[kSpan][V], u[kSpan][V], A[V], B[V];
+  float k[T][V], u[T][V], A[V], B[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kSpan; ++i) {
+  for (int i = 0; i < T; ++i) {
     const bool f = first >> i & 1u;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -447,54 +504,67 @@ __global__ __launch_bounds__(64 * W) void scan_tiles(ScanArgs a, ScanWork w) {
   if (lane == 0) sh.resets[wave] = first;
   __syncthreads();
   float state[V];
-  join_tiles<V, W, 1>(a, w, tile, c0, nv, sh, state);
-  wave_start<V, W, 1>(sh, wave, lane, state);
-  if (a.carry && tokens > 0) store_row<kF32, V>(a.carry, t0 / kSpan * a.dim + c0, nv, state);
+  join_tiles<V, W, T, 1>(a, w, tile, c0, mine, sh, state);
+  wave_start<V, W, T, 1>(sh, wave, lane, state);
+  const Buffer carry = span_buffer<kF32>(a.carry, a.dim, t0 / kCarry, (tokens + kCarry - 1) / kCarry, c,
+                                         a.dim);
+  const Buffer h = span_buffer<ST>(a.h, a.dim, t0, tokens, c, a.dim);
+  const uint32_t step = static_cast<uint32_t>(a.dim) * bytes;
 #pragma unroll
-  for (int i = 0; i < kSpan; ++i) {
+  for (int i = 0; i < T; ++i) {
     const bool f = first >> i & 1u;
+    if (i % kCarry == 0 && a.carry)
+      store_row<kF32, V>(carry, at32 + i / kCarry * static_cast<uint32_t>(a.dim) * 4, state);
 #pragma unroll
     for (int v = 0; v < V; ++v) state[v] = f ? u[i][v] : fmaf(k[i][v], state[v], u[i][v]);
-    if (i < tokens) store_row<ST, V>(a.h, (t0 + i) * a.dim + c0, nv, state);
+    store_row<ST, V>(h, at + i * step, state);
     if (last >> i & 1u) {
       const int64_t s = __builtin_amdgcn_readlane(ends, i);
-      store_row<kF32, V>(a.final, s * a.dim + c0, nv, state);
+      store_row<kF32, V>(span_buffer<kF32>(a.final, a.dim, s, 1, c, a.dim), at32, state);
     }
   }
 }
 
-template <int ST, int V, bool SIGMOID, int W>
-__global__ __launch_bounds__(64 * W) void scan_tiles_back(ScanArgs a, ScanWork w) {
-  __shared__ TileShared<V, W> sh;
+template <int ST, int V, bool SIGMOID, int W, int T>
+__global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWork w) {
+  __shared__ TileShared<V, W, T> sh;
   const uint32_t ticket = take_ticket(w, sh);
   const int64_t tile = w.tiles - 1 - ticket / w.channel_blocks;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c0 = static_cast<int64_t>(ticket % w.channel_blocks) * (64 * V) + lane * V;
-  const int nv = c0 >= a.dim ? 0 : c0 + V <= a.dim ? V : static_cast<int>(a.dim - c0);
-  const int64_t t0 = tile * (W * kSpan) + wave * kSpan;
-  const int tokens = static_cast<int>(a.tokens - t0 < 0 ? 0 : a.tokens - t0 < kSpan ? a.tokens - t0
-                                                                                     : kSpan);
-  StoredVec<ST, V> x[kSpan], g[kSpan], dh[kSpan];
-  load_span<ST, V>(a.gate, a.gate_stride, t0, tokens, c0, nv, g);
-  load_span<ST, V>(a.x, a.x_stride, t0, tokens, c0, nv, x);
-  load_span<ST, V>(a.grad_h, a.grad_h_stride, t0, a.grad_h ? tokens : 0, c0, nv, dh);
+  const int64_t c = static_cast<int64_t>(ticket % w.channel_blocks) * (64 * V), c0 = c + lane * V;
+  const bool mine = c0 < a.dim;  // V divides dim
+  constexpr int bytes = StorageTraits<ST>::bytes;
+  const uint32_t at = mine ? lane * V * bytes : kOutside, at32 = mine ? lane * V * 4 : kOutside;
+  const int64_t t0 = tile * (W * T) + wave * T;
+  const int tokens = static_cast<int>(a.tokens - t0 < 0 ? 0 : a.tokens - t0 < T ? a.tokens - t0
+                                                                                     : T);
+  StoredVec<ST, V> x[T], g[T], dh[T];
+  load_span<ST, V, T>(span_buffer<ST>(a.gate, a.gate_stride, t0, tokens, c, a.dim), a.gate_stride, at, g);
+  load_span<ST, V, T>(span_buffer<ST>(a.x, a.x_stride, t0, tokens, c, a.dim), a.x_stride, at, x);
+  load_span<ST, V, T>(span_buffer<ST>(a.grad_h, a.grad_h_stride, t0, tokens, c, a.dim), a.grad_h_stride,
+                   at, dh);
   float state[V];
+  {
+    const auto r = __builtin_bit_cast(
+        StoredVec<kF32, V>,
+        RowWord<kF32, V>::load(span_buffer<kF32>(a.carried, a.dim, t0 / kCarry, tokens > 0, c, a.dim),
+                               at32));
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    state[v] = tokens > 0 && v < nv ? a.carried[t0 / kSpan * a.dim + c0 + v] : 0.0f;
-  list_sequences<V, W>(a, w, tile, sh);
+    for (int v = 0; v < V; ++v) state[v] = r[v];
+  }
+  list_sequences<V, W, T>(a, w, tile, sh);
   __syncthreads();
-  const int32_t starts = lane < kSpan ? sh.lists[0][wave * kSpan + lane] : -1;
-  const int32_t ends = lane < kSpan ? sh.lists[1][wave * kSpan + lane] : -1;
+  const int32_t starts = lane < T ? sh.lists[0][wave * T + lane] : -1;
+  const int32_t ends = lane < T ? sh.lists[1][wave * T + lane] : -1;
   const uint32_t first = static_cast<uint32_t>(__ballot(starts >= 0));
   const uint32_t last = static_cast<uint32_t>(__ballot(ends >= 0));
   // before[i]: the state before token i; lam_i = up_i + (last ? 0 : mu_{i+1}), mu_i = a_i lam_i,
   // the gradient of a final state being in its up
-  float before[kSpan][V], up[kSpan][V], A[V], B[V];
-  load_marked<V>(a.initial, a.initial_stride, first, starts, c0, nv, before);
-  load_marked<V>(a.grad_final, a.grad_final_stride, last, ends, c0, nv, up);
+  float before[T][V], up[T][V], A[V], B[V];
+  load_marked<V, T>(a.initial, a.initial_stride, first, starts, c, a.dim, at32, before);
+  load_marked<V, T>(a.grad_final, a.grad_final_stride, last, ends, c, a.dim, at32, up);
 #pragma unroll
-  for (int i = 0; i < kSpan; ++i) {
+  for (int i = 0; i < T; ++i) {
     const bool f = first >> i & 1u;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -509,7 +579,7 @@ __global__ __launch_bounds__(64 * W) void scan_tiles_back(ScanArgs a, ScanWork w
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
 #pragma unroll
-  for (int i = kSpan - 1; i >= 0; --i) {
+  for (int i = T - 1; i >= 0; --i) {
     const bool l = last >> i & 1u;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -526,10 +596,14 @@ __global__ __launch_bounds__(64 * W) void scan_tiles_back(ScanArgs a, ScanWork w
   if (lane == 0) sh.resets[wave] = last;
   __syncthreads();
   float mu[V];
-  join_tiles<V, W, -1>(a, w, tile, c0, nv, sh, mu);
-  wave_start<V, W, -1>(sh, wave, lane, mu);
+  join_tiles<V, W, T, -1>(a, w, tile, c0, mine, sh, mu);
+  wave_start<V, W, T, -1>(sh, wave, lane, mu);
+  const Buffer dxs = span_buffer<ST>(a.dx, a.dx_stride, t0, tokens, c, a.dim);
+  const Buffer dgs = span_buffer<ST>(a.dgate, a.dgate_stride, t0, tokens, c, a.dim);
+  const uint32_t dx_step = static_cast<uint32_t>(a.dx_stride) * bytes;
+  const uint32_t dg_step = static_cast<uint32_t>(a.dgate_stride) * bytes;
 #pragma unroll
-  for (int i = kSpan - 1; i >= 0; --i) {
+  for (int i = T - 1; i >= 0; --i) {
     const bool l = last >> i & 1u;
     float dx[V], dg[V];
 #pragma unroll
@@ -541,29 +615,30 @@ __global__ __launch_bounds__(64 * W) void scan_tiles_back(ScanArgs a, ScanWork w
                       : lam * before[i][v];
       mu[v] = i < tokens ? t.a * lam : mu[v];
     }
-    if (i < tokens) {
-      store_row<ST, V>(a.dx, (t0 + i) * a.dx_stride + c0, nv, dx);
-      store_row<ST, V>(a.dgate, (t0 + i) * a.dgate_stride + c0, nv, dg);
-    }
+    store_row<ST, V>(dxs, at + i * dx_step, dx);
+    store_row<ST, V>(dgs, at + i * dg_step, dg);
     if (a.dinitial && (first >> i & 1u)) {
       const int64_t s = __builtin_amdgcn_readlane(starts, i);
-      store_row<kF32, V>(a.dinitial, s * a.dim + c0, nv, mu);
+      store_row<kF32, V>(span_buffer<kF32>(a.dinitial, a.dim, s, 1, c, a.dim), at32, mu);
     }
   }
 }
 
-// Waves in a tile.
-constexpr int kForwardWaves = 8, kBackWaves = 4;
+// Waves in a tile and tokens in a wave's span.  The backward pass holds twice as
+// much for each token: its spans are as short as the carry's rows.
+constexpr int kForwardWaves = 8, kForwardSpan = 16;
+constexpr int kBackWaves = 8, kBacT = kCarry;
+constexpr int kForwardTokens = kForwardWaves * kForwardSpan, kBackTokens = kBackWaves * kBacT;
 
 template <int ST, int V, bool SIGMOID>
 hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, bool back, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(w.tiles * w.channel_blocks));
   if (back)
-    hipLaunchKernelGGL((scan_tiles_back<ST, V, SIGMOID, kBackWaves>), grid, dim3(64 * kBackWaves), 0,
-                       s, a, w);
+    hipLaunchKernelGGL((scan_tiles_back<ST, V, SIGMOID, kBackWaves, kBacT>), grid,
+                       dim3(64 * kBackWaves), 0, s, a, w);
   else
-    hipLaunchKernelGGL((scan_tiles<ST, V, SIGMOID, kForwardWaves>), grid, dim3(64 * kForwardWaves),
-                       0, s, a, w);
+    hipLaunchKernelGGL((scan_tiles<ST, V, SIGMOID, kForwardWaves, kForwardSpan>), grid,
+                       dim3(64 * kForwardWaves), 0, s, a, w);
   return hipGetLastError();
 }
 
@@ -574,11 +649,20 @@ hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, int32_t kind, bool
                                   : launch_tiles<ST, V, false>(a, w, back, s);
 }
 
-// Channels a lane: a wave covers 64 or 128.
-int lane_channels(int32_t dtype, int64_t dim) { return dtype != TBE_F32 && dim > 64 ? 2 : 1; }
+// Channels a lane: two neighbours of 16-bit rows, where every row starts at an
+// even element and a wave's 128 channels are not mostly past the end.
+int lane_channels(const tbe_scan_input* in, const ScanArgs& a) {
+  if (in->dtype == TBE_F32 || a.dim <= 64 || a.dim % 2) return 1;
+  const auto even = [](const void* p, int64_t stride) { return aligned_to(p, 4) && stride % 2 == 0; };
+  return even(a.x, a.x_stride) && even(a.gate, a.gate_stride) && even(a.h, 0) &&
+                 even(a.grad_h, a.grad_h_stride) && even(a.dx, a.dx_stride) &&
+                 even(a.dgate, a.dgate_stride)
+             ? 2
+             : 1;
+}
 
 int64_t tiles_of(int64_t tokens, bool back) {
-  const int64_t n = (back ? kBackWaves : kForwardWaves) * kSpan;
+  const int64_t n = back ? kBackTokens : kForwardTokens;
   return (tokens + n - 1) / n;
 }
 
@@ -586,15 +670,17 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // The workspace: ticket, first offsets, pairs, states.
 size_t workspace_bytes_of(int64_t tokens, int64_t dim) {
-  const size_t tiles = static_cast<size_t>(tiles_of(tokens, kBackWaves < kForwardWaves));
+  const size_t tiles = static_cast<size_t>(tiles_of(tokens, kBackTokens < kForwardTokens));
   return 256 + up256((tiles + 1) * 4) + up256(tiles * dim * 8) + up256(tiles * dim * 4);
 }
 
-hipError_t launch_scan(const ScanArgs& a, const tbe_scan_input* in, bool back, void* workspace,
+hipError_t launch_scan(ScanArgs a, const tbe_scan_input* in, bool back, void* workspace,
                        hipStream_t s) {
+  if (a.tokens <= 1)  // a single row's stride says nothing
+    a.x_stride = a.gate_stride = a.grad_h_stride = a.dx_stride = a.dgate_stride = a.dim;
   ScanWork w{};
   w.tiles = tiles_of(a.tokens, back);
-  const int v = lane_channels(in->dtype, a.dim);
+  const int v = lane_channels(in, a);
   w.channel_blocks = static_cast<int32_t>((a.dim + 64 * v - 1) / (64 * v));
   char* p = static_cast<char*>(workspace);
   w.ticket = reinterpret_cast<uint32_t*>(p);
@@ -607,7 +693,7 @@ hipError_t launch_scan(const ScanArgs& a, const tbe_scan_input* in, bool back, v
   const int64_t work = std::max(w.tiles * a.dim, a.seqs);
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((work + kBlock - 1) / kBlock, 1024));
   hipLaunchKernelGGL(scan_prepare, dim3(static_cast<unsigned>(blocks)), dim3(kBlock), 0, s, a, w,
-                     static_cast<int32_t>((back ? kBackWaves : kForwardWaves) * kSpan),
+                     back ? kBackTokens : kForwardTokens,
                      back ? a.grad_final : a.initial,
                      back ? a.grad_final_stride : a.initial_stride, back ? a.dinitial : a.final);
   hipError_t e = hipGetLastError();
@@ -620,19 +706,22 @@ hipError_t launch_scan(const ScanArgs& a, const tbe_scan_input* in, bool back, v
                 : launch_tiles<kBF16, 1>(a, w, in->gate_kind, back, s);
 }
 
-// Sizes a call can take: 31-bit tokens, sequences and channels, 2^32 threads in a launch.
+// A span's rows lie within a buffer descriptor's reach.
+constexpr int64_t kMaxRow = int64_t{1} << 24;
+
+// Sizes a call can take: 31-bit tokens and sequences, 2^32 threads in a launch.
 tbe_status check_sizes(int64_t tokens, int64_t seqs, int64_t dim, int32_t dtype) {
   constexpr int64_t kMax = 0x7FFFFFFF;
   if (tokens < 0 || seqs < 0 || dim < 1 || !known_dtype(dtype)) return TBE_ERR_INVALID_ARGUMENT;
   if (seqs == 0 && tokens > 0) return TBE_ERR_INVALID_ARGUMENT;
-  if (tokens >= kMax || seqs >= kMax || dim >= kMax) return TBE_ERR_UNSUPPORTED;
-  // 256 threads for 64 tokens of 64 channels, in tiles of up to 128 tokens
-  if ((tokens + 127) / 128 * 2 * ((dim + 63) / 64) >= (int64_t{1} << 24)) return TBE_ERR_UNSUPPORTED;
+  if (tokens >= kMax || seqs >= kMax || dim > kMaxRow) return TBE_ERR_UNSUPPORTED;
+  // 512 threads for 64 tokens of 64 channels
+  if ((tokens + 63) / 64 * ((dim + 63) / 64) >= (int64_t{1} << 23)) return TBE_ERR_UNSUPPORTED;
   return TBE_OK;
 }
 
 size_t carry_bytes_of(int64_t tokens, int64_t dim) {
-  return static_cast<size_t>((tokens + kSpan - 1) / kSpan) * static_cast<size_t>(dim) * sizeof(float);
+  return static_cast<size_t>((tokens + kCarry - 1) / kCarry) * static_cast<size_t>(dim) * sizeof(float);
 }
 
 tbe_status check_input(const tbe_scan_input* in) {
@@ -647,6 +736,8 @@ tbe_status check_input(const tbe_scan_input* in) {
   if (!aligned_to(in->offsets, in->index_dtype == TBE_I64 ? 8 : 4)) return TBE_ERR_INVALID_ARGUMENT;
   if (in->tokens > 0 && (!in->x || !in->gate || !aligned_to(in->x, e) || !aligned_to(in->gate, e)))
     return TBE_ERR_INVALID_ARGUMENT;
+  if (in->tokens > 1 && (in->x_stride > kMaxRow || in->gate_stride > kMaxRow))
+    return TBE_ERR_UNSUPPORTED;
   if (in->x_stride < 0 || in->gate_stride < 0 || in->initial_stride < 0 ||
       !aligned_to(in->initial, 4))
     return TBE_ERR_INVALID_ARGUMENT;
@@ -756,6 +847,8 @@ tbe_status tbe_scan_backward(const tbe_scan_input* in, const float* carry, const
     return TBE_ERR_INVALID_ARGUMENT;
   if (in->tokens > 1 && (dx_stride < in->dim || dgate_stride < in->dim))
     return TBE_ERR_INVALID_ARGUMENT;
+  if (in->tokens > 1 && (grad_h_stride > kMaxRow || dx_stride > kMaxRow || dgate_stride > kMaxRow))
+    return TBE_ERR_UNSUPPORTED;
   ScanArgs a = scan_args(in);
   a.carried = carry;
   a.grad_h = grad_h;
