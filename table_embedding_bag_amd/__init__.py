@@ -89,8 +89,8 @@ class _Runs(ctypes.Structure):
 class _ScanInput(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("gate_kind", ctypes.c_int32),
-                ("index_dtype", ctypes.c_int32), ("x", ctypes.c_void_p),
-                ("x_stride", ctypes.c_int64), ("gate", ctypes.c_void_p),
+                ("index_dtype", ctypes.c_int32), ("max_polls", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("gate", ctypes.c_void_p),
                 ("gate_stride", ctypes.c_int64), ("offsets", ctypes.c_void_p),
                 ("initial", ctypes.c_void_p), ("initial_stride", ctypes.c_int64)]
 

@@ -118,31 +118,46 @@ __device__ __forceinline__ int64_t offset_at(const ScanArgs& a, int64_t s) {
 // The token axis is cut into tiles whatever the sequences: W waves of T tokens
 // each (a span), and 64 V channels, V neighbours a lane.  Within its span a wave
 // reduces the recurrence to "state out = A state in + B" per channel, the waves'
-// pairs join in LDS, and the tiles' in the workspace: a tile publishes its own
-// (A, B), or, where a sequence starts inside, the state it ends with, which
-// depends on no earlier tile; it then looks back for the nearest tile whose end
-// state is known and folds the pairs between, first tile first, into its own
-// start state and the end state it publishes.  Every state is the same sequence
-// of operations whichever tile was found, so results do not depend on timing.
-// The waves then run their tokens from their start states.  One pass: inputs are
-// read once and stay in registers in between.
+// pairs join in LDS, and the tiles' in the workspace.  A tile publishes its own
+// (A, B) or, where a sequence starts inside, the state it ends with, which
+// depends on no earlier tile.  Sixteen tiles make a group; its last tile
+// publishes the group's pair or state the same way, and, once it knows the state
+// the group starts from, the group's end state.  A tile's start state is that of
+// its group (the nearest earlier group whose end state is there, taken through
+// the pairs of the groups between) taken through the tiles before it in the
+// group, or from the nearest of them that knows its state: within a group nothing
+// waits for a chain, and the chain has one link for 16 tiles.  Every state is the
+// same sequence of operations whatever was found when, so results do not depend
+// on timing.  The waves then run their tokens from their start states.  One pass:
+// inputs are read once and stay in registers in between.
 //
 // What passes between tiles is written and read with 8- and 4-byte device-scope
 // atomics; a value is there once it differs from all ones (a NaN that canonical()
-// never lets through).  Tiles are numbered by a ticket taken at a workgroup's
-// start, so every tile waited for is running or done.
+// never lets through).  Workgroups start in the order of their numbers, so the
+// tiles waited for are running; nothing rests on that: a wait ends after
+// max_polls, and the tile then walks its sequence's earlier tokens itself.  (A
+// ticket taken at each workgroup's start, which would fix the order, costs 14 ns
+// a workgroup on its one counter.)
 constexpr int kCarry = 8;                  // tokens between the states that are carried
 constexpr uint64_t kNoPair = ~uint64_t{0};
 constexpr uint32_t kNoState = ~uint32_t{0};
-constexpr uint32_t kSpinLimit = 1u << 22;  // polls before a wait gives up (states turn NaN)
+constexpr uint32_t kMaxPolls = 1u << 16;   // each about a microsecond
 
+constexpr int kGroup = 16;                 // tiles
+
+// What a row of `dim` channels publishes: a pair, a state, or both.
+struct Published {
+  uint64_t* pairs;
+  uint32_t* states;
+};
 struct ScanWork {
-  uint32_t* ticket;
-  int32_t* lo;       // [tiles + 1]: first offset at or past the tile's first token
-  uint64_t* pairs;   // [tiles, dim]
-  uint32_t* states;  // [tiles, dim]
-  int64_t tiles;
+  int2* marks;       // [tokens]: the sequences that start and end with a token, or -1
+  Published tile;    // [tiles, dim]: a pair or a state
+  Published group;   // [groups, dim]: a pair, then a state
+  int64_t tiles, rows;  // rows: of all published ones, tiles first
   int32_t channel_blocks;
+  int32_t deep;         // sequences span tiles: look at a whole group at once
+  uint32_t max_polls;
 };
 
 __device__ __forceinline__ float canonical(float v) {
@@ -163,32 +178,53 @@ __device__ __forceinline__ void st_state(uint32_t* p, float v) {
   __hip_atomic_store(p, __float_as_uint(canonical(v)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Before the tiles: nothing published, the tiles' first offsets found, and the
-// empty sequences' outputs, which belong to no token (copied from `from`).
-__global__ __launch_bounds__(kBlock) void scan_prepare(ScanArgs a, ScanWork w, int32_t tile_tokens,
-                                                       const float* from, int64_t from_stride,
-                                                       float* to) {
+// The first offset at or past `token`: 64 probes at a time.
+__device__ __forceinline__ int64_t find_offset(const ScanArgs& a, int64_t token) {
+  const int lane = lane_id();
+  int64_t lo = 0, hi = a.seqs + 1;
+  while (hi > lo) {
+    const int64_t step = (hi - lo + 63) / 64, at = lo + (lane + 1) * step - 1;
+    const int below = __popcll(__ballot(at < hi && offset_at(a, at) < token));
+    lo += below * step;
+    if (step == 1) break;
+    hi = lo + step - 1 < hi ? lo + step - 1 : hi;
+  }
+  return lo;
+}
+
+// Before the tiles: nothing published, each token's sequences marked (a wave
+// takes 64 tokens), and the empty sequences' outputs, which belong to no token,
+// copied from `from`.
+__global__ __launch_bounds__(kBlock) void scan_prepare(ScanArgs a, ScanWork w, const float* from,
+                                                       int64_t from_stride, float* to) {
+  __shared__ int2 marks[kWavesPerBlock][64];
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
   const int64_t all = static_cast<int64_t>(gridDim.x) * kBlock;
-  if (id == 0) *w.ticket = 0u;
-  const int64_t words = w.tiles * a.dim;
-  for (int64_t i = id; i < words; i += all) {
-    w.pairs[i] = kNoPair;
-    w.states[i] = kNoState;
-  }
-  if (w.tiles > 0)
-    for (int64_t k = id; k <= w.tiles; k += all) {
-      const int64_t token = k * tile_tokens;
-      int64_t lo = 0, hi = a.seqs + 1;
-      while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (offset_at(a, mid) < token) lo = mid + 1;
-        else hi = mid;
-      }
-      w.lo[k] = static_cast<int32_t>(lo);
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  for (int64_t t0 = id - lane; t0 < a.tokens; t0 += all) {
+    marks[wave][lane] = make_int2(-1, -1);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int64_t end = t0 + 64;
+    bool more = true;
+    for (int64_t i0 = find_offset(a, t0); more && i0 <= a.seqs; i0 += 64) {
+      const int64_t i = i0 + lane < a.seqs ? i0 + lane : a.seqs;
+      const int64_t o = offset_at(a, i), next = offset_at(a, i < a.seqs ? i + 1 : i),
+                    before = offset_at(a, i > 0 ? i - 1 : i);
+      const bool in = i0 + lane <= a.seqs;
+      if (in && o >= t0 && o < end && next > o) marks[wave][o - t0].x = static_cast<int32_t>(i);
+      if (in && o > t0 && o <= end && before < o)
+        marks[wave][o - 1 - t0].y = static_cast<int32_t>(i - 1);
+      more = __all(o <= end);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (t0 + lane < a.tokens) w.marks[t0 + lane] = marks[wave][lane];
+  }
+  const int64_t words = w.rows * a.dim;
+  for (int64_t i = id; i < words; i += all) {
+    w.tile.pairs[i] = kNoPair;
+    w.tile.states[i] = kNoState;
+  }
   if (!to) return;
-  const int lane = lane_id();
   for (int64_t s0 = id - lane; s0 < a.seqs; s0 += all) {
     const int64_t s = s0 + lane;
     uint64_t empty = __ballot(s < a.seqs && offset_at(a, s) >= offset_at(a, s + 1));
@@ -200,52 +236,81 @@ __global__ __launch_bounds__(kBlock) void scan_prepare(ScanArgs a, ScanWork w, i
   }
 }
 
+// The sequence that holds the token before `token` (a thread by itself).
+__device__ int64_t sequence_before(const ScanArgs& a, int64_t token) {
+  int64_t lo = 0, hi = a.seqs + 1;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (offset_at(a, mid) < token) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo - 1;
+}
+
 // What the waves of a tile share.
 template <int V, int W, int T>
 struct TileShared {
-  static constexpr int kWindow = 2 * W;  // tiles looked back on at a time
-  uint32_t ticket;
-  int32_t lists[2][W * T];               // sequence that starts at / ends with a token, or -1
-  uint32_t resets[W];                    // the wave's span holds a reset
+  uint32_t resets[W];                    // tokens of the wave's span that start afresh
   float A[W][64 * V], B[W][64 * V];
-  float pair_a[kWindow][64 * V], pair_b[kWindow][64 * V];
-  uint32_t state[kWindow][64 * V];
+  uint64_t pair[kGroup][64 * V];         // of the tiles before this one in its group
+  uint32_t state[kGroup][64 * V];
+  uint64_t group_pair[W][64 * V];        // of the W groups before this one
+  uint32_t group_state[W][64 * V];
+  uint32_t kind[kGroup], group_kind[W];
 };
 
-// Which sequences start in and end with the tile's tokens.
-template <int V, int W, int T>
-__device__ __forceinline__ void list_sequences(const ScanArgs& a, const ScanWork& w, int64_t tile,
-                                               TileShared<V, W, T>& sh) {
-  constexpr int kTokens = W * T;
-  const int64_t t0 = tile * kTokens;
-  const int64_t lo = w.lo[tile], hi = w.lo[tile + 1];
-  for (int64_t i = lo + threadIdx.x; i <= hi && i <= a.seqs; i += 64 * W) {
-    const int64_t o = offset_at(a, i);
-    const int64_t at = o - t0;
-    if (i < a.seqs && at >= 0 && at < kTokens && offset_at(a, i + 1) > o)
-      sh.lists[0][at] = static_cast<int32_t>(i);
-    if (i > 0 && at >= 1 && at <= kTokens && offset_at(a, i - 1) < o)
-      sh.lists[1][at - 1] = static_cast<int32_t>(i - 1);
+// An entry as a wave reads it.
+enum Kind : uint32_t { kAbsent, kPair, kState };
+template <int V>
+struct Entry {
+  uint64_t pair[V];
+  uint32_t state[V];
+  // What is there of row r for all the wave's channels.
+  __device__ __forceinline__ Kind read(const Published& p, int64_t at, bool mine) {
+    bool paired = true, known = true;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      pair[v] = 0;
+      state[v] = 0;
+      if (mine) {
+        state[v] = ld_state(p.states + at + v);
+        pair[v] = ld_pair(p.pairs + at + v);
+      }
+      known = known && state[v] != kNoState;
+      paired = paired && pair[v] != kNoPair;
+    }
+    return __all(known) ? kState : __all(paired) ? kPair : kAbsent;
   }
+};
+__device__ __forceinline__ float pair_a(uint64_t p) {
+  return __uint_as_float(static_cast<uint32_t>(p));
+}
+__device__ __forceinline__ float pair_b(uint64_t p) {
+  return __uint_as_float(static_cast<uint32_t>(p >> 32));
 }
 
 // A tile's start state per channel (the state after its predecessor in scan
-// order), the tile's own pair, and the end state published.  STEP: +1 where
-// tile k follows tile k - 1, -1 where it follows tile k + 1.
-template <int V, int W, int T, int STEP>
+// order), and the tile's and its group's entries published.  STEP: +1 where tile
+// k follows tile k - 1, -1 where it follows tile k + 1; tiles and groups are
+// numbered in scan order here.  walk(start) works the start state out from the
+// inputs, for waits that give up.
+template <int V, int W, int T, int STEP, typename Walk>
 __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w, int64_t tile,
                                            int64_t c0, bool mine, TileShared<V, W, T>& sh,
-                                           float (&start)[V]) {
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
+                                           float (&start)[V], Walk walk) {
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t k = STEP > 0 ? tile : w.tiles - 1 - tile, group = k / kGroup;
+  const int in_group = static_cast<int>(k % kGroup);
+  const bool first = k == 0, last = in_group == kGroup - 1;
   // the tile's pair: wave by wave in scan order
   float A[V], B[V];
-  bool reset = false;
+  bool reset = first;
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
-#pragma unroll
+#pragma unroll 2
   for (int q = 0; q < W; ++q) {
     const int i = STEP > 0 ? q : W - 1 - q;
-    const bool r = sh.resets[i];
+    const bool r = sh.resets[i] != 0u;
     reset |= r;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -254,84 +319,146 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
       A[v] *= wa;
     }
   }
-  const bool first = STEP > 0 ? tile == 0 : tile == w.tiles - 1;
-  const int64_t here = tile * a.dim + c0;
-  if (wave == 0) {
+  const int64_t at = k * a.dim + c0, group_at = group * a.dim + c0;
+  const auto publish = [&](const Published& p, int64_t to, bool known) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (mine) {
-        if (reset || first) st_state(w.states + here + v, B[v]);
-        else st_pair(w.pairs + here + v, A[v], B[v]);
+        if (known) st_state(p.states + to + v, B[v]);
+        else st_pair(p.pairs + to + v, A[v], B[v]);
       }
+  };
+  if (wave == 0) {
+    publish(w.tile, at, reset);
+    if (last && reset) publish(w.group, group_at, true);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) start[v] = 0.0f;
-  // no state comes in where the tile's first token (in scan order) starts afresh
-  if (first || sh.lists[STEP > 0 ? 0 : 1][STEP > 0 ? 0 : W * T - 1] >= 0) return;
-  constexpr int kWindow = TileShared<V, W, T>::kWindow;
-  uint32_t spins = 0;
-  for (int round = 0;; ++round) {
-    // The first look is at the nearest tile alone (with short sequences it knows
-    // its end state by itself), the later ones at the whole window.
-    const int n = round == 0 ? 1 : kWindow;
+  // No state comes in where the tile's first token (in scan order) starts afresh.
+  if (first || (STEP > 0 ? sh.resets[0] & 1u : sh.resets[W - 1] >> (T - 1) & 1u)) return;
+
+  // The tiles before this one in the group, nearest first, up to the nearest that
+  // knows its state.  Unless sequences span tiles the nearest alone is looked at
+  // first: mostly it does.
+  uint32_t polls = 0;
+  int depth = 0;        // tiles taken
+  bool known = false, given_up = false;
+  while (depth < in_group && !known && !given_up) {
+    const int n = depth == 0 && !w.deep ? 1 : in_group;
+    for (int e = depth + wave; e < n; e += W) {
+      Entry<V> x;
+      Kind kind;
+      for (;; ++polls) {
+        kind = x.read(w.tile, (k - 1 - e) * a.dim + c0, mine);
+        if (kind != kAbsent || polls >= w.max_polls) break;
+        __builtin_amdgcn_s_sleep(1);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        sh.pair[e][lane * V + v] = x.pair[v];
+        sh.state[e][lane * V + v] = x.state[v];
+      }
+      if (lane == 0) sh.kind[e] = kind;
+    }
     __syncthreads();
-    for (int e = wave; e < n; e += W) {
-      const int64_t k = tile - static_cast<int64_t>(STEP) * (e + 1);
-      const bool real = k >= 0 && k < w.tiles;
-      uint64_t pair[V];
-      uint32_t state[V];
-      bool there;
-      do {
-        there = true;
+    const uint32_t kind = lane >= depth && lane < n ? sh.kind[lane] : kPair;
+    const uint64_t states = __ballot(kind == kState), absent = __ballot(kind == kAbsent);
+    const int to = states ? __builtin_ctzll(states) + 1 : n;
+    given_up = absent != 0 && __builtin_ctzll(absent) < to;
+    known = states != 0;
+    depth = to;
+  }
+
+  // The state the group starts from, unless a tile of the group knows its own.
+  float ga[V], gb[V];  // the group's pair
+#pragma unroll
+  for (int v = 0; v < V; ++v) ga[v] = 1.0f, gb[v] = 0.0f;
+  const bool chained = !known && !given_up && group > 0;
+  if (chained) {
+    if (wave == 0 && last && !reset) {  // first tile first
+#pragma unroll 4
+      for (int e = kGroup - 2; e >= 0; --e)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          pair[v] = 0;
-          state[v] = 0;
-          if (real && mine) {
-            state[v] = ld_state(w.states + k * a.dim + c0 + v);
-            pair[v] = ld_pair(w.pairs + k * a.dim + c0 + v);
-            there = there && (state[v] != kNoState || pair[v] != kNoPair);
-          }
+          const uint64_t p = sh.pair[e][lane * V + v];
+          gb[v] = fmaf(pair_a(p), gb[v], pair_b(p));
+          ga[v] *= pair_a(p);
         }
-        if (__all(there)) break;
-        if (++spins > kSpinLimit) break;
-        __builtin_amdgcn_s_sleep(1);
-      } while (true);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        sh.pair_a[e][lane * V + v] = __uint_as_float(static_cast<uint32_t>(pair[v]));
-        sh.pair_b[e][lane * V + v] = __uint_as_float(static_cast<uint32_t>(pair[v] >> 32));
-        sh.state[e][lane * V + v] = state[v];
+        gb[v] = fmaf(A[v], gb[v], B[v]);
+        ga[v] *= A[v];
+        if (mine) st_pair(w.group.pairs + group_at + v, ga[v], gb[v]);
       }
     }
-    __syncthreads();
-    // from the nearest tile whose end state is there, through the pairs of those
-    // after it (a tile without a state has its pair)
-    bool have[V];
+    // Wave e watches the e-th group before; each wave goes on by itself as soon as
+    // the nearest state is there with the pairs of the groups after it.
+    volatile uint32_t* kinds = sh.group_kind;
+    const bool real = group - 1 - wave >= 0;
+    uint32_t seen = kAbsent;
+    int found = -1;
+    for (;; ++polls) {
+      if (seen != kState) {
+        Entry<V> x;
+        const uint32_t now = real ? x.read(w.group, (group - 1 - wave) * a.dim + c0, mine) : kPair;
+        if (now > seen) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) have[v] = false;
-    for (int e = n - 1; e >= 0; --e)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const uint32_t s = sh.state[e][lane * V + v];
-        const float on = fmaf(sh.pair_a[e][lane * V + v], start[v], sh.pair_b[e][lane * V + v]);
-        start[v] = s != kNoState ? __uint_as_float(s) : on;
-        have[v] = have[v] || s != kNoState;
+          for (int v = 0; v < V; ++v) {
+            if (now == kPair) sh.group_pair[wave][lane * V + v] = x.pair[v];
+            else sh.group_state[wave][lane * V + v] = x.state[v];
+          }
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+          if (lane == 0) kinds[wave] = now;
+          seen = now;
+        }
       }
-    bool all = true;
+      uint32_t kind[W];
 #pragma unroll
-    for (int v = 0; v < V; ++v) all = all && have[v];
-    if (__all(all)) break;
-    if (round > static_cast<int>(kSpinLimit >> 4)) {
+      for (int e = 0; e < W; ++e) kind[e] = kinds[e];
+      found = -1;
 #pragma unroll
-      for (int v = 0; v < V; ++v) start[v] = __uint_as_float(0x7FC00000u);
-      break;
+      for (int e = W - 1; e >= 0; --e) found = kind[e] == kState ? e : kind[e] == kPair ? found : -1;
+      found = __builtin_amdgcn_readfirstlane(found);
+      if (found >= 0 || polls >= w.max_polls) break;
+      __builtin_amdgcn_s_sleep(1);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    given_up = found < 0;
+    if (!given_up) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) start[v] = __uint_as_float(sh.group_state[found][lane * V + v]);
+      for (int e = found - 1; e >= 0; --e)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const uint64_t p = sh.group_pair[e][lane * V + v];
+          start[v] = fmaf(pair_a(p), start[v], pair_b(p));
+        }
+#pragma unroll
+      for (int v = 0; v < V; ++v) gb[v] = fmaf(ga[v], start[v], gb[v]);  // the group's end
     }
   }
-  if (wave == 0 && !reset) {
+  if (given_up) {
+    walk(start);
+  } else {
+    if (known) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        start[v] = __uint_as_float(sh.state[depth - 1][lane * V + v]);
+    }
+#pragma unroll 4
+    for (int e = known ? depth - 2 : depth - 1; e >= 0; --e)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint64_t p = sh.pair[e][lane * V + v];
+        start[v] = fmaf(pair_a(p), start[v], pair_b(p));
+      }
+  }
+  if (wave == 0 && last && !reset) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (mine) st_state(w.states + here + v, fmaf(A[v], start[v], B[v]));
+      if (mine)
+        st_state(w.group.states + group_at + v,
+                 chained && !given_up ? gb[v] : fmaf(A[v], start[v], B[v]));
   }
 }
 
@@ -339,7 +466,7 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
 template <int V, int W, int T, int STEP>
 __device__ __forceinline__ void wave_start(const TileShared<V, W, T>& sh, int wave, int lane,
                                            float (&state)[V]) {
-#pragma unroll
+#pragma unroll 2
   for (int q = 0; q < W; ++q) {
     const int i = STEP > 0 ? q : W - 1 - q;
     if (STEP > 0 ? i < wave : i > wave) {
@@ -352,6 +479,11 @@ __device__ __forceinline__ void wave_start(const TileShared<V, W, T>& sh, int wa
     }
   }
 }
+
+// Has v in its register from here on.  Without it the compiler puts the last
+// operations on a span's values off until they are used, holds more than their
+// results in the meantime, and spills.
+__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
 
 // A buffer descriptor: loads past `bytes` give 0, stores there are dropped.  The
 // spans' loads and stores go through these, so that no branch parts them and all
@@ -416,11 +548,12 @@ __device__ __forceinline__ void load_span(Buffer rows, int64_t stride, uint32_t 
   for (int i = 0; i < T; ++i)
     out[i] = __builtin_bit_cast(StoredVec<ST, V>, RowWord<ST, V>::load(rows, lane_off + i * step));
 }
-// The rows of `base` of the sequences whose bits are set in mask (list: lane i
-// holds the sequence of token i), 0 for the others.
+// The rows of `base` of the sequences whose bits are set in mask (list: lane at +
+// i holds the sequence of token i), 0 for the others.
 template <int V, int T>
 __device__ __forceinline__ void load_marked(const float* base, int64_t stride, uint32_t mask,
-                                            int32_t list, int64_t c, int64_t dim, uint32_t lane_off,
+                                            int32_t list, int at, int64_t c, int64_t dim,
+                                            uint32_t lane_off,
                                             float (&out)[T][V]) {
 #pragma unroll
   for (int i = 0; i < T; ++i)
@@ -429,7 +562,7 @@ __device__ __forceinline__ void load_marked(const float* base, int64_t stride, u
   if (!base || !mask) return;
 #pragma unroll
   for (int i = 0; i < T; ++i) {
-    const int64_t s = __builtin_amdgcn_readlane(list, i);
+    const int64_t s = __builtin_amdgcn_readlane(list, at + i);
     const Buffer row = buffer(base + (s < 0 ? 0 : s * stride) + c, s < 0 ? 0 : (dim - c) * 4);
     const auto r = __builtin_bit_cast(StoredVec<kF32, V>, RowWord<kF32, V>::load(row, lane_off));
 #pragma unroll
@@ -444,54 +577,45 @@ __device__ __forceinline__ void store_row(Buffer rows, uint32_t off, const float
   RowWord<ST, V>::store(__builtin_bit_cast(typename RowWord<ST, V>::type, o), rows, off);
 }
 
-// Tile and channels of a workgroup, in the order of the tickets, and the lists cleared.
-template <int V, int W, int T>
-__device__ __forceinline__ uint32_t take_ticket(const ScanWork& w, TileShared<V, W, T>& sh) {
-  if (threadIdx.x == 0) sh.ticket = atomicAdd(w.ticket, 1u);
-  for (int i = threadIdx.x; i < 2 * W * T; i += 64 * W) (&sh.lists[0][0])[i] = -1;
-  __syncthreads();
-  return sh.ticket;
-}
-
 template <int ST, int V, bool SIGMOID, int W, int T>
 __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) {
   __shared__ TileShared<V, W, T> sh;
-  const uint32_t ticket = take_ticket(w, sh);
-  const int64_t tile = ticket / w.channel_blocks;
+  const uint32_t order = blockIdx.x;
+  const int64_t tile = order / w.channel_blocks;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c = static_cast<int64_t>(ticket % w.channel_blocks) * (64 * V), c0 = c + lane * V;
+  const int64_t c = static_cast<int64_t>(order % w.channel_blocks) * (64 * V), c0 = c + lane * V;
   const bool mine = c0 < a.dim;  // V divides dim
   constexpr int bytes = StorageTraits<ST>::bytes;
   const uint32_t at = mine ? lane * V * bytes : kOutside, at32 = mine ? lane * V * 4 : kOutside;
   const int64_t t0 = tile * (W * T) + wave * T;
   const int tokens = static_cast<int>(a.tokens - t0 < 0 ? 0 : a.tokens - t0 < T ? a.tokens - t0
                                                                                      : T);
+  // First of all: their answer does not wait for the rows' then.
+  const int2 marks = lane < tokens ? w.marks[t0 + lane] : make_int2(-1, -1);
   StoredVec<ST, V> x[T], g[T];
   load_span<ST, V, T>(span_buffer<ST>(a.gate, a.gate_stride, t0, tokens, c, a.dim), a.gate_stride, at, g);
   load_span<ST, V, T>(span_buffer<ST>(a.x, a.x_stride, t0, tokens, c, a.dim), a.x_stride, at, x);
-  list_sequences<V, W, T>(a, w, tile, sh);
-  __syncthreads();
-  const int32_t starts = lane < T ? sh.lists[0][wave * T + lane] : -1;
-  const int32_t ends = lane < T ? sh.lists[1][wave * T + lane] : -1;
+  if (threadIdx.x < W) sh.group_kind[threadIdx.x] = kAbsent;
+  const int32_t starts = marks.x, ends = marks.y;
   const uint32_t first = static_cast<uint32_t>(__ballot(starts >= 0));
   const uint32_t last = static_cast<uint32_t>(__ballot(ends >= 0));
-  float init[T][V];
-  load_marked<V, T>(a.initial, a.initial_stride, first, starts, c, a.dim, at32, init);
-
   // state_i = first ? u_i : k_i state_{i-1} + u_i, the state before a first token being in its u
-  float k[T][V], u[T][V], A[V], B[V];
+  float k[T][V], u[T][V], A[V], B[V], init[4][V];
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
 #pragma unroll
   for (int i = 0; i < T; ++i) {
     const bool f = first >> i & 1u;
+    if (i % 4 == 0)  // initial states of four tokens at a time: few spans have more starts
+      load_marked<V, 4>(a.initial, a.initial_stride, first >> i & 15u, starts, i, c, a.dim, at32, init);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const Gates t = gates<SIGMOID>(static_cast<float>(g[i][v]));
       const bool in = i < tokens;
       k[i][v] = in ? t.a : 1.0f;
       const float in_x = t.b * static_cast<float>(x[i][v]);
-      u[i][v] = f ? fmaf(t.a, init[i][v], in_x) : in ? in_x : 0.0f;
+      u[i][v] = f ? fmaf(t.a, init[i % 4][v], in_x) : in ? in_x : 0.0f;
+      settle(k[i][v]), settle(u[i][v]);
       B[v] = f ? u[i][v] : fmaf(k[i][v], B[v], u[i][v]);
       A[v] *= k[i][v];
     }
@@ -504,7 +628,20 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
   if (lane == 0) sh.resets[wave] = first;
   __syncthreads();
   float state[V];
-  join_tiles<V, W, T, 1>(a, w, tile, c0, mine, sh, state);
+  join_tiles<V, W, T, 1>(a, w, tile, c0, mine, sh, state, [&](float (&v)[V]) {
+    // the sequence that the tile's first token goes on
+    const int64_t end = tile * (W * T), s = sequence_before(a, end);
+    if (s < 0 || s >= a.seqs) return;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      if (!mine) continue;
+      v[q] = a.initial ? a.initial[s * a.initial_stride + c0 + q] : 0.0f;
+      for (int64_t t = offset_at(a, s); t < end; ++t) {
+        const Gates n = gates<SIGMOID>(load_one<ST>(a.gate, t * a.gate_stride + c0 + q));
+        v[q] = fmaf(n.a, v[q], n.b * load_one<ST>(a.x, t * a.x_stride + c0 + q));
+      }
+    }
+  });
   wave_start<V, W, T, 1>(sh, wave, lane, state);
   const Buffer carry = span_buffer<kF32>(a.carry, a.dim, t0 / kCarry, (tokens + kCarry - 1) / kCarry, c,
                                          a.dim);
@@ -528,16 +665,18 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
 template <int ST, int V, bool SIGMOID, int W, int T>
 __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWork w) {
   __shared__ TileShared<V, W, T> sh;
-  const uint32_t ticket = take_ticket(w, sh);
-  const int64_t tile = w.tiles - 1 - ticket / w.channel_blocks;
+  const uint32_t order = blockIdx.x;
+  const int64_t tile = w.tiles - 1 - order / w.channel_blocks;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c = static_cast<int64_t>(ticket % w.channel_blocks) * (64 * V), c0 = c + lane * V;
+  const int64_t c = static_cast<int64_t>(order % w.channel_blocks) * (64 * V), c0 = c + lane * V;
   const bool mine = c0 < a.dim;  // V divides dim
   constexpr int bytes = StorageTraits<ST>::bytes;
   const uint32_t at = mine ? lane * V * bytes : kOutside, at32 = mine ? lane * V * 4 : kOutside;
   const int64_t t0 = tile * (W * T) + wave * T;
   const int tokens = static_cast<int>(a.tokens - t0 < 0 ? 0 : a.tokens - t0 < T ? a.tokens - t0
                                                                                      : T);
+  // First of all: their answer does not wait for the rows' then.
+  const int2 marks = lane < tokens ? w.marks[t0 + lane] : make_int2(-1, -1);
   StoredVec<ST, V> x[T], g[T], dh[T];
   load_span<ST, V, T>(span_buffer<ST>(a.gate, a.gate_stride, t0, tokens, c, a.dim), a.gate_stride, at, g);
   load_span<ST, V, T>(span_buffer<ST>(a.x, a.x_stride, t0, tokens, c, a.dim), a.x_stride, at, x);
@@ -552,28 +691,29 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
 #pragma unroll
     for (int v = 0; v < V; ++v) state[v] = r[v];
   }
-  list_sequences<V, W, T>(a, w, tile, sh);
-  __syncthreads();
-  const int32_t starts = lane < T ? sh.lists[0][wave * T + lane] : -1;
-  const int32_t ends = lane < T ? sh.lists[1][wave * T + lane] : -1;
+  if (threadIdx.x < W) sh.group_kind[threadIdx.x] = kAbsent;
+  const int32_t starts = marks.x, ends = marks.y;
   const uint32_t first = static_cast<uint32_t>(__ballot(starts >= 0));
   const uint32_t last = static_cast<uint32_t>(__ballot(ends >= 0));
-  // before[i]: the state before token i; lam_i = up_i + (last ? 0 : mu_{i+1}), mu_i = a_i lam_i,
-  // the gradient of a final state being in its up
-  float before[T][V], up[T][V], A[V], B[V];
-  load_marked<V, T>(a.initial, a.initial_stride, first, starts, c, a.dim, at32, before);
-  load_marked<V, T>(a.grad_final, a.grad_final_stride, last, ends, c, a.dim, at32, up);
+  // lam_i = up_i + (last ? 0 : mu_{i+1}), mu_i = a_i lam_i, the gradient of a final
+  // state being in its up; dgate_i = q_i lam_i with q_i of the state before token i
+  float ka[T][V], kb[T][V], q[T][V], up[T][V], A[V], B[V];
+  load_marked<V, T>(a.initial, a.initial_stride, first, starts, 0, c, a.dim, at32, q);
+  load_marked<V, T>(a.grad_final, a.grad_final_stride, last, ends, 0, c, a.dim, at32, up);
 #pragma unroll
   for (int i = 0; i < T; ++i) {
     const bool f = first >> i & 1u;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const Gates t = gates<SIGMOID>(static_cast<float>(g[i][v]));
-      before[i][v] = f ? before[i][v] : state[v];
-      const float u = t.b * static_cast<float>(x[i][v]);
-      // as the forward pass rounds it
-      state[v] = f ? fmaf(t.a, before[i][v], u) : fmaf(t.a, state[v], u);
+      const bool in = i < tokens;
+      ka[i][v] = in ? t.a : 1.0f;
+      kb[i][v] = t.b;
+      const float before = f ? q[i][v] : state[v], xi = static_cast<float>(x[i][v]);
+      state[v] = fmaf(t.a, before, t.b * xi);  // as the forward pass rounds it
+      q[i][v] = SIGMOID ? (before - xi) * (t.a * t.b) : before;
       up[i][v] += static_cast<float>(dh[i][v]);
+      settle(ka[i][v]), settle(kb[i][v]), settle(q[i][v]), settle(up[i][v]);
     }
   }
 #pragma unroll
@@ -583,9 +723,8 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
     const bool l = last >> i & 1u;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float k = i < tokens ? gates<SIGMOID>(static_cast<float>(g[i][v])).a : 1.0f;
-      B[v] = k * (l ? up[i][v] : up[i][v] + B[v]);
-      A[v] *= k;
+      B[v] = ka[i][v] * (l ? up[i][v] : up[i][v] + B[v]);
+      A[v] *= ka[i][v];
     }
   }
 #pragma unroll
@@ -596,7 +735,21 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
   if (lane == 0) sh.resets[wave] = last;
   __syncthreads();
   float mu[V];
-  join_tiles<V, W, T, -1>(a, w, tile, c0, mine, sh, mu);
+  join_tiles<V, W, T, -1>(a, w, tile, c0, mine, sh, mu, [&](float (&v)[V]) {
+    // the sequence that the token after the tile goes on
+    const int64_t begin = (tile + 1) * (W * T);
+    const int64_t s = sequence_before(a, begin);
+    if (s < 0 || s >= a.seqs) return;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      if (!mine) continue;
+      v[q] = a.grad_final ? a.grad_final[s * a.grad_final_stride + c0 + q] : 0.0f;
+      for (int64_t t = offset_at(a, s + 1) - 1; t >= begin; --t) {
+        const float up = a.grad_h ? load_one<ST>(a.grad_h, t * a.grad_h_stride + c0 + q) : 0.0f;
+        v[q] = gates<SIGMOID>(load_one<ST>(a.gate, t * a.gate_stride + c0 + q)).a * (up + v[q]);
+      }
+    }
+  });
   wave_start<V, W, T, -1>(sh, wave, lane, mu);
   const Buffer dxs = span_buffer<ST>(a.dx, a.dx_stride, t0, tokens, c, a.dim);
   const Buffer dgs = span_buffer<ST>(a.dgate, a.dgate_stride, t0, tokens, c, a.dim);
@@ -608,12 +761,10 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
     float dx[V], dg[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const Gates t = gates<SIGMOID>(static_cast<float>(g[i][v]));
       const float lam = l ? up[i][v] : up[i][v] + mu[v];
-      dx[v] = t.b * lam;
-      dg[v] = SIGMOID ? lam * (before[i][v] - static_cast<float>(x[i][v])) * (t.a * t.b)
-                      : lam * before[i][v];
-      mu[v] = i < tokens ? t.a * lam : mu[v];
+      dx[v] = kb[i][v] * lam;
+      dg[v] = lam * q[i][v];
+      mu[v] = ka[i][v] * lam;
     }
     store_row<ST, V>(dxs, at + i * dx_step, dx);
     store_row<ST, V>(dgs, at + i * dg_step, dg);
@@ -627,14 +778,14 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
 // Waves in a tile and tokens in a wave's span.  The backward pass holds twice as
 // much for each token: its spans are as short as the carry's rows.
 constexpr int kForwardWaves = 8, kForwardSpan = 16;
-constexpr int kBackWaves = 8, kBacT = kCarry;
-constexpr int kForwardTokens = kForwardWaves * kForwardSpan, kBackTokens = kBackWaves * kBacT;
+constexpr int kBackWaves = 8, kBackSpan = kCarry;
+constexpr int kForwardTokens = kForwardWaves * kForwardSpan, kBackTokens = kBackWaves * kBackSpan;
 
 template <int ST, int V, bool SIGMOID>
 hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, bool back, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(w.tiles * w.channel_blocks));
   if (back)
-    hipLaunchKernelGGL((scan_tiles_back<ST, V, SIGMOID, kBackWaves, kBacT>), grid,
+    hipLaunchKernelGGL((scan_tiles_back<ST, V, SIGMOID, kBackWaves, kBackSpan>), grid,
                        dim3(64 * kBackWaves), 0, s, a, w);
   else
     hipLaunchKernelGGL((scan_tiles<ST, V, SIGMOID, kForwardWaves, kForwardSpan>), grid,
@@ -668,10 +819,13 @@ int64_t tiles_of(int64_t tokens, bool back) {
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The workspace: ticket, first offsets, pairs, states.
+int64_t groups_of(int64_t tiles) { return (tiles + kGroup - 1) / kGroup; }
+
+// The workspace: marks, pairs and states of tiles and groups.
 size_t workspace_bytes_of(int64_t tokens, int64_t dim) {
-  const size_t tiles = static_cast<size_t>(tiles_of(tokens, kBackTokens < kForwardTokens));
-  return 256 + up256((tiles + 1) * 4) + up256(tiles * dim * 8) + up256(tiles * dim * 4);
+  const int64_t tiles = tiles_of(tokens, kBackTokens < kForwardTokens);
+  const size_t words = static_cast<size_t>((tiles + groups_of(tiles)) * dim);
+  return up256(static_cast<size_t>(tokens) * 8) + up256(words * 8) + up256(words * 4);
 }
 
 hipError_t launch_scan(ScanArgs a, const tbe_scan_input* in, bool back, void* workspace,
@@ -682,18 +836,22 @@ hipError_t launch_scan(ScanArgs a, const tbe_scan_input* in, bool back, void* wo
   w.tiles = tiles_of(a.tokens, back);
   const int v = lane_channels(in, a);
   w.channel_blocks = static_cast<int32_t>((a.dim + 64 * v - 1) / (64 * v));
+  w.rows = w.tiles + groups_of(w.tiles);
   char* p = static_cast<char*>(workspace);
-  w.ticket = reinterpret_cast<uint32_t*>(p);
-  p += 256;
-  w.lo = reinterpret_cast<int32_t*>(p);
-  p += up256(static_cast<size_t>(w.tiles + 1) * 4);
-  w.pairs = reinterpret_cast<uint64_t*>(p);
-  p += up256(static_cast<size_t>(w.tiles) * a.dim * 8);
-  w.states = reinterpret_cast<uint32_t*>(p);
-  const int64_t work = std::max(w.tiles * a.dim, a.seqs);
+  w.marks = reinterpret_cast<int2*>(p);
+  p += up256(static_cast<size_t>(a.tokens) * 8);
+  w.tile.pairs = reinterpret_cast<uint64_t*>(p);
+  p += up256(static_cast<size_t>(w.rows) * a.dim * 8);
+  w.tile.states = reinterpret_cast<uint32_t*>(p);
+  w.group.pairs = w.tile.pairs + w.tiles * a.dim;
+  w.group.states = w.tile.states + w.tiles * a.dim;
+  w.max_polls = in->max_polls == 0  ? kMaxPolls
+                : in->max_polls < 0 ? 0u
+                                    : static_cast<uint32_t>(in->max_polls);
+  w.deep = a.tokens >= a.seqs * 2 * (back ? kBackTokens : kForwardTokens);
+  const int64_t work = std::max(std::max(w.rows * a.dim, a.tokens), a.seqs);
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((work + kBlock - 1) / kBlock, 1024));
   hipLaunchKernelGGL(scan_prepare, dim3(static_cast<unsigned>(blocks)), dim3(kBlock), 0, s, a, w,
-                     back ? kBackTokens : kForwardTokens,
                      back ? a.grad_final : a.initial,
                      back ? a.grad_final_stride : a.initial_stride, back ? a.dinitial : a.final);
   hipError_t e = hipGetLastError();
@@ -745,8 +903,10 @@ tbe_status check_input(const tbe_scan_input* in) {
 }
 
 tbe_status check_workspace(const tbe_scan_input* in, const void* workspace, size_t bytes) {
+  const size_t need = workspace_bytes_of(in->tokens, in->dim);
+  if (need == 0) return TBE_OK;  // no tokens
   if (!workspace || !aligned_to(workspace, 256)) return TBE_ERR_INVALID_ARGUMENT;
-  return bytes < workspace_bytes_of(in->tokens, in->dim) ? TBE_ERR_WORKSPACE_TOO_SMALL : TBE_OK;
+  return bytes < need ? TBE_ERR_WORKSPACE_TOO_SMALL : TBE_OK;
 }
 
 ScanArgs scan_args(const tbe_scan_input* in) {

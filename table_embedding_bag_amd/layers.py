@@ -17,6 +17,7 @@ from . import (BF16, F16, F32, GATE_DECAY, GATE_SIGMOID, I32, I64, _check, _Scan
 
 _DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
+_MAX_POLLS = 0   # tbe_scan_input.max_polls: the library's default
 _GATE = {"sigmoid": GATE_SIGMOID, "decay": GATE_DECAY}
 
 
@@ -193,8 +194,8 @@ def _scan_input(x, gate, offsets, initial, gate_kind):
     if S == 0 and N > 0:
         _fail("offsets hold no sequence for the tokens")
     ins = 0 if initial is None else _rows(initial, "initial", torch.float32, (S, D))
-    return S, _ScanInput(N, S, D, _DTYPE[x.dtype], kind, _INDEX[offsets.dtype], x.data_ptr(), xs,
-                         gate.data_ptr(), gs, offsets.data_ptr(), _p(initial), ins)
+    return S, _ScanInput(N, S, D, _DTYPE[x.dtype], kind, _INDEX[offsets.dtype], _MAX_POLLS,
+                         x.data_ptr(), xs, gate.data_ptr(), gs, offsets.data_ptr(), _p(initial), ins)
 
 
 def _scan_sizes(N, S, D, dtype):

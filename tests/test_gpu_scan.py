@@ -146,6 +146,15 @@ def test_a_sequence_does_not_reach_its_neighbours():
         assert torch.isnan(dirty["dx"][lo:lo + 31, 10]).all()
 
 
+@pytest.mark.parametrize("polls", [-1, 1])
+@pytest.mark.parametrize("dtype,kind", [("fp32", "decay"), ("bf16", "sigmoid")])
+def test_waits_that_give_up(polls, dtype, kind, monkeypatch):
+    """A part of a sequence that does not wait for the one before works its state out itself."""
+    monkeypatch.setattr(tbe.layers, "_MAX_POLLS", polls)
+    for D in (40, 130, 131):
+        Problem([5, 700, 0, 3, 300, 64, 128, 1], D, DTYPES[dtype], kind, seed=20).check()
+
+
 def test_extreme_gates():
     """Gates of the types' ends: a is 0 or 1, and nothing but the state is lost or kept."""
     p = Problem([50, 200], 16, torch.float32, "sigmoid", seed=9)

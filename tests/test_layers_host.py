@@ -166,7 +166,7 @@ def test_c_dropout_refuses(kw, status):
 
 
 def _scan_input(**kw):
-    a = dict(tokens=6, seqs=2, dim=4, dtype=0, gate_kind=0, index_dtype=1, x=A, x_stride=4, gate=A,
+    a = dict(tokens=6, seqs=2, dim=4, dtype=0, gate_kind=0, index_dtype=1, max_polls=0, x=A, x_stride=4, gate=A,
              gate_stride=4, offsets=A, initial=None, initial_stride=0)
     a.update(kw)
     return tbe._ScanInput(*a.values())
