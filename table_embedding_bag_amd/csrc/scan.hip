@@ -120,13 +120,13 @@ __device__ __forceinline__ int64_t offset_at(const ScanArgs& a, int64_t s) {
 // reduces the recurrence to "state out = A state in + B" per channel, the waves'
 // pairs join in LDS, and the tiles' in the workspace.  A tile publishes its own
 // (A, B) or, where a sequence starts inside, the state it ends with, which
-// depends on no earlier tile.  Sixteen tiles make a group; its last tile
+// depends on no earlier tile.  Eight tiles make a group; its last tile
 // publishes the group's pair or state the same way, and, once it knows the state
 // the group starts from, the group's end state.  A tile's start state is that of
 // its group (the nearest earlier group whose end state is there, taken through
 // the pairs of the groups between) taken through the tiles before it in the
 // group, or from the nearest of them that knows its state: within a group nothing
-// waits for a chain, and the chain has one link for 16 tiles.  Every state is the
+// waits for a chain, and the chain has one link for 8 tiles.  Every state is the
 // same sequence of operations whatever was found when, so results do not depend
 // on timing.  The waves then run their tokens from their start states.  One pass:
 // inputs are read once and stay in registers in between.
@@ -143,7 +143,7 @@ constexpr uint64_t kNoPair = ~uint64_t{0};
 constexpr uint32_t kNoState = ~uint32_t{0};
 constexpr uint32_t kMaxPolls = 1u << 16;   // each about a microsecond
 
-constexpr int kGroup = 16;                 // tiles
+constexpr int kGroup = 8;                  // tiles
 
 // What a row of `dim` channels publishes: a pair, a state, or both.
 struct Published {
@@ -156,7 +156,6 @@ struct ScanWork {
   Published group;   // [groups, dim]: a pair, then a state
   int64_t tiles, rows;  // rows: of all published ones, tiles first
   int32_t channel_blocks;
-  int32_t deep;         // sequences span tiles: look at a whole group at once
   uint32_t max_polls;
 };
 
@@ -338,13 +337,13 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
   if (first || (STEP > 0 ? sh.resets[0] & 1u : sh.resets[W - 1] >> (T - 1) & 1u)) return;
 
   // The tiles before this one in the group, nearest first, up to the nearest that
-  // knows its state.  Unless sequences span tiles the nearest alone is looked at
-  // first: mostly it does.
+  // knows its state.  The nearest alone is looked at first: with short sequences
+  // it does, and with long ones looking at all at once gains nothing.
   uint32_t polls = 0;
   int depth = 0;        // tiles taken
   bool known = false, given_up = false;
   while (depth < in_group && !known && !given_up) {
-    const int n = depth == 0 && !w.deep ? 1 : in_group;
+    const int n = depth == 0 ? 1 : in_group;
     for (int e = depth + wave; e < n; e += W) {
       Entry<V> x;
       Kind kind;
@@ -775,22 +774,31 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
   }
 }
 
-// Waves in a tile and tokens in a wave's span.  The backward pass holds twice as
-// much for each token: its spans are as short as the carry's rows.
-constexpr int kForwardWaves = 8, kForwardSpan = 16;
-constexpr int kBackWaves = 8, kBackSpan = kCarry;
-constexpr int kForwardTokens = kForwardWaves * kForwardSpan, kBackTokens = kBackWaves * kBackSpan;
+// Tokens in a wave's span.  The backward pass holds twice as much for each token:
+// its spans are as short as the carry's rows.
+constexpr int kForwardSpan = 16, kBackSpan = kCarry;
+// Waves in a tile: 4, or 8 where sequences span tiles.  Fewer wait less for each
+// other (8192 sequences of about 20 x 256 bf16: 64 and 100 us with 4, 70 and 113
+// with 8), more make the chain of tiles shorter (4 of 16384 x 1024 bf16: 127 and
+// 227 us with 8, 164 and 314 with 4).
+constexpr int kFewWaves = 4, kManyWaves = 8;
+int waves_of(int64_t tokens, int64_t seqs) { return tokens < seqs * 256 ? kFewWaves : kManyWaves; }
 
-template <int ST, int V, bool SIGMOID>
+template <int ST, int V, bool SIGMOID, int W>
 hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, bool back, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(w.tiles * w.channel_blocks));
   if (back)
-    hipLaunchKernelGGL((scan_tiles_back<ST, V, SIGMOID, kBackWaves, kBackSpan>), grid,
-                       dim3(64 * kBackWaves), 0, s, a, w);
+    hipLaunchKernelGGL((scan_tiles_back<ST, V, SIGMOID, W, kBackSpan>), grid, dim3(64 * W), 0, s, a,
+                       w);
   else
-    hipLaunchKernelGGL((scan_tiles<ST, V, SIGMOID, kForwardWaves, kForwardSpan>), grid,
-                       dim3(64 * kForwardWaves), 0, s, a, w);
+    hipLaunchKernelGGL((scan_tiles<ST, V, SIGMOID, W, kForwardSpan>), grid, dim3(64 * W), 0, s, a, w);
   return hipGetLastError();
+}
+template <int ST, int V, bool SIGMOID>
+hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, bool back, hipStream_t s) {
+  return waves_of(a.tokens, a.seqs) == kFewWaves
+             ? launch_tiles<ST, V, SIGMOID, kFewWaves>(a, w, back, s)
+             : launch_tiles<ST, V, SIGMOID, kManyWaves>(a, w, back, s);
 }
 
 template <int ST, int V>
@@ -812,8 +820,8 @@ int lane_channels(const tbe_scan_input* in, const ScanArgs& a) {
              : 1;
 }
 
-int64_t tiles_of(int64_t tokens, bool back) {
-  const int64_t n = back ? kBackTokens : kForwardTokens;
+int64_t tiles_of(int64_t tokens, int64_t seqs, bool back) {
+  const int64_t n = waves_of(tokens, seqs) * (back ? kBackSpan : kForwardSpan);
   return (tokens + n - 1) / n;
 }
 
@@ -822,8 +830,9 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t groups_of(int64_t tiles) { return (tiles + kGroup - 1) / kGroup; }
 
 // The workspace: marks, pairs and states of tiles and groups.
-size_t workspace_bytes_of(int64_t tokens, int64_t dim) {
-  const int64_t tiles = tiles_of(tokens, kBackTokens < kForwardTokens);
+size_t workspace_bytes_of(int64_t tokens, int64_t seqs, int64_t dim) {
+  static_assert(kBackSpan <= kForwardSpan, "the backward pass has the more tiles");
+  const int64_t tiles = tiles_of(tokens, seqs, true);
   const size_t words = static_cast<size_t>((tiles + groups_of(tiles)) * dim);
   return up256(static_cast<size_t>(tokens) * 8) + up256(words * 8) + up256(words * 4);
 }
@@ -833,7 +842,7 @@ hipError_t launch_scan(ScanArgs a, const tbe_scan_input* in, bool back, void* wo
   if (a.tokens <= 1)  // a single row's stride says nothing
     a.x_stride = a.gate_stride = a.grad_h_stride = a.dx_stride = a.dgate_stride = a.dim;
   ScanWork w{};
-  w.tiles = tiles_of(a.tokens, back);
+  w.tiles = tiles_of(a.tokens, a.seqs, back);
   const int v = lane_channels(in, a);
   w.channel_blocks = static_cast<int32_t>((a.dim + 64 * v - 1) / (64 * v));
   w.rows = w.tiles + groups_of(w.tiles);
@@ -848,7 +857,6 @@ hipError_t launch_scan(ScanArgs a, const tbe_scan_input* in, bool back, void* wo
   w.max_polls = in->max_polls == 0  ? kMaxPolls
                 : in->max_polls < 0 ? 0u
                                     : static_cast<uint32_t>(in->max_polls);
-  w.deep = a.tokens >= a.seqs * 2 * (back ? kBackTokens : kForwardTokens);
   const int64_t work = std::max(std::max(w.rows * a.dim, a.tokens), a.seqs);
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((work + kBlock - 1) / kBlock, 1024));
   hipLaunchKernelGGL(scan_prepare, dim3(static_cast<unsigned>(blocks)), dim3(kBlock), 0, s, a, w,
@@ -873,7 +881,7 @@ tbe_status check_sizes(int64_t tokens, int64_t seqs, int64_t dim, int32_t dtype)
   if (tokens < 0 || seqs < 0 || dim < 1 || !known_dtype(dtype)) return TBE_ERR_INVALID_ARGUMENT;
   if (seqs == 0 && tokens > 0) return TBE_ERR_INVALID_ARGUMENT;
   if (tokens >= kMax || seqs >= kMax || dim > kMaxRow) return TBE_ERR_UNSUPPORTED;
-  // 512 threads for 64 tokens of 64 channels
+  // 512 threads for 64 tokens of 64 channels at most
   if ((tokens + 63) / 64 * ((dim + 63) / 64) >= (int64_t{1} << 23)) return TBE_ERR_UNSUPPORTED;
   return TBE_OK;
 }
@@ -903,7 +911,7 @@ tbe_status check_input(const tbe_scan_input* in) {
 }
 
 tbe_status check_workspace(const tbe_scan_input* in, const void* workspace, size_t bytes) {
-  const size_t need = workspace_bytes_of(in->tokens, in->dim);
+  const size_t need = workspace_bytes_of(in->tokens, in->seqs, in->dim);
   if (need == 0) return TBE_OK;  // no tokens
   if (!workspace || !aligned_to(workspace, 256)) return TBE_ERR_INVALID_ARGUMENT;
   return bytes < need ? TBE_ERR_WORKSPACE_TOO_SMALL : TBE_OK;
@@ -965,7 +973,7 @@ tbe_status tbe_scan_sizes(int64_t tokens, int64_t seqs, int64_t dim, int32_t dty
   const tbe_status st = check_sizes(tokens, seqs, dim, dtype);
   if (st != TBE_OK) return st;
   *carry_bytes = carry_bytes_of(tokens, dim);
-  *workspace_bytes = seqs > 0 ? workspace_bytes_of(tokens, dim) : 0;
+  *workspace_bytes = seqs > 0 ? workspace_bytes_of(tokens, seqs, dim) : 0;
   return TBE_OK;
 }
 

@@ -96,6 +96,9 @@ def test_long_sequences():
     p = Problem([6000, 1, 0, 5001], 8, torch.float32, "sigmoid", seed=6)
     p.gate.add_(4)                      # long memories
     p.check()
+    # one among many short ones (tiles of the size for those), and few of some tiles each
+    Problem([2] * 60 + [4000, 0, 1], 33, torch.bfloat16, "decay", seed=7, halves=True).check()
+    Problem([300] * 9, 130, torch.float16, "sigmoid", seed=8).check()
 
 
 @pytest.mark.parametrize("kind", ["sigmoid", "decay"])
