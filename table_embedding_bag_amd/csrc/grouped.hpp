@@ -137,6 +137,18 @@ __device__ bool find_row_tile(const GroupedArgs& a, int64_t na, Tile* t) {
   return false;
 }
 
+// 16 bytes a lane from a buffer to LDS at `lds` + 16 lane; zeros for offsets past
+// the buffer's end.  In assembly (it writes no register) because the compiler,
+// which cannot tell the slices apart, waits for all such loads before it reads
+// LDS with the transposing instruction; wait_loads() waits for them here.  (m0
+// is never kept by the compiler, which sets it before each use of its own.)
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t offset, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+      ::"s"(lds), "v"(offset), "s"(rsrc)
+      : "memory");
+}
+
 // One operand of a tile: where its chunks come from and which exist.
 //   KMAJ: `free` rows of the tile at base + r * stride, the summed index along them.
 //   else: rows of the summed index at base + k * stride, `free` columns along them.
@@ -147,6 +159,7 @@ struct Operand {
   static constexpr int BK = kRowBytes / bytes;     // summed values in a slice
   static constexpr int CPR = KMAJ ? 8 : R * bytes / 16;  // chunks in a row
   static constexpr int NL = R * 8 / (64 * NW);     // chunks a thread
+  static constexpr int kFragmentReads = KMAJ ? 1 : bytes == 2 ? 2 : 4;
   static_assert(NL >= 1, "every thread has a chunk");
 
   const char* base;
@@ -193,13 +206,14 @@ struct Operand {
       if constexpr (KMAJ) extent = (free - 1) * stride + static_cast<int64_t>(left) * bytes;
       else extent = ((left < BK ? left : BK) - 1) * stride + static_cast<int64_t>(free) * bytes;
       const uint32_t records = left > 0 ? static_cast<uint32_t>(extent) : 0u;
-      auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, records, 0x00020000);
+      const uint64_t at = reinterpret_cast<uint64_t>(p);
+      const u32x4 rsrc = {static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32) & 0xFFFFu, records,
+                          0x00020000u};
+      const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(TBE_LDS(void, to)));
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const uint32_t o = static_cast<int32_t>(column[i]) < left ? off[i] : kOutside;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rsrc, TBE_LDS(void, to + (i * NW + wave) * 1024), 16, o, 0, 0, 0);
-      }
+      for (int i = 0; i < NL; ++i)
+        load_to_lds(rsrc, static_cast<int32_t>(column[i]) < left ? off[i] : kOutside,
+                    lds + (i * NW + wave) * 1024);
     } else {
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
@@ -333,6 +347,20 @@ __device__ __forceinline__ void store_fragment(void* p, const f32x16& v, int64_t
   }
 }
 
+// The order of a quarter's instructions: reads and products in turn.
+// Left to itself the compiler moves the reads behind the products, next to their
+// use, and every quarter starts with a wait for LDS.
+template <int READS, int PRODUCTS>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < (READS > PRODUCTS ? READS : PRODUCTS); ++i) {
+    constexpr int kRead = 0x100, kProduct = 0x8;
+    if (i < READS) __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+    if (i < PRODUCTS) __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -390,42 +418,59 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
 #pragma unroll
     for (int j = 0; j < S::WB; ++j) acc[i][j] = f32x16{};
 
-  auto compute = [&](const unsigned char* from) {
+  auto read = [&](const unsigned char* from, int kk, u32x4 (&fa)[S::WA], u32x4 (&fb)[S::WB]) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      u32x4 fa[S::WA], fb[S::WB];
+    for (int j = 0; j < S::WB; ++j)
+      fb[j] = OpB::fragment(from + S::TA * kRowBytes, wb + 32 * j, kk, lane);
 #pragma unroll
-      for (int j = 0; j < S::WB; ++j)
-        fb[j] = OpB::fragment(from + S::TA * kRowBytes, wb + 32 * j, kk, lane);
+    for (int i = 0; i < S::WA; ++i) fa[i] = OpA::fragment(from, wa + 32 * i, kk, lane);
+  };
+  auto products = [&](const u32x4 (&fa)[S::WA], const u32x4 (&fb)[S::WB]) {
 #pragma unroll
-      for (int i = 0; i < S::WA; ++i) fa[i] = OpA::fragment(from, wa + 32 * i, kk, lane);
+    for (int i = 0; i < S::WA; ++i)
 #pragma unroll
-      for (int i = 0; i < S::WA; ++i)
-#pragma unroll
-        for (int j = 0; j < S::WB; ++j) acc[i][j] = multiply<ST>(fa[i], fb[j], acc[i][j]);
-    }
+      for (int j = 0; j < S::WB; ++j) acc[i][j] = multiply<ST>(fa[i], fb[j], acc[i][j]);
   };
 
   const int32_t slices = static_cast<int32_t>((depth + BK - 1) / BK);
   if constexpr (DIRECT) {
-    // NS - 1 slices ahead; slices past the end load nothing, but count.
-    constexpr int kAhead = S::NS - 1, kLoads = OpA::NL + OpB::NL;
+    // All NS buffers are in flight; slices past the end load nothing, but count.
+    // Each quarter's fragments are read while the one before is multiplied, those
+    // of a slice's first quarter at the end of the slice before: the wait for the
+    // slice's loads and the barrier come before a last quarter, whose fragments
+    // are in registers, and its products cover what follows.
+    constexpr int kLoads = OpA::NL + OpB::NL;
+    constexpr int kReads = S::WA * OpA::kFragmentReads + S::WB * OpB::kFragmentReads;
+    constexpr int kProducts = S::WA * S::WB * (bytes == 4 ? 4 : 1);
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
+    for (int s = 0; s < S::NS; ++s) {
       oa.issue(s * BK, lds + s * S::stage, wave, lane);
       ob.issue(s * BK, lds + s * S::stage + S::TA * kRowBytes, wave, lane);
     }
-    int at = 0, to = kAhead;
+    u32x4 fa[2][S::WA], fb[2][S::WB];
+    unsigned char* at = lds;
+    wait_loads<(S::NS - 1) * kLoads>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read(at, 0, fa[0], fb[0]);
     for (int32_t s = 0; s < slices; ++s) {
-      wait_loads<(kAhead - 1) * kLoads>();  // this wave's loads of slice s are in LDS
-      __builtin_amdgcn_s_barrier();         // all waves', and slice s - 1 is read
+#pragma unroll
+      for (int kk = 0; kk < 3; ++kk) {
+        read(at, kk + 1, fa[(kk + 1) & 1], fb[(kk + 1) & 1]);
+        products(fa[kk & 1], fb[kk & 1]);
+        interleave<kReads, kProducts>();
+      }
+      unsigned char* next = at + S::stage == lds + S::NS * S::stage ? lds : at + S::stage;
+      wait_loads<(S::NS - 2) * kLoads>();  // this wave's loads of the next slice are in LDS
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // and its reads of this one done
+      __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      unsigned char* next = lds + to * S::stage;
-      oa.issue((s + kAhead) * BK, next, wave, lane);
-      ob.issue((s + kAhead) * BK, next + S::TA * kRowBytes, wave, lane);
-      compute(lds + at * S::stage);
-      at = at + 1 == S::NS ? 0 : at + 1;
-      to = to + 1 == S::NS ? 0 : to + 1;
+      oa.issue((s + S::NS) * BK, at, wave, lane);
+      ob.issue((s + S::NS) * BK, at + S::TA * kRowBytes, wave, lane);
+      read(next, 0, fa[0], fb[0]);
+      products(fa[1], fb[1]);
+      interleave<kReads, kProducts>();
+      at = next;
     }
     wait_loads<0>();
   } else {
@@ -437,7 +482,12 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
     for (int32_t s = 0; s < slices; ++s) {
       oa.issue((s + 1) * BK, lds, wave, lane);
       ob.issue((s + 1) * BK, lds, wave, lane);
-      compute(lds + (s & 1) * S::stage);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        u32x4 fa[S::WA], fb[S::WB];
+        read(lds + (s & 1) * S::stage, kk, fa, fb);
+        products(fa, fb);
+      }
       unsigned char* next = lds + ((s + 1) & 1) * S::stage;
       oa.put(next, wave, lane);
       ob.put(next + S::TA * kRowBytes, wave, lane);
@@ -453,9 +503,18 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
       if (a.bias) {  // one value for each of the lane's columns, the same for all rows
         f32x16 b;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int64_t c = c0 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
-          b[e] = c < cols ? load_one<ST>(a.bias, t.group * a.M + c) : 0.0f;
+        for (int q = 0; q < 4; ++q) {
+          const int64_t c = c0 + 8 * q + 4 * (lane >> 5), at = t.group * a.M + c;
+          StoredVec<ST, 4> four = {};
+          if (c + 4 <= cols) {
+            four = load_vec<ST, 4>(a.bias, at);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (c + e < cols) four[e] = static_cast<const typename Stored<ST>::type*>(a.bias)[at + e];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) b[4 * q + e] = static_cast<float>(four[e]);
         }
 #pragma unroll
         for (int j = 0; j < S::WB; ++j) acc[i][j] += b;
