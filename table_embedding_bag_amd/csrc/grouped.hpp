@@ -13,8 +13,9 @@
 //
 // A workgroup stages slices of 128 bytes of the summed index (64 16-bit or 32
 // fp32 values) of both operands in LDS, in 16-byte chunks:
-//   k-major     row r of the tile at 128 r, chunk c at slot c ^ (r & 7), so that
-//               the 32 lanes that read one chunk of 32 rows spread over the banks;
+//   k-major     row r of the tile at 128 r, chunk c at slot c ^ (r / 2 & 7), so that
+//               16 lanes that read one chunk of 16 rows cover the 256 bytes of the
+//               banks once (c ^ (r & 7) made half of the reads' cycles conflicts);
 //   free-major  row k of the slice at k * (tile width), 16-bit chunks c at slot
 //               c ^ 4 (k & 3): the transposing LDS read takes 4 rows x 16 columns
 //               for each 16 lanes, and this spreads the rows over the banks.
@@ -174,7 +175,7 @@ struct Operand {
     const int q = (i * NW + wave) * 64 + lane;
     *row = q / CPR;
     const int slot = q % CPR;
-    if constexpr (KMAJ) *chunk = slot ^ (*row & 7);
+    if constexpr (KMAJ) *chunk = slot ^ (*row >> 1 & 7);
     else if constexpr (bytes == 2) *chunk = slot ^ ((4 * (*row & 3)) & (CPR - 1));
     else *chunk = slot;
   }
@@ -255,7 +256,7 @@ struct Operand {
   static __device__ __forceinline__ u32x4 fragment(const unsigned char* from, int at, int kk,
                                                    int lane) {
     if constexpr (KMAJ) {
-      const int row = at + (lane & 31), chunk = (2 * kk + (lane >> 5)) ^ (lane & 7);
+      const int row = at + (lane & 31), chunk = (2 * kk + (lane >> 5)) ^ (lane >> 1 & 7);
       return *reinterpret_cast<const u32x4*>(from + row * kRowBytes + chunk * 16);
     } else if constexpr (bytes == 2) {
       const int k = 16 * kk + 8 * (lane >> 5) + ((lane & 15) >> 2);
