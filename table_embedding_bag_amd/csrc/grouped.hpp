@@ -11,18 +11,24 @@
 // operand is "k-major" where the summed index is the one adjacent in memory
 // (both in kForward, B in kGradX) and "free-major" otherwise.
 //
-// A workgroup stages slices of 128 bytes of the summed index (64 16-bit or 32
-// fp32 values) of both operands in LDS, in 16-byte chunks:
-//   k-major     row r of the tile at 128 r, chunk c at slot c ^ (r / 2 & 7), so that
-//               16 lanes that read one chunk of 16 rows cover the 256 bytes of the
-//               banks once (c ^ (r & 7) made half of the reads' cycles conflicts);
+// A workgroup stages slices of RB = 128 or 64 bytes of the summed index of both
+// operands in LDS, in 16-byte chunks:
+//   k-major     row r of the tile at RB r, chunk c at slot c ^ (r / 2 & 7) (128) or
+//               c ^ (r / 4 & 3) (64), so that 16 lanes that read one chunk of 16 rows
+//               cover the 256 bytes of the banks once (c ^ (r & 7) made half of the
+//               reads' cycles conflicts);
 //   free-major  row k of the slice at k * (tile width), 16-bit chunks c at slot
 //               c ^ 4 (k & 3): the transposing LDS read takes 4 rows x 16 columns
 //               for each 16 lanes, and this spreads the rows over the banks.
-// Aligned operands go from memory to LDS directly (buffer loads that write LDS,
-// their descriptor's bounds giving zeros past the rows' and the group's ends);
-// others through registers, element by element at the ends.
+// Slices come by one of two ways.  Through registers, a slice ahead of LDS: the
+// registers are a third buffer beside LDS's two, so a load has a whole slice's
+// products to arrive.  Or, where tiles are small and memory is what counts, from
+// memory to LDS directly, several slices ahead.  Aligned operands are read with
+// buffer loads, whose descriptor's bounds give zeros past the rows' and the
+// group's ends; others element by element at the ends.
 #pragma once
+
+#include <type_traits>
 
 #include "layers.hpp"
 
@@ -62,16 +68,17 @@ using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
 #define TBE_LDS(T, p) ((__attribute__((address_space(3))) T*)(p))
 
-constexpr int kRowBytes = 128;                 // of the summed index in a slice
-constexpr uint32_t kOutside = 0x80000000u;     // past every descriptor's end
+constexpr uint32_t kOutside = 0x80000000u;      // past every descriptor's end
+constexpr uint32_t kBufferFlags = 0x00020000u;  // of a descriptor: 32-bit data, no swizzle
 
-// Tile shape: TA x TB outputs, NA x NB waves, NS slices of LDS.
-template <int TA_, int TB_, int NA_, int NB_, int NS_>
+// Tile shape: TA x TB outputs, NA x NB waves, NS slices of LDS with RB bytes of
+// the summed index each.
+template <int TA_, int TB_, int NA_, int NB_, int NS_, int RB_>
 struct Shape {
-  static constexpr int TA = TA_, TB = TB_, NA = NA_, NB = NB_, NS = NS_;
+  static constexpr int TA = TA_, TB = TB_, NA = NA_, NB = NB_, NS = NS_, RB = RB_;
   static constexpr int NW = NA * NB, threads = 64 * NW;
   static constexpr int WA = TA / NA / 32, WB = TB / NB / 32;  // 32 x 32 outputs a wave
-  static constexpr int stage = (TA + TB) * kRowBytes;
+  static constexpr int stage = (TA + TB) * RB;
 };
 
 __device__ __forceinline__ int64_t group_offset(const GroupedArgs& a, int64_t g) {
@@ -153,13 +160,13 @@ __device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t offset, uint32_
 // One operand of a tile: where its chunks come from and which exist.
 //   KMAJ: `free` rows of the tile at base + r * stride, the summed index along them.
 //   else: rows of the summed index at base + k * stride, `free` columns along them.
-template <int ST, bool KMAJ, int R, int NW, bool DIRECT>
+template <int ST, bool KMAJ, int R, int NW, bool DIRECT, int RB>
 struct Operand {
   static constexpr int bytes = StorageTraits<ST>::bytes;
   static constexpr int EL = 16 / bytes;            // values in a chunk
-  static constexpr int BK = kRowBytes / bytes;     // summed values in a slice
-  static constexpr int CPR = KMAJ ? 8 : R * bytes / 16;  // chunks in a row
-  static constexpr int NL = R * 8 / (64 * NW);     // chunks a thread
+  static constexpr int BK = RB / bytes;     // summed values in a slice
+  static constexpr int CPR = KMAJ ? RB / 16 : R * bytes / 16;  // chunks in a row
+  static constexpr int NL = R * RB / 16 / (64 * NW);     // chunks a thread
   static constexpr int kFragmentReads = KMAJ ? 1 : bytes == 2 ? 2 : 4;
   static_assert(NL >= 1, "every thread has a chunk");
 
@@ -168,14 +175,22 @@ struct Operand {
   int32_t free, depth;       // bounds of the free index from the tile's start, of the summed one
   uint32_t off[DIRECT ? NL : 1];
   uint32_t column[DIRECT ? NL : 1];
-  u32x4 held[DIRECT ? 1 : NL];
+  u32x4 held[NL];
+  const char* from;  // the slice aimed at
+  uint32_t records;
+  int32_t left;
 
+  // What a k-major row's chunk numbers are xored with: rows that lie 256 bytes (all
+  // banks) apart differ in it.
+  static __device__ __forceinline__ int swizzle(int row) {
+    return RB == 128 ? row >> 1 & 7 : row >> 2 & 3;
+  }
   // Row and (global) chunk that thread's i-th LDS chunk holds.
   static __device__ __forceinline__ void place(int i, int wave, int lane, int* row, int* chunk) {
     const int q = (i * NW + wave) * 64 + lane;
     *row = q / CPR;
     const int slot = q % CPR;
-    if constexpr (KMAJ) *chunk = slot ^ (*row >> 1 & 7);
+    if constexpr (KMAJ) *chunk = slot ^ swizzle(*row);
     else if constexpr (bytes == 2) *chunk = slot ^ ((4 * (*row & 3)) & (CPR - 1));
     else *chunk = slot;
   }
@@ -198,56 +213,59 @@ struct Operand {
     }
   }
 
-  // Start the loads of the slice at k0: into LDS at `to`, or into registers.
-  __device__ __forceinline__ void issue(int32_t k0, unsigned char* to, int wave, int lane) {
-    const int32_t left = depth - k0;  // at most 0: a slice past the end, all zeros
-    if constexpr (DIRECT) {
-      const char* p = base + (KMAJ ? static_cast<int64_t>(k0) * bytes : k0 * stride);
-      int64_t extent;
-      if constexpr (KMAJ) extent = (free - 1) * stride + static_cast<int64_t>(left) * bytes;
-      else extent = ((left < BK ? left : BK) - 1) * stride + static_cast<int64_t>(free) * bytes;
-      const uint32_t records = left > 0 ? static_cast<uint32_t>(extent) : 0u;
-      const uint64_t at = reinterpret_cast<uint64_t>(p);
-      const u32x4 rsrc = {static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32) & 0xFFFFu, records,
-                          0x00020000u};
-      const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(TBE_LDS(void, to)));
-#pragma unroll
-      for (int i = 0; i < NL; ++i)
-        load_to_lds(rsrc, static_cast<int32_t>(column[i]) < left ? off[i] : kOutside,
-                    lds + (i * NW + wave) * 1024);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        int row, chunk;
-        place(i, wave, lane, &row, &chunk);
-        const int32_t r = KMAJ ? row : chunk * EL;        // free index
-        const int32_t k = KMAJ ? chunk * EL : row;        // summed index
-        const int64_t e = KMAJ ? k0 + k : r;              // first element along the memory row
-        const char* p = base + (KMAJ ? r * stride : static_cast<int64_t>(k0 + k) * stride);
-        const int32_t room = KMAJ ? left - k : free - r;  // elements of the chunk that exist
-        const bool any = KMAJ ? r < free : k < left;
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (any && room >= EL) {
-          v = __builtin_bit_cast(u32x4, load_vec<ST, EL>(p, e));
-        } else if (any && room > 0) {
-          StoredVec<ST, EL> w = __builtin_bit_cast(StoredVec<ST, EL>, v);
-#pragma unroll
-          for (int j = 0; j < EL; ++j)
-            if (j < room) w[j] = reinterpret_cast<const typename Stored<ST>::type*>(p)[e + j];
-          v = __builtin_bit_cast(u32x4, w);
-        }
-        held[i] = v;
-      }
-    }
+  // The slice at k0 for the loads that follow (past the end: all zeros), ...
+  __device__ __forceinline__ void aim(int32_t k0) {
+    left = depth - k0;
+    const char* p = base + (KMAJ ? static_cast<int64_t>(k0) * bytes : k0 * stride);
+    from = p;
+    int64_t extent;
+    if constexpr (KMAJ) extent = (free - 1) * stride + static_cast<int64_t>(left) * bytes;
+    else extent = ((left < BK ? left : BK) - 1) * stride + static_cast<int64_t>(free) * bytes;
+    records = left > 0 ? static_cast<uint32_t>(extent) : 0u;
+  }
+  // ... and, directly, the load of the thread's i-th chunk of it into the slice at `to`.
+  __device__ __forceinline__ void load(int i, unsigned char* to, int wave) const {
+    const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(TBE_LDS(void, to)));
+    const uint64_t at = reinterpret_cast<uint64_t>(from);
+    const u32x4 rsrc = {static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32) & 0xFFFFu, records,
+                        kBufferFlags};
+    load_to_lds(rsrc, static_cast<int32_t>(column[i]) < left ? off[i] : kOutside,
+                lds + (i * NW + wave) * 1024);
   }
 
-  // Registers to LDS (operands that are not loaded there directly).
-  __device__ __forceinline__ void put(unsigned char* to, int wave, int lane) {
-    if constexpr (!DIRECT) {
+  // Through registers: the load of the i-th chunk of the slice aimed at, ...
+  __device__ __forceinline__ void fetch(int i, int wave, int lane) {
+    if constexpr (DIRECT) {
+      held[i] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                     __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0,
+                                                       static_cast<int>(records), kBufferFlags),
+                     static_cast<int32_t>(column[i]) < left ? off[i] : kOutside, 0, 0));
+    } else {
+      int row, chunk;
+      place(i, wave, lane, &row, &chunk);
+      const int32_t r = KMAJ ? row : chunk * EL;        // free index
+      const int32_t k = KMAJ ? chunk * EL : row;        // summed index
+      const int64_t e = KMAJ ? k : r;                   // first element along the memory row
+      const char* p = from + (KMAJ ? r : k) * stride;
+      const int32_t room = KMAJ ? left - k : free - r;  // elements of the chunk that exist
+      const bool any = KMAJ ? r < free : k < left;
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (any && room >= EL) {
+        v = __builtin_bit_cast(u32x4, load_vec<ST, EL>(p, e));
+      } else if (any && room > 0) {
+        StoredVec<ST, EL> w = __builtin_bit_cast(StoredVec<ST, EL>, v);
 #pragma unroll
-      for (int i = 0; i < NL; ++i)
-        *reinterpret_cast<u32x4*>(to + (i * NW + wave) * 1024 + lane * 16) = held[i];
+        for (int j = 0; j < EL; ++j)
+          if (j < room) w[j] = reinterpret_cast<const typename Stored<ST>::type*>(p)[e + j];
+        v = __builtin_bit_cast(u32x4, w);
+      }
+      held[i] = v;
     }
+  }
+  // ... and its write into the slice at `to`.
+  __device__ __forceinline__ void put(int i, unsigned char* to, int wave, int lane) const {
+    *reinterpret_cast<u32x4*>(to + (i * NW + wave) * 1024 + lane * 16) = held[i];
   }
 
   // The lane's fragment of the 32 free indices from `at`, 16 bytes of the summed
@@ -256,8 +274,8 @@ struct Operand {
   static __device__ __forceinline__ u32x4 fragment(const unsigned char* from, int at, int kk,
                                                    int lane) {
     if constexpr (KMAJ) {
-      const int row = at + (lane & 31), chunk = (2 * kk + (lane >> 5)) ^ (lane >> 1 & 7);
-      return *reinterpret_cast<const u32x4*>(from + row * kRowBytes + chunk * 16);
+      const int row = at + (lane & 31), chunk = (2 * kk + (lane >> 5)) ^ swizzle(lane & 31);
+      return *reinterpret_cast<const u32x4*>(from + row * RB + chunk * 16);
     } else if constexpr (bytes == 2) {
       const int k = 16 * kk + 8 * (lane >> 5) + ((lane & 15) >> 2);
       const int col = at + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
@@ -348,9 +366,9 @@ __device__ __forceinline__ void store_fragment(void* p, const f32x16& v, int64_t
   }
 }
 
-// The order of a quarter's instructions: reads and products in turn.
-// Left to itself the compiler moves the reads behind the products, next to their
-// use, and every quarter starts with a wait for LDS.
+// The order of some instructions: reads and products in turn.  Left to itself the
+// compiler moves the reads behind the products, next to their use, and every
+// step starts with a wait for LDS.
 template <int READS, int PRODUCTS>
 __device__ __forceinline__ void interleave() {
 #pragma unroll
@@ -362,6 +380,15 @@ __device__ __forceinline__ void interleave() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// for (i = FROM; i < TO; ++i) with i known to the compiler.
+template <int FROM, int TO, typename F>
+__device__ __forceinline__ void repeat(F f) {
+  if constexpr (FROM < TO) {
+    f(std::integral_constant<int, FROM>{});
+    repeat<FROM + 1, TO>(f);
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -370,9 +397,9 @@ __device__ __forceinline__ void wait_loads() {
 template <int ST, Product P, typename S, bool DIRECT>
 __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
   constexpr bool kAKmaj = P == kForward, kBKmaj = P != kGradW;
-  using OpA = Operand<ST, kAKmaj, S::TA, S::NW, DIRECT>;
-  using OpB = Operand<ST, kBKmaj, S::TB, S::NW, DIRECT>;
-  constexpr int BK = OpA::BK;
+  using OpA = Operand<ST, kAKmaj, S::TA, S::NW, DIRECT, S::RB>;
+  using OpB = Operand<ST, kBKmaj, S::TB, S::NW, DIRECT, S::RB>;
+  constexpr int BK = OpA::BK, KK = S::RB / 32;  // of a slice: values, steps of 32 bytes
   constexpr int bytes = StorageTraits<ST>::bytes;
   __shared__ __align__(1024) unsigned char lds[S::NS * S::stage];
 
@@ -419,80 +446,134 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
 #pragma unroll
     for (int j = 0; j < S::WB; ++j) acc[i][j] = f32x16{};
 
-  auto read = [&](const unsigned char* from, int kk, u32x4 (&fa)[S::WA], u32x4 (&fb)[S::WB]) {
-#pragma unroll
-    for (int j = 0; j < S::WB; ++j)
-      fb[j] = OpB::fragment(from + S::TA * kRowBytes, wb + 32 * j, kk, lane);
-#pragma unroll
-    for (int i = 0; i < S::WA; ++i) fa[i] = OpA::fragment(from, wa + 32 * i, kk, lane);
+  // Fragment f of a step: first B's, then A's.
+  auto read = [&](const unsigned char* from, int kk, int f, u32x4 (&fa)[S::WA], u32x4 (&fb)[S::WB]) {
+    if (f < S::WB)
+      fb[f < S::WB ? f : 0] = OpB::fragment(from + S::TA * S::RB, wb + 32 * f, kk, lane);
+    else
+      fa[f < S::WB ? 0 : f - S::WB] = OpA::fragment(from, wa + 32 * (f - S::WB), kk, lane);
   };
-  auto products = [&](const u32x4 (&fa)[S::WA], const u32x4 (&fb)[S::WB]) {
-#pragma unroll
-    for (int i = 0; i < S::WA; ++i)
-#pragma unroll
-      for (int j = 0; j < S::WB; ++j) acc[i][j] = multiply<ST>(fa[i], fb[j], acc[i][j]);
-  };
+  constexpr int kFragments = S::WA + S::WB, kTiles = S::WA * S::WB;
 
   const int32_t slices = static_cast<int32_t>((depth + BK - 1) / BK);
-  if constexpr (DIRECT) {
-    // All NS buffers are in flight; slices past the end load nothing, but count.
-    // Each quarter's fragments are read while the one before is multiplied, those
-    // of a slice's first quarter at the end of the slice before: the wait for the
-    // slice's loads and the barrier come before a last quarter, whose fragments
-    // are in registers, and its products cover what follows.
-    constexpr int kLoads = OpA::NL + OpB::NL;
-    constexpr int kReads = S::WA * OpA::kFragmentReads + S::WB * OpB::kFragmentReads;
-    constexpr int kProducts = S::WA * S::WB * (bytes == 4 ? 4 : 1);
+  constexpr int kLoads = OpA::NL + OpB::NL;
+  u32x4 fa[2][S::WA], fb[2][S::WB];
+  // Part p of n of a step: reads of the next step's fragments and products of this
+  // one's, taking turns.
+  auto part = [&](auto p_, auto parts, auto kk_, const unsigned char* next_step) {
+    constexpr int p = p_, n = parts, kk = kk_;
+    constexpr int f0 = p * kFragments / n, f1 = (p + 1) * kFragments / n;
+    constexpr int t0 = p * kTiles / n, t1 = (p + 1) * kTiles / n;
+    constexpr int kFragmentB = f1 < S::WB ? f1 - f0 : f0 < S::WB ? S::WB - f0 : 0;
 #pragma unroll
-    for (int s = 0; s < S::NS; ++s) {
-      oa.issue(s * BK, lds + s * S::stage, wave, lane);
-      ob.issue(s * BK, lds + s * S::stage + S::TA * kRowBytes, wave, lane);
+    for (int f = f0; f < f1; ++f) read(next_step, (kk + 1) % KK, f, fa[(kk + 1) & 1], fb[(kk + 1) & 1]);
+#pragma unroll
+    for (int t = t0; t < t1; ++t)
+      acc[t / S::WB][t % S::WB] =
+          multiply<ST>(fa[kk & 1][t / S::WB], fb[kk & 1][t % S::WB], acc[t / S::WB][t % S::WB]);
+    interleave<kFragmentB * OpB::kFragmentReads + (f1 - f0 - kFragmentB) * OpA::kFragmentReads,
+               (t1 - t0) * (bytes == 4 ? 4 : 1)>();
+  };
+  if constexpr (DIRECT && S::NS > 2) {
+    // Of the NS buffers one is read, NS - 2 are in flight and one, read before, is
+    // being filled; slices past the end load nothing, but count.  A step's loads,
+    // the reads of the next step's fragments and its products take turns: loads all
+    // at once block the wave, in front of its products, until the memory pipeline
+    // has taken them (1.1 ms of a 0.85 ms product).  A slice's first fragments are
+    // read at the end of the slice before: the wait for the slice's loads and the
+    // barrier come before a last step, whose fragments are in registers, and its
+    // products cover what follows.
+    constexpr int kBefore = (KK - 1) * kLoads / KK;  // a slice's loads before that wait
+    auto load = [&](int i, unsigned char* to) {
+      if (i < OpA::NL) oa.load(i < OpA::NL ? i : 0, to, wave);
+      else ob.load(i < OpA::NL ? 0 : i - OpA::NL, to + S::TA * S::RB, wave);
+    };
+#pragma unroll
+    for (int s = 0; s < S::NS - 1; ++s) {
+      oa.aim(s * BK);
+      ob.aim(s * BK);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load(i, lds + s * S::stage);
     }
-    u32x4 fa[2][S::WA], fb[2][S::WB];
-    unsigned char* at = lds;
-    wait_loads<(S::NS - 1) * kLoads>();
+    unsigned char *at = lds, *fill = lds + (S::NS - 1) * S::stage;
+    wait_loads<(S::NS - 2) * kLoads>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    read(at, 0, fa[0], fb[0]);
-    for (int32_t s = 0; s < slices; ++s) {
 #pragma unroll
-      for (int kk = 0; kk < 3; ++kk) {
-        read(at, kk + 1, fa[(kk + 1) & 1], fb[(kk + 1) & 1]);
-        products(fa[kk & 1], fb[kk & 1]);
-        interleave<kReads, kProducts>();
-      }
+    for (int f = 0; f < kFragments; ++f) read(at, 0, f, fa[0], fb[0]);
+    for (int32_t s = 0; s < slices; ++s) {
       unsigned char* next = at + S::stage == lds + S::NS * S::stage ? lds : at + S::stage;
-      wait_loads<(S::NS - 2) * kLoads>();  // this wave's loads of the next slice are in LDS
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // and its reads of this one done
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      oa.issue((s + S::NS) * BK, at, wave, lane);
-      ob.issue((s + S::NS) * BK, at + S::TA * kRowBytes, wave, lane);
-      read(next, 0, fa[0], fb[0]);
-      products(fa[1], fb[1]);
-      interleave<kReads, kProducts>();
+      oa.aim((s + S::NS - 1) * BK);
+      ob.aim((s + S::NS - 1) * BK);
+      repeat<0, KK>([&](auto kk_) {
+        constexpr int kk = kk_, kFrom = kk * kLoads / KK, kTo = (kk + 1) * kLoads / KK;
+        constexpr int kParts = kTo - kFrom > 1 ? kTo - kFrom : 1;
+        if constexpr (kk == KK - 1) {
+          // this wave's loads of the next slice are in LDS, its reads of this one done
+          wait_loads<(S::NS - 3) * kLoads + kBefore>();
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
+        repeat<0, kParts>([&](auto p_) {
+          if constexpr (kFrom + p_ < kTo) load(kFrom + p_, fill);
+          part(p_, std::integral_constant<int, kParts>{}, kk_, kk == KK - 1 ? next : at);
+        });
+      });
+      fill = at;
       at = next;
     }
     wait_loads<0>();
   } else {
-    oa.issue(0, lds, wave, lane);
-    ob.issue(0, lds, wave, lane);
-    oa.put(lds, wave, lane);
-    ob.put(lds + S::TA * kRowBytes, wave, lane);
-    __syncthreads();
-    for (int32_t s = 0; s < slices; ++s) {
-      oa.issue((s + 1) * BK, lds, wave, lane);
-      ob.issue((s + 1) * BK, lds, wave, lane);
+    // While slice s is read from its buffer, the registers' slice s + 1 goes into the
+    // other one, chunk by chunk, and each chunk's register takes its load of slice
+    // s + 2 at once: a load has one slice's products to arrive.  All writes come
+    // before the last step, which reads the next slice's first fragments.
+    auto fetch = [&](int i) {
+      if (i < OpA::NL) oa.fetch(i < OpA::NL ? i : 0, wave, lane);
+      else ob.fetch(i < OpA::NL ? 0 : i - OpA::NL, wave, lane);
+    };
+    auto put = [&](int i, unsigned char* to) {
+      if (i < OpA::NL) oa.put(i < OpA::NL ? i : 0, to, wave, lane);
+      else ob.put(i < OpA::NL ? 0 : i - OpA::NL, to + S::TA * S::RB, wave, lane);
+    };
+    oa.aim(0);
+    ob.aim(0);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        u32x4 fa[S::WA], fb[S::WB];
-        read(lds + (s & 1) * S::stage, kk, fa, fb);
-        products(fa, fb);
-      }
+    for (int i = 0; i < kLoads; ++i) fetch(i);
+    oa.aim(BK);
+    ob.aim(BK);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      put(i, lds);
+      fetch(i);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int f = 0; f < kFragments; ++f) read(lds, 0, f, fa[0], fb[0]);
+    for (int32_t s = 0; s < slices; ++s) {
+      const unsigned char* at = lds + (s & 1) * S::stage;
       unsigned char* next = lds + ((s + 1) & 1) * S::stage;
-      oa.put(next, wave, lane);
-      ob.put(next + S::TA * kRowBytes, wave, lane);
-      __syncthreads();
+      oa.aim((s + 2) * BK);
+      ob.aim((s + 2) * BK);
+      repeat<0, KK>([&](auto kk_) {
+        constexpr int kk = kk_;
+        constexpr int kFrom = kk == KK - 1 ? kLoads : kk * kLoads / (KK - 1);
+        constexpr int kTo = kk == KK - 1 ? kLoads : (kk + 1) * kLoads / (KK - 1);
+        constexpr int kParts = kTo - kFrom > 1 ? kTo - kFrom : 1;
+        if constexpr (kk == KK - 1) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads and writes
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
+        repeat<0, kParts>([&](auto p_) {
+          if constexpr (kFrom + p_ < kTo) {
+            put(kFrom + p_, next);
+            fetch(kFrom + p_);
+          }
+          part(p_, std::integral_constant<int, kParts>{}, kk_, kk == KK - 1 ? next : at);
+        });
+      });
     }
   }
 
@@ -572,9 +653,9 @@ hipError_t launch_product(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-using Large = Shape<256, 256, 2, 4, 2>;
-using Medium = Shape<128, 128, 2, 2, 2>;
-using Small = Shape<128, 32, 4, 1, 4>;
+using Large = Shape<256, 256, 2, 4, 2, 128>;
+using Medium = Shape<128, 128, 2, 2, 2, 128>;
+using Small = Shape<128, 32, 4, 1, 4, 128>;
 
 template <int ST, Product P>
 hipError_t launch_rows(const GroupedArgs& a, hipStream_t s) {
