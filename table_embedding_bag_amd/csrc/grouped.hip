@@ -28,6 +28,12 @@ bool chunked(const void* p, int64_t stride, int64_t width, int32_t dtype) {
          stride <= (int64_t{1} << 20) && width <= stride;
 }
 
+// The chunks' sums of the weights' and the bias's gradients.
+size_t backward_bytes_of(int64_t rows, int64_t groups, int64_t K, int64_t M, int32_t dtype) {
+  return static_cast<size_t>(plan_grad_w(rows, groups, K, M, dtype).slots) *
+         static_cast<size_t>(M * K + M) * sizeof(float);
+}
+
 tbe_status check_sizes(int64_t rows, int64_t groups, int64_t K, int64_t M, int32_t dtype) {
   if (rows < 0 || groups < 0 || K < 1 || M < 1 || !known_dtype(dtype))
     return TBE_ERR_INVALID_ARGUMENT;
@@ -54,7 +60,7 @@ tbe_status tbe_grouped_linear_sizes(int64_t rows, int64_t groups, int64_t in_fea
   const tbe_status st = check_sizes(rows, groups, in_features, out_features, dtype);
   if (st != TBE_OK) return st;
   *forward_bytes = 0;
-  *backward_bytes = 0;
+  *backward_bytes = backward_bytes_of(rows, groups, in_features, out_features, dtype);
   return TBE_OK;
 }
 
@@ -125,6 +131,16 @@ tbe_status tbe_grouped_linear_backward(const void* x, int64_t x_stride, const vo
   a.dx_stride = dx_stride;
   a.dw = dweight;
   a.db = dbias;
+  if (dweight) {
+    const GradWPlan plan = plan_grad_w(rows, groups, in_features, out_features, dtype);
+    const size_t need = backward_bytes_of(rows, groups, in_features, out_features, dtype);
+    if (need > 0 && (!workspace || !aligned_to(workspace, 256))) return TBE_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return TBE_ERR_WORKSPACE_TOO_SMALL;
+    a.chunk = plan.chunk;
+    a.slots = plan.slots;
+    a.parts = static_cast<float*>(workspace);
+    a.bias_parts = a.parts + plan.slots * out_features * in_features;
+  }
   a.index64 = index_dtype == TBE_I64;
   a.direct = chunked(x, x_stride, in_features, dtype) &&
              chunked(weight, in_features, in_features, dtype) &&

@@ -48,7 +48,36 @@ struct GroupedArgs {
   int64_t x_stride, y_stride, grad_stride, dx_stride;
   int32_t index64;
   int32_t direct;      // every operand's rows are whole, aligned 16-byte chunks
+  // The weights' gradient: groups of more than chunk rows are summed in chunks
+  // (0: never), whose sums go to parts [slots][M * K] and bias_parts [slots][M].
+  int64_t chunk, slots;
+  float* parts;
+  float* bias_parts;
 };
+
+// How the weights' gradient is summed, from the call's sizes alone.
+struct GradWPlan {
+  bool large;         // 256 x 256 tiles, else 128 x 128
+  int64_t chunk;      // as above
+  int64_t slots;
+};
+inline GradWPlan plan_grad_w(int64_t rows, int64_t groups, int64_t K, int64_t M, int32_t dtype) {
+  const auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((K + t - 1) / t); };
+  // Large tiles are a fifth faster, but need some for each CU: groups differ in
+  // size, and the last round leaves CUs idle.  (16384 rows in 8 groups of very
+  // different sizes, 1024 x 4096, bf16: 512 large tiles 320 us, 2048 small ones 196.)
+  GradWPlan p{groups * tiles(256) >= 1024, 0, 0};
+  const int64_t t = tiles(128);
+  if (!p.large && groups * t < 512 && rows > 0) {
+    // too few tiles for the chip: chunks of rows, about one for each place
+    const int64_t least = dtype == TBE_F32 ? 128 : 256;
+    const int64_t want = (rows * t + 511) / 512;
+    p.chunk = std::max(least, (want + 63) / 64 * 64);
+    // a group of n > chunk rows has at most 2 n / chunk chunks
+    p.slots = rows > p.chunk ? 2 * rows / p.chunk : 0;
+  }
+  return p;
+}
 
 // The products of one call; defined for each type in its own file.
 hipError_t launch_grouped_f32(const GroupedArgs& a, bool backward, hipStream_t s);
@@ -155,6 +184,61 @@ __device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t offset, uint32_
       "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
       ::"s"(lds), "v"(offset), "s"(rsrc)
       : "memory");
+}
+
+// Row chunk `unit` of the groups' chunks of a.chunk rows (an empty group has one):
+// its group and rows, and its slot among the chunks of the groups that have
+// several, or -1; false where there are fewer.
+struct Unit {
+  int64_t group, first, end, slot;
+};
+__device__ bool find_chunk(const GroupedArgs& a, int64_t unit, Unit* u) {
+  const int lane = lane_id();
+  int64_t slots = 0;
+  for (int64_t g0 = 0; g0 < a.groups; g0 += 64) {
+    int64_t lo = 0, n = 0;
+    const bool real = g0 + lane < a.groups;
+    if (real) {
+      lo = group_offset(a, g0 + lane);
+      n = group_offset(a, g0 + lane + 1) - lo;
+      n = n > 0 ? n : 0;
+    }
+    uint32_t chunks = static_cast<uint32_t>((n + a.chunk - 1) / a.chunk);
+    if (real && chunks == 0) chunks = 1;
+    const uint32_t many = chunks > 1 ? chunks : 0;
+    const uint32_t incl = wave_inclusive_sum(chunks), slot = wave_inclusive_sum(many);
+    const uint64_t past = __ballot(static_cast<int64_t>(incl) > unit);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const int64_t c = unit - __builtin_amdgcn_readlane(incl - chunks, l);
+      const int64_t rows = __builtin_amdgcn_readlane(static_cast<uint32_t>(n), l);
+      u->group = g0 + l;
+      u->first = __builtin_amdgcn_readlane(static_cast<uint32_t>(lo), l) + c * a.chunk;
+      u->end = u->first + (rows - c * a.chunk < a.chunk ? rows - c * a.chunk : a.chunk);
+      u->slot = __builtin_amdgcn_readlane(many, l)
+                    ? slots + __builtin_amdgcn_readlane(slot - many, l) + c
+                    : -1;
+      return true;
+    }
+    unit -= __builtin_amdgcn_readlane(incl, 63);
+    slots += __builtin_amdgcn_readlane(slot, 63);
+  }
+  return false;
+}
+
+// The group with the r-th most rows (of up to 64; more are taken as they come).
+__device__ int64_t ranked_group(const GroupedArgs& a, int64_t r) {
+  if (a.groups > 64) return r;
+  const int lane = lane_id();
+  int32_t n = -1;
+  if (lane < a.groups) n = static_cast<int32_t>(group_offset(a, lane + 1) - group_offset(a, lane));
+  int rank = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const int32_t other = __builtin_amdgcn_readlane(n, g);
+    rank += other > n || (other == n && g < lane);
+  }
+  const uint64_t is = __ballot(lane < a.groups && rank == r);
+  return is ? __builtin_ctzll(is) : r;
 }
 
 // One operand of a tile: where its chunks come from and which exist.
@@ -407,14 +491,26 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
   const int64_t cols = P == kForward ? a.M : a.K;      // of the output: A's free index
   const int64_t na = (cols + S::TA - 1) / S::TA;
   Tile t;
+  int64_t slot = -1;
   if constexpr (P == kGradW) {
-    const int64_t nb = (a.M + S::TB - 1) / S::TB;
-    const int64_t q = xcd_contiguous_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
-    t.group = q / (na * nb);
-    t.first = group_offset(a, t.group);
-    t.end = group_offset(a, t.group + 1);
-    if (t.end < t.first) t.end = t.first;
-    band_order(q - t.group * na * nb, na, nb, &t);
+    // A group's (or chunk's) tiles spread over all XCDs, each taking a contiguous
+    // part of them; groups with the most rows come first, so that short ones fill
+    // the gaps at the end.
+    const int64_t nb = (a.M + S::TB - 1) / S::TB, tiles = na * nb, unit = blockIdx.x / tiles;
+    const int64_t q = xcd_contiguous_block(static_cast<int>(blockIdx.x - unit * tiles),
+                                           static_cast<int>(tiles));
+    if (a.chunk) {
+      Unit u;
+      if (!find_chunk(a, unit, &u)) return;
+      t.group = u.group, t.first = u.first, t.end = u.end, slot = u.slot;
+      if (slot >= a.slots) return;  // groups that overlap: bad offsets
+    } else {
+      t.group = ranked_group(a, unit);
+      t.first = group_offset(a, t.group);
+      t.end = group_offset(a, t.group + 1);
+      if (t.end < t.first) t.end = t.first;
+    }
+    band_order(q, na, nb, &t);
   } else {
     if (!find_row_tile<S::TB>(a, na, &t)) return;
   }
@@ -458,6 +554,18 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
   const int32_t slices = static_cast<int32_t>((depth + BK - 1) / BK);
   constexpr int kLoads = OpA::NL + OpB::NL;
   u32x4 fa[2][S::WA], fb[2][S::WB];
+  // The bias's gradient: the sums of operand B's columns (dy) over the rows, by the
+  // waves that have them first, each lane half of the rows.
+  const bool sums = P == kGradW && a.db && t.ta == 0 && wave % S::NA == 0;
+  float column_sum[S::WB] = {};
+  auto add_columns = [&](const u32x4 (&f)[S::WB]) {
+#pragma unroll
+    for (int j = 0; j < S::WB; ++j) {
+      const auto v = __builtin_bit_cast(StoredVec<ST, 16 / bytes>, f[j]);
+#pragma unroll
+      for (int e = 0; e < 16 / bytes; ++e) column_sum[j] += static_cast<float>(v[e]);
+    }
+  };
   // Part p of n of a step: reads of the next step's fragments and products of this
   // one's, taking turns.
   auto part = [&](auto p_, auto parts, auto kk_, const unsigned char* next_step) {
@@ -473,6 +581,8 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
           multiply<ST>(fa[kk & 1][t / S::WB], fb[kk & 1][t % S::WB], acc[t / S::WB][t % S::WB]);
     interleave<kFragmentB * OpB::kFragmentReads + (f1 - f0 - kFragmentB) * OpA::kFragmentReads,
                (t1 - t0) * (bytes == 4 ? 4 : 1)>();
+    if constexpr (P == kGradW && p == n - 1)
+      if (sums) add_columns(fb[kk & 1]);
   };
   if constexpr (DIRECT && S::NS > 2) {
     // Of the NS buffers one is read, NS - 2 are in flight and one, read before, is
@@ -606,6 +716,10 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
     for (int j = 0; j < S::WB; ++j) {
       const int64_t r = b0 + wb + 32 * j + (lane & 31);
       const bool row = r - b0 < out_rows;
+      if (P == kGradW && slot >= 0) {
+        store_fragment<kF32>(a.parts + (slot * a.M + r) * a.K + c0, acc[i][j], cols - c0, row, lane);
+        continue;
+      }
       char* p;
       if constexpr (P == kForward)
         p = static_cast<char*>(a.y) + ((t.first + r) * a.y_stride + c0) * bytes;
@@ -616,25 +730,86 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
       store_fragment<ST>(p, acc[i][j], cols - c0, row, lane);
     }
   }
+  if constexpr (P == kGradW) {
+    if (sums) {
+#pragma unroll
+      for (int j = 0; j < S::WB; ++j) {
+        const float v = column_sum[j] + __shfl_xor(column_sum[j], 32);
+        const int64_t m = b0 + wb + 32 * j + lane;
+        if (lane < 32 && m < a.M) {
+          if (slot >= 0) a.bias_parts[slot * a.M + m] = v;
+          else store_one<ST>(a.db, t.group * a.M + m, v);
+        }
+      }
+    }
+  }
 }
 
-// dbias: a workgroup sums 64 columns of one group, four rows at a time.
+// The chunks' sums of a group, first chunk first, to its gradients.
 template <int ST>
-__global__ __launch_bounds__(kBlock) void grouped_bias_grad(GroupedArgs a) {
-  __shared__ float part[4][64];
+__global__ __launch_bounds__(kBlock) void grouped_join(GroupedArgs a, int64_t blocks) {
+  const int64_t g = blockIdx.x / blocks, block = blockIdx.x - g * blocks;
+  int64_t slot = 0, mine = 0;  // of this group's first chunk; its chunks
+  const int lane = lane_id();
+  for (int64_t g0 = 0; g0 <= g; g0 += 64) {
+    uint32_t many = 0;
+    if (g0 + lane <= g) {
+      const int64_t n = group_offset(a, g0 + lane + 1) - group_offset(a, g0 + lane);
+      many = n > a.chunk ? static_cast<uint32_t>((n + a.chunk - 1) / a.chunk) : 0;
+    }
+    const uint32_t sum = wave_inclusive_sum(many);
+    slot += __builtin_amdgcn_readlane(sum, 63);
+    if (g - g0 < 64) mine = __builtin_amdgcn_readlane(many, static_cast<int>(g - g0));
+  }
+  slot -= mine;
+  // written by its only chunk; or bad offsets
+  if (mine == 0 || slot + mine > a.slots) return;
+  const int64_t all = a.M * a.K;
+  const int64_t e0 = (block * kBlock + threadIdx.x) * 4;
+  if (e0 < all) {
+    f32x4 sum = {};
+    const int n = all - e0 < 4 ? static_cast<int>(all - e0) : 4;
+    for (int64_t c = 0; c < mine; ++c) {
+      const float* p = a.parts + (slot + c) * all + e0;
+      if (n == 4) {
+        sum += load_vec<kF32, 4>(p, 0);
+      } else {
+        for (int j = 0; j < n; ++j) sum[j] += p[j];
+      }
+    }
+    for (int j = 0; j < n; ++j) store_one<ST>(a.dw, g * all + e0 + j, sum[j]);
+  }
+  if (a.db) {
+    const int64_t m = block * kBlock + threadIdx.x;
+    if (m < a.M) {
+      float sum = 0.0f;
+      for (int64_t c = 0; c < mine; ++c) sum += a.bias_parts[(slot + c) * a.M + m];
+      store_one<ST>(a.db, g * a.M + m, sum);
+    }
+  }
+}
+
+// The bias's gradient where the weights' is not wanted: a workgroup sums 64 columns
+// of one group, 16 rows at a time.
+template <int ST>
+__global__ __launch_bounds__(1024) void grouped_bias_grad(GroupedArgs a) {
+  __shared__ float part[16][64];
   const int64_t g = blockIdx.y;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
-  const int w = threadIdx.x >> 6;
+  const int lane = lane_id(), w = threadIdx.x >> 6;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  const int64_t end = group_offset(a, g + 1);
   float sum = 0.0f;
-  if (c < a.M)
-    for (int64_t n = group_offset(a, g) + w; n < group_offset(a, g + 1); n += 4)
+  if (c < a.M) {
+#pragma unroll 4
+    for (int64_t n = group_offset(a, g) + w; n < end; n += 16)
       sum += load_one<ST>(a.grad, n * a.grad_stride + c);
-  part[w][threadIdx.x & 63] = sum;
+  }
+  part[w][lane] = sum;
   __syncthreads();
-  if (w == 0 && c < a.M)
-    store_one<ST>(a.db, g * a.M + c,
-                  (part[0][threadIdx.x] + part[1][threadIdx.x]) +
-                      (part[2][threadIdx.x] + part[3][threadIdx.x]));
+  if (w == 0 && c < a.M) {
+    for (int i = 1; i < 16; ++i) sum += part[i][lane];
+    store_one<ST>(a.db, g * a.M + c, sum);
+  }
 }
 
 inline int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
@@ -642,10 +817,12 @@ inline int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 template <int ST, Product P, typename S>
 hipError_t launch_product(const GroupedArgs& a, hipStream_t s) {
   const int64_t na = ceil_div(P == kForward ? a.M : a.K, S::TA);
-  // a group's last row tile may be partial: at most one more for each group
-  const int64_t nb = P == kGradW ? a.groups * ceil_div(a.M, S::TB)
-                                 : a.rows / S::TB + std::min(a.groups, a.rows);
-  const dim3 grid(static_cast<unsigned>(na * nb));
+  // a group's last row tile (or chunk) may be partial: at most one more for each group
+  const int64_t units = P != kGradW ? a.rows / S::TB + std::min(a.groups, a.rows)
+                        : a.chunk   ? a.rows / a.chunk + a.groups
+                                    : a.groups;
+  const int64_t nb = P == kGradW ? ceil_div(a.M, S::TB) : 1;
+  const dim3 grid(static_cast<unsigned>(na * nb * units));
   if (a.direct)
     hipLaunchKernelGGL((grouped_product<ST, P, S, true>), grid, dim3(S::threads), 0, s, a);
   else
@@ -655,15 +832,28 @@ hipError_t launch_product(const GroupedArgs& a, hipStream_t s) {
 
 using Large = Shape<256, 256, 2, 4, 2, 128>;
 using Medium = Shape<128, 128, 2, 2, 2, 128>;
-using Small = Shape<128, 32, 4, 1, 4, 128>;
+using Square = Shape<64, 64, 2, 2, 2, 128>;
+using Narrow = Shape<128, 32, 4, 1, 4, 128>;
 
 template <int ST, Product P>
 hipError_t launch_rows(const GroupedArgs& a, hipStream_t s) {
-  const int64_t mean = a.rows / a.groups, cols = P == kForward ? a.M : a.K;
-  if (mean <= 32) return launch_product<ST, P, Small>(a, s);
-  if (mean >= 256 && ceil_div(a.rows, 256) * ceil_div(cols, 256) >= 256)
-    return launch_product<ST, P, Large>(a, s);
-  return launch_product<ST, P, Medium>(a, s);
+  const int64_t cols = P == kForward ? a.M : a.K;
+  const auto tiles = [&](int64_t t) { return (a.rows / t + a.groups) * ceil_div(cols, t); };
+  if (a.rows <= a.groups * 32) return launch_product<ST, P, Narrow>(a, s);
+  if (tiles(256) >= 1024) return launch_product<ST, P, Large>(a, s);
+  if (tiles(128) >= 1024) return launch_product<ST, P, Medium>(a, s);
+  return launch_product<ST, P, Square>(a, s);
+}
+
+template <int ST>
+hipError_t launch_grad_w(const GroupedArgs& a, const GradWPlan& plan, hipStream_t s) {
+  hipError_t e = plan.large ? launch_product<ST, kGradW, Large>(a, s)
+                            : launch_product<ST, kGradW, Medium>(a, s);
+  if (e != hipSuccess || plan.slots == 0) return e;
+  const int64_t blocks = ceil_div(std::max(ceil_div(a.M * a.K, 4), a.M), kBlock);
+  hipLaunchKernelGGL((grouped_join<ST>), dim3(static_cast<unsigned>(blocks * a.groups)), dim3(kBlock),
+                     0, s, a, blocks);
+  return hipGetLastError();
 }
 
 template <int ST>
@@ -671,16 +861,15 @@ hipError_t launch_grouped(const GroupedArgs& a, bool backward, hipStream_t s) {
   if (!backward) return launch_rows<ST, kForward>(a, s);
   hipError_t e = hipSuccess;
   if (a.dx && a.rows > 0) e = launch_rows<ST, kGradX>(a, s);
-  if (e == hipSuccess && a.dw) {
-    if (a.groups * ceil_div(a.M, 256) * ceil_div(a.K, 256) >= 256)
-      e = launch_product<ST, kGradW, Large>(a, s);
-    else
-      e = launch_product<ST, kGradW, Medium>(a, s);
+  if (e != hipSuccess) return e;
+  if (a.dw) {
+    constexpr int32_t dtype = ST;
+    return launch_grad_w<ST>(a, plan_grad_w(a.rows, a.groups, a.K, a.M, dtype), s);
   }
-  if (e == hipSuccess && a.db) {
+  if (a.db) {
     hipLaunchKernelGGL((grouped_bias_grad<ST>),
                        dim3(static_cast<unsigned>(ceil_div(a.M, 64)), static_cast<unsigned>(a.groups)),
-                       dim3(kBlock), 0, s, a);
+                       dim3(1024), 0, s, a);
     e = hipGetLastError();
   }
   return e;

@@ -79,6 +79,33 @@ def test_many_groups_of_few_rows(dtype):
     Problem(g.integers(0, 3, 64), 512, 96, DTYPES[dtype], seed=4).check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("name,G,N,K,M,wide", [("forward", 12, 12801, 264, 4104, 0), ("dx", 12, 12801, 4104, 264, 8),
+                                               ("dw", 64, 2600, 1040, 1040, 0), ("unaligned", 12, 12801, 263, 4099, 0),
+                                               ("128", 3, 16000, 1096, 1032, 0)])
+def test_many_tiles(name, G, N, K, M, wide, dtype):
+    """Sizes whose products take the largest tiles (and, last, those of 128 on all sides), held to
+    64-bit products on the GPU."""
+    print(f"[grouped] many tiles {name} {dtype}", flush=True)
+    g = np.random.default_rng(20)
+    p = Problem(g.multinomial(N, g.dirichlet(np.ones(G))), K, M, DTYPES[dtype], seed=21, wide=wide)
+    got = p.run()
+    for i in list(range(G))[:: max(1, G // 6)]:
+        r = slice(int(p.off[i]), int(p.off[i + 1]))
+        x, w, dy = p.x[r].double(), p.w[i].double(), p.grad[r].double().contiguous()
+        b = p.bias[i].double()
+        n = r.stop - r.start
+        for what, mine, want, size, terms in (
+                ("y", got["y"][r], x @ w.t().contiguous() + b, x.abs() @ w.abs().t().contiguous() + b.abs(), K),
+                ("dx", got["dx"][r], dy @ w, dy.abs() @ w.abs(), M),
+                ("dw", got["dw"][i], dy.t().contiguous() @ x, dy.abs().t().contiguous() @ x.abs(), n),
+                ("db", got["db"][i], dy.sum(0), dy.abs().sum(0), n)):
+            off = (mine.double() - want).abs()
+            bound = (terms + 2) * ref.U32 * size
+            bound = bound + ref.half_step(p.dtype) * (want.abs() + bound) + ref.TINY[p.dtype]
+            assert (off <= bound).all(), (what, i, float((off / bound).max()))
+
+
 def test_no_rows_and_no_groups():
     for G in (0, 3):
         off = torch.zeros(G + 1, dtype=torch.int64, device="cuda")
