@@ -426,8 +426,10 @@ _LAYERS = ("dropout", "dropout_backward", "scan_step", "scan_forward", "scan_bac
 
 def __getattr__(name):
     """The layers on first use: their module needs torch, this one alone does not."""
-    if name in _LAYERS:
-        from . import layers
-        globals()[name] = value = getattr(layers, name)
+    if name == "layers" or name in _LAYERS:
+        import importlib
+        layers = importlib.import_module(".layers", __name__)
+        value = layers if name == "layers" else getattr(layers, name)
+        globals()[name] = value
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -9,7 +9,7 @@ arguments raise ValueError, statuses of the library TBEError.
 from __future__ import annotations
 
 import ctypes
-from contextlib import nullcontext
+import functools
 
 import torch
 
@@ -17,6 +17,7 @@ from . import (BF16, F16, F32, GATE_DECAY, GATE_SIGMOID, I32, I64, _check, _Scan
 
 _DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
+_U64 = (1 << 64) - 1
 _MAX_POLLS = 0   # tbe_scan_input.max_polls: the library's default
 _GATE = {"sigmoid": GATE_SIGMOID, "decay": GATE_DECAY}
 
@@ -27,8 +28,9 @@ def _fail(what):
 
 def _rows(t, name, dtype=None, shape=None):
     """The row stride of a 2-D tensor of rows, its type, shape and layout checked."""
-    if t.dim() != 2:
-        _fail(f"{name} must have 2 dimensions, got {t.dim()}")
+    stride = t.stride()
+    if len(stride) != 2:
+        _fail(f"{name} must have 2 dimensions, got {len(stride)}")
     if dtype is None:
         if t.dtype not in _DTYPE:
             _fail(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
@@ -36,10 +38,9 @@ def _rows(t, name, dtype=None, shape=None):
         _fail(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         _fail(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    row, col = t.stride()
-    if col != 1 and t.shape[1] > 1 and t.numel():
+    if stride[1] != 1 and t.shape[1] > 1 and t.numel():
         _fail(f"the elements of a row of {name} must be adjacent")
-    return row
+    return stride[0]
 
 
 def _out(t, name, dtype, shape):
@@ -72,29 +73,42 @@ def _on_one_gpu(*tensors):
     """The tensors' GPU; None stands for an argument that was not given."""
     device = tensors[0].device
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            _fail("tensor must live on the GPU")
-        if t.device != device:
-            _fail("tensors must live on one GPU")
+        if t is not None:
+            if not t.is_cuda:
+                _fail("tensor must live on the GPU")
+            if t.device != device:
+                _fail("tensors must live on one GPU")
     return device
 
 
-def _current(device):
-    return nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+# One call's worth of microseconds counts for the smallest calls: the raw stream without a Stream
+# object around it, where torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(device, name, *args):
+    """The library's function on the current stream of the device."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = getattr(load(), name)(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = getattr(load(), name)(*args, _raw_stream(index))
+    if status:
+        _check(status, name)
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+def _like(t):
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
-def _workspace(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+def _workspace(nbytes, like):
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 # --- dropout -----------------------------------------------------------------------------------
@@ -111,36 +125,34 @@ def dropout(x, p, seed, offset, residual=None, out=None):
     """
     if not 0.0 <= p <= 1.0:
         _fail(f"p must lie in [0, 1], got {p}")
-    for name, v in (("seed", seed), ("offset", offset)):
-        if not 0 <= v < 1 << 64:
-            _fail(f"{name} must lie in [0, 2**64), got {v}")
+    if not 0 <= seed <= _U64:
+        _fail(f"seed must lie in [0, 2**64), got {seed}")
+    if not 0 <= offset <= _U64:
+        _fail(f"offset must lie in [0, 2**64), got {offset}")
     shape = x.shape
     if residual is not None and residual.shape != shape:
         _fail(f"residual must have the shape {tuple(shape)}, got {tuple(residual.shape)}")
     if out is not None and out.shape != shape:
         _fail(f"out must have the shape {tuple(shape)}, got {tuple(out.shape)}")
-    if x.dim() != 2:
-        flat = []
+    x2, r2, out2 = x, residual, out
+    if len(shape) != 2:
         for t in (x, residual, out):
             if t is not None and not t.is_contiguous():
                 _fail("a tensor that is no matrix must be contiguous")
-            flat.append(None if t is None else t.view(1, -1))
-        x2, residual, out2 = flat
-    else:
-        x2, out2 = x, out
+        x2 = x.view(1, -1)
+        r2 = None if residual is None else residual.view(1, -1)
+        out2 = None if out is None else out.view(1, -1)
     xs = _rows(x2, "x")
-    rs = 0 if residual is None else _rows(residual, "residual", x.dtype)
-    if out2 is not None:
-        _out(out2, "out", x.dtype, x2.shape)
-    device = _on_one_gpu(x2, residual, out2)
-    with _current(device):
-        if out2 is None:
-            out = torch.empty(shape, dtype=x.dtype, device=device)
-            out2 = out if x.dim() == 2 else out.view(1, -1)
-        rows, cols = x2.shape
-        _check(load().tbe_dropout(x2.data_ptr(), xs, _p(residual), rs, out2.data_ptr(),
-                                  out2.stride(0), rows, cols, _DTYPE[x.dtype], p, seed, offset,
-                                  _raw_stream(device)), "tbe_dropout")
+    rs = 0 if r2 is None else _rows(r2, "residual", x.dtype)
+    if out is not None:
+        ys = _out(out2, "out", x.dtype, x2.shape)
+        device = _on_one_gpu(x, residual, out)
+    else:
+        device = _on_one_gpu(x, residual)
+        out = _like(x)
+        ys = x2.shape[1]
+    _call(device, "tbe_dropout", x.data_ptr(), xs, _p(residual), rs, out.data_ptr(), ys, *x2.shape,
+          _DTYPE[x.dtype], p, seed, offset)
     return out
 
 
@@ -173,13 +185,11 @@ def scan_step(x, gate, state=None, gate_kind="sigmoid", out_state=None):
     if out_state is not None:
         _dense(out_state, "out_state", torch.float32, x.shape)
     device = _on_one_gpu(x, gate, state, out_state)
-    with _current(device):
-        h = torch.empty(x.shape, dtype=x.dtype, device=device)
-        if out_state is None:
-            out_state = torch.empty(x.shape, dtype=torch.float32, device=device)
-        _check(load().tbe_scan_step(x.data_ptr(), xs, gate.data_ptr(), gs, _p(state), ss,
-                                    h.data_ptr(), out_state.data_ptr(), x.shape[0], x.shape[1],
-                                    _DTYPE[x.dtype], kind, _raw_stream(device)), "tbe_scan_step")
+    h = _like(x)
+    if out_state is None:
+        out_state = x.new_empty(x.shape, dtype=torch.float32) if state is None else _like(state)
+    _call(device, "tbe_scan_step", x.data_ptr(), xs, gate.data_ptr(), gs, _p(state), ss, h.data_ptr(),
+          out_state.data_ptr(), *x.shape, _DTYPE[x.dtype], kind)
     return h, out_state
 
 
@@ -198,6 +208,7 @@ def _scan_input(x, gate, offsets, initial, gate_kind):
                          x.data_ptr(), xs, gate.data_ptr(), gs, offsets.data_ptr(), _p(initial), ins)
 
 
+@functools.lru_cache(maxsize=256)
 def _scan_sizes(N, S, D, dtype):
     carry, ws = ctypes.c_size_t(0), ctypes.c_size_t(0)
     _check(load().tbe_scan_sizes(N, S, D, _DTYPE[dtype], ctypes.byref(carry), ctypes.byref(ws)),
@@ -218,13 +229,12 @@ def scan_forward(x, gate, offsets, initial=None, gate_kind="sigmoid", need_carry
     device = _on_one_gpu(x, gate, offsets, initial)
     N, D = x.shape
     nc, nw = _scan_sizes(N, S, D, x.dtype)
-    with _current(device):
-        h = torch.empty((N, D), dtype=x.dtype, device=device)
-        final = torch.empty((S, D), dtype=torch.float32, device=device)
-        carry = torch.empty(nc // 4, dtype=torch.float32, device=device) if need_carry else None
-        ws = _workspace(nw, device)
-        _check(load().tbe_scan_forward(ctypes.byref(inp), h.data_ptr(), final.data_ptr(), _p(carry),
-                                       _p(ws), nw, _raw_stream(device)), "tbe_scan_forward")
+    h = x.new_empty((N, D))
+    final = x.new_empty((S, D), dtype=torch.float32)
+    carry = x.new_empty(nc // 4, dtype=torch.float32) if need_carry else None
+    ws = _workspace(nw, x)
+    _call(device, "tbe_scan_forward", ctypes.byref(inp), h.data_ptr(), final.data_ptr(), _p(carry), _p(ws),
+          nw)
     return h, final, carry
 
 
@@ -248,19 +258,23 @@ def scan_backward(x, gate, offsets, carry, grad_h=None, grad_final=None, initial
         for t, name in zip(out, ("dx", "dgate")):
             _out(t, name, x.dtype, x.shape)
     device = _on_one_gpu(x, gate, offsets, initial, carry, grad_h, grad_final, *(out or ()))
-    with _current(device):
-        dx, dgate = out if out is not None else (torch.empty((N, D), dtype=x.dtype, device=device),
-                                                 torch.empty((N, D), dtype=x.dtype, device=device))
-        dinitial = torch.empty((S, D), dtype=torch.float32, device=device)
-        ws = _workspace(nw, device)
-        _check(load().tbe_scan_backward(ctypes.byref(inp), carry.data_ptr(), _p(grad_h), hs,
-                                        _p(grad_final), fs, dx.data_ptr(), dx.stride(0),
-                                        dgate.data_ptr(), dgate.stride(0), dinitial.data_ptr(),
-                                        _p(ws), nw, _raw_stream(device)), "tbe_scan_backward")
+    dx, dgate = out if out is not None else (x.new_empty((N, D)), x.new_empty((N, D)))
+    dinitial = x.new_empty((S, D), dtype=torch.float32)
+    ws = _workspace(nw, x)
+    _call(device, "tbe_scan_backward", ctypes.byref(inp), carry.data_ptr(), _p(grad_h), hs, _p(grad_final),
+          fs, dx.data_ptr(), dx.stride(0), dgate.data_ptr(), dgate.stride(0), dinitial.data_ptr(), _p(ws), nw)
     return dx, dgate, dinitial
 
 
 # --- grouped linear layer ----------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=256)
+def _grouped_sizes(N, G, K, M, dtype):
+    fw, bw = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().tbe_grouped_linear_sizes(N, G, K, M, _DTYPE[dtype], ctypes.byref(fw), ctypes.byref(bw)),
+           "tbe_grouped_linear_sizes")
+    return fw.value, bw.value
+
 
 def _grouped(x, weight, offsets):
     xs = _rows(x, "x")
@@ -275,10 +289,7 @@ def _grouped(x, weight, offsets):
     if G == 0 and N > 0:
         _fail("offsets hold no group for the rows")
     M = weight.shape[1]
-    fw, bw = ctypes.c_size_t(0), ctypes.c_size_t(0)
-    _check(load().tbe_grouped_linear_sizes(N, G, K, M, _DTYPE[x.dtype], ctypes.byref(fw),
-                                           ctypes.byref(bw)), "tbe_grouped_linear_sizes")
-    return xs, N, G, K, M, fw.value, bw.value
+    return (xs, N, G, K, M, *_grouped_sizes(N, G, K, M, x.dtype))
 
 
 def grouped_linear(x, weight, offsets, bias=None, out=None):
@@ -293,14 +304,12 @@ def grouped_linear(x, weight, offsets, bias=None, out=None):
     if out is not None:
         _out(out, "out", x.dtype, (N, M))
     device = _on_one_gpu(x, weight, offsets, bias, out)
-    with _current(device):
-        if out is None:
-            out = torch.empty((N, M), dtype=x.dtype, device=device)
-        ws = _workspace(nw, device)
-        _check(load().tbe_grouped_linear(x.data_ptr(), xs, weight.data_ptr(), _p(bias),
-                                         offsets.data_ptr(), _INDEX[offsets.dtype], out.data_ptr(),
-                                         out.stride(0), N, G, K, M, _DTYPE[x.dtype], _p(ws), nw,
-                                         _raw_stream(device)), "tbe_grouped_linear")
+    ys = M if out is None else out.stride(0)
+    if out is None:
+        out = x.new_empty((N, M))
+    ws = _workspace(nw, x)
+    _call(device, "tbe_grouped_linear", x.data_ptr(), xs, weight.data_ptr(), _p(bias), offsets.data_ptr(),
+          _INDEX[offsets.dtype], out.data_ptr(), ys, N, G, K, M, _DTYPE[x.dtype], _p(ws), nw)
     return out
 
 
@@ -313,13 +322,11 @@ def grouped_linear_backward(x, weight, offsets, grad, bias=False, need_dx=True, 
     xs, N, G, K, M, _, nw = _grouped(x, weight, offsets)
     gs = _rows(grad, "grad", x.dtype, (N, M))
     device = _on_one_gpu(x, weight, offsets, grad)
-    with _current(device):
-        dx = torch.empty((N, K), dtype=x.dtype, device=device) if need_dx else None
-        dw = torch.empty((G, M, K), dtype=x.dtype, device=device) if need_dweight else None
-        db = torch.empty((G, M), dtype=x.dtype, device=device) if bias else None
-        ws = _workspace(nw, device)
-        _check(load().tbe_grouped_linear_backward(
-            x.data_ptr(), xs, weight.data_ptr(), offsets.data_ptr(), _INDEX[offsets.dtype],
-            grad.data_ptr(), gs, _p(dx), K, _p(dw), _p(db), N, G, K, M, _DTYPE[x.dtype], _p(ws), nw,
-            _raw_stream(device)), "tbe_grouped_linear_backward")
+    dx = x.new_empty((N, K)) if need_dx else None
+    dw = x.new_empty((G, M, K)) if need_dweight else None
+    db = x.new_empty((G, M)) if bias else None
+    ws = _workspace(nw, x)
+    _call(device, "tbe_grouped_linear_backward", x.data_ptr(), xs, weight.data_ptr(), offsets.data_ptr(),
+          _INDEX[offsets.dtype], grad.data_ptr(), gs, _p(dx), K, _p(dw), _p(db), N, G, K, M, _DTYPE[x.dtype],
+          _p(ws), nw)
     return dx, dw, db
