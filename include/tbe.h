@@ -448,7 +448,10 @@ tbe_status tbe_grouped_linear_sizes(int64_t rows, int64_t groups, int64_t in_fea
  * offsets[g] .. offsets[g+1] of x [rows, in_features] and y [rows,
  * out_features], y_n = weight[g] x_n + bias[g].  weight [groups, out_features,
  * in_features] and bias [groups, out_features] (NULL: none) are contiguous;
- * offsets [groups + 1] start at 0 and end at rows.  Groups may be empty. */
+ * offsets [groups + 1] start at 0 and end at rows.  Groups may be empty.  rows
+ * below 2^30, at most 65535 groups, features and strides of inputs at most 2^20,
+ * (rows / 32 + groups) (features / 128) and groups (in_features / 128)
+ * (out_features / 128), rounded up, at most 2^22. */
 tbe_status tbe_grouped_linear(const void* x, int64_t x_stride, const void* weight, const void* bias,
                               const void* offsets, int32_t index_dtype, void* y, int64_t y_stride,
                               int64_t rows, int64_t groups, int64_t in_features,

@@ -20,13 +20,14 @@ hipError_t launch(const GroupedArgs& a, int32_t dtype, bool backward, hipStream_
                             : launch_grouped_bf16(a, backward, s);
 }
 
-// Rows that are whole 16-byte chunks at aligned addresses, close enough that a
-// tile's 256 rows lie within a buffer descriptor's reach.
+// Rows that are whole 16-byte chunks at aligned addresses.
 bool chunked(const void* p, int64_t stride, int64_t width, int32_t dtype) {
   const int64_t b = dtype_bytes(dtype);
-  return aligned_to(p, 16) && stride * b % 16 == 0 && width * b % 16 == 0 &&
-         stride <= (int64_t{1} << 20) && width <= stride;
+  return aligned_to(p, 16) && stride * b % 16 == 0 && width * b % 16 == 0;
 }
+
+// Longest rows and strides: 256 of them lie within a buffer descriptor's reach.
+constexpr int64_t kMaxFeatures = int64_t{1} << 20;
 
 // The chunks' sums of the weights' and the bias's gradients.
 size_t backward_bytes_of(int64_t rows, int64_t groups, int64_t K, int64_t M, int32_t dtype) {
@@ -39,7 +40,6 @@ tbe_status check_sizes(int64_t rows, int64_t groups, int64_t K, int64_t M, int32
     return TBE_ERR_INVALID_ARGUMENT;
   if (groups == 0 && rows > 0) return TBE_ERR_INVALID_ARGUMENT;
   // 31-bit rows, and grids of at most 2^31 threads whatever the tiles
-  constexpr int64_t kMaxFeatures = int64_t{1} << 20;
   if (rows >= (int64_t{1} << 30) || groups > 65535 || K > kMaxFeatures || M > kMaxFeatures)
     return TBE_ERR_UNSUPPORTED;
   const int64_t tk = (K + 127) / 128, tm = (M + 127) / 128;
@@ -79,6 +79,8 @@ tbe_status tbe_grouped_linear(const void* x, int64_t x_stride, const void* weigh
       !aligned_to(offsets, index_dtype == TBE_I64 ? 8 : 4))
     return TBE_ERR_INVALID_ARGUMENT;
   if (x_stride < 0 || (rows > 1 && y_stride < out_features)) return TBE_ERR_INVALID_ARGUMENT;
+  if (rows == 1) x_stride = in_features;  // a single row's stride says nothing
+  if (x_stride > kMaxFeatures) return TBE_ERR_UNSUPPORTED;
   GroupedArgs a{};
   a.rows = rows;
   a.groups = groups;
@@ -116,6 +118,8 @@ tbe_status tbe_grouped_linear_backward(const void* x, int64_t x_stride, const vo
   if (rows > 0 && (!grad || (dx && !weight) || (dweight && !x))) return TBE_ERR_INVALID_ARGUMENT;
   if (x_stride < 0 || grad_stride < 0 || (dx && rows > 1 && dx_stride < in_features))
     return TBE_ERR_INVALID_ARGUMENT;
+  if (rows <= 1) x_stride = in_features, grad_stride = out_features;
+  if (x_stride > kMaxFeatures || grad_stride > kMaxFeatures) return TBE_ERR_UNSUPPORTED;
   GroupedArgs a{};
   a.rows = rows;
   a.groups = groups;

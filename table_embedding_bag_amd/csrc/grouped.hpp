@@ -23,9 +23,11 @@
 // Slices come by one of two ways.  Through registers, a slice ahead of LDS: the
 // registers are a third buffer beside LDS's two, so a load has a whole slice's
 // products to arrive.  Or, where tiles are small and memory is what counts, from
-// memory to LDS directly, several slices ahead.  Aligned operands are read with
-// buffer loads, whose descriptor's bounds give zeros past the rows' and the
-// group's ends; others element by element at the ends.
+// memory to LDS directly, several slices ahead (aligned operands only).
+// All loads are buffer loads, whose descriptor's bounds give zeros past the rows'
+// and the group's ends.  Where rows are not whole aligned chunks, a chunk is
+// loaded as the aligned words it lies in and shifted into place, and what
+// follows a row's end is masked in the last slice.
 #pragma once
 
 #include <type_traits>
@@ -251,15 +253,19 @@ struct Operand {
   static constexpr int BK = RB / bytes;     // summed values in a slice
   static constexpr int CPR = KMAJ ? RB / 16 : R * bytes / 16;  // chunks in a row
   static constexpr int NL = R * RB / 16 / (64 * NW);     // chunks a thread
+  static constexpr bool SHIFT = !DIRECT && bytes == 2;  // rows may start between words
   static constexpr int kFragmentReads = KMAJ ? 1 : bytes == 2 ? 2 : 4;
   static_assert(NL >= 1, "every thread has a chunk");
 
   const char* base;
   int64_t stride;            // bytes
   int32_t free, depth;       // bounds of the free index from the tile's start, of the summed one
-  uint32_t off[DIRECT ? NL : 1];
-  uint32_t column[DIRECT ? NL : 1];
+  uint32_t off[NL];
+  uint32_t column[NL];
   u32x4 held[NL];
+  uint32_t more[SHIFT ? NL : 1];  // the word after
+  uint32_t skew;                  // bytes from the aligned word before base to base
+  uint32_t shift = 0;             // bit i: the chunk held starts between words
   const char* from;  // the slice aimed at
   uint32_t records;
   int32_t left;
@@ -281,30 +287,30 @@ struct Operand {
 
   __device__ __forceinline__ void init(const void* p, int64_t stride_, int64_t free_, int64_t depth_,
                                        int wave, int lane) {
-    base = static_cast<const char*>(p);
+    skew = SHIFT ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 2u : 0u;
+    base = static_cast<const char*>(p) - skew;
     stride = stride_ * bytes;
     free = static_cast<int32_t>(free_ < R ? free_ : R);
     depth = static_cast<int32_t>(depth_);
-    if constexpr (DIRECT) {
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        int row, chunk;
-        place(i, wave, lane, &row, &chunk);
-        const bool inside = (KMAJ ? row : chunk * EL) < free;
-        off[i] = inside ? static_cast<uint32_t>(row * stride) + chunk * 16 : kOutside;
-        column[i] = KMAJ ? chunk * EL : row;   // along the summed index
-      }
+    for (int i = 0; i < NL; ++i) {
+      int row, chunk;
+      place(i, wave, lane, &row, &chunk);
+      const bool inside = (KMAJ ? row : chunk * EL) < free;
+      off[i] = inside ? static_cast<uint32_t>(row * stride) + chunk * 16 + skew : kOutside;
+      column[i] = KMAJ ? chunk * EL : row;   // along the summed index
     }
   }
 
   // The slice at k0 for the loads that follow (past the end: all zeros), ...
   __device__ __forceinline__ void aim(int32_t k0) {
     left = depth - k0;
-    const char* p = base + (KMAJ ? static_cast<int64_t>(k0) * bytes : k0 * stride);
-    from = p;
+    from = base + (KMAJ ? static_cast<int64_t>(k0) * bytes : k0 * stride);
     int64_t extent;
     if constexpr (KMAJ) extent = (free - 1) * stride + static_cast<int64_t>(left) * bytes;
     else extent = ((left < BK ? left : BK) - 1) * stride + static_cast<int64_t>(free) * bytes;
+    // up to the end of the word that holds the last value
+    if constexpr (SHIFT) extent = (extent + skew + 3) & ~int64_t{3};
     records = left > 0 ? static_cast<uint32_t>(extent) : 0u;
   }
   // ... and, directly, the load of the thread's i-th chunk of it into the slice at `to`.
@@ -318,38 +324,38 @@ struct Operand {
   }
 
   // Through registers: the load of the i-th chunk of the slice aimed at, ...
-  __device__ __forceinline__ void fetch(int i, int wave, int lane) {
-    if constexpr (DIRECT) {
-      held[i] = __builtin_bit_cast(
-          u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                     __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0,
-                                                       static_cast<int>(records), kBufferFlags),
-                     static_cast<int32_t>(column[i]) < left ? off[i] : kOutside, 0, 0));
-    } else {
-      int row, chunk;
-      place(i, wave, lane, &row, &chunk);
-      const int32_t r = KMAJ ? row : chunk * EL;        // free index
-      const int32_t k = KMAJ ? chunk * EL : row;        // summed index
-      const int64_t e = KMAJ ? k : r;                   // first element along the memory row
-      const char* p = from + (KMAJ ? r : k) * stride;
-      const int32_t room = KMAJ ? left - k : free - r;  // elements of the chunk that exist
-      const bool any = KMAJ ? r < free : k < left;
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (any && room >= EL) {
-        v = __builtin_bit_cast(u32x4, load_vec<ST, EL>(p, e));
-      } else if (any && room > 0) {
-        StoredVec<ST, EL> w = __builtin_bit_cast(StoredVec<ST, EL>, v);
-#pragma unroll
-        for (int j = 0; j < EL; ++j)
-          if (j < room) w[j] = reinterpret_cast<const typename Stored<ST>::type*>(p)[e + j];
-        v = __builtin_bit_cast(u32x4, w);
-      }
-      held[i] = v;
+  __device__ __forceinline__ void fetch(int i) {
+    const auto rows = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0,
+                                                        static_cast<int>(records), kBufferFlags);
+    uint32_t o = static_cast<int32_t>(column[i]) < left ? off[i] : kOutside;
+    if constexpr (SHIFT) {
+      more[i] = __builtin_amdgcn_raw_buffer_load_b32(rows, (o & ~3u) + 16, 0, 0);
+      shift = (shift & ~(1u << i)) | (o >> 1 & 1u) << i;
+      o &= ~3u;
     }
+    held[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, o, 0, 0));
   }
   // ... and its write into the slice at `to`.
   __device__ __forceinline__ void put(int i, unsigned char* to, int wave, int lane) const {
-    *reinterpret_cast<u32x4*>(to + (i * NW + wave) * 1024 + lane * 16) = held[i];
+    u32x4 v = held[i];
+    if constexpr (SHIFT) {
+      const uint32_t by = (shift >> i & 1u) * 16;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = __builtin_amdgcn_alignbit(j < 3 ? held[i][j < 3 ? j + 1 : 0] : more[i], held[i][j], by);
+    }
+    if constexpr (!DIRECT && KMAJ) {
+      const int32_t held_left = left + BK;  // the slice held is the one before that aimed at
+      if (held_left < BK) {  // the last: nothing past the summed index's end
+        const int32_t room = (held_left - static_cast<int32_t>(column[i])) * bytes * 8;  // bits
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int32_t bits = room - 32 * j;
+          v[j] &= bits >= 32 ? ~0u : bits <= 0 ? 0u : (1u << bits) - 1u;
+        }
+      }
+    }
+    *reinterpret_cast<u32x4*>(to + (i * NW + wave) * 1024 + lane * 16) = v;
   }
 
   // The lane's fragment of the 32 free indices from `at`, 16 bytes of the summed
@@ -640,8 +646,8 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
     // s + 2 at once: a load has one slice's products to arrive.  All writes come
     // before the last step, which reads the next slice's first fragments.
     auto fetch = [&](int i) {
-      if (i < OpA::NL) oa.fetch(i < OpA::NL ? i : 0, wave, lane);
-      else ob.fetch(i < OpA::NL ? 0 : i - OpA::NL, wave, lane);
+      if (i < OpA::NL) oa.fetch(i < OpA::NL ? i : 0);
+      else ob.fetch(i < OpA::NL ? 0 : i - OpA::NL);
     };
     auto put = [&](int i, unsigned char* to) {
       if (i < OpA::NL) oa.put(i < OpA::NL ? i : 0, to, wave, lane);
@@ -832,7 +838,7 @@ hipError_t launch_product(const GroupedArgs& a, hipStream_t s) {
 
 using Large = Shape<256, 256, 2, 4, 2, 128>;
 using Medium = Shape<128, 128, 2, 2, 2, 128>;
-using Square = Shape<64, 64, 2, 2, 2, 128>;
+using Square = Shape<64, 64, 2, 2, 4, 128>;
 using Narrow = Shape<128, 32, 4, 1, 4, 128>;
 
 template <int ST, Product P>

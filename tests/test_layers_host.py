@@ -257,7 +257,7 @@ def _linear_back(**kw):
     ({"M": 0}, INVALID), ({"dtype": 3}, INVALID), ({"index": 2}, INVALID), ({"x": None}, INVALID),
     ({"w": None}, INVALID), ({"off": None}, INVALID), ({"off": A + 4}, INVALID), ({"x": A + 2}, INVALID),
     ({"w": A + 2}, INVALID), ({"xs": -4}, INVALID), ({"rows": 1 << 31}, UNSUPPORTED),
-    ({"K": 1 << 21}, UNSUPPORTED), ({"M": 1 << 21}, UNSUPPORTED), ({"groups": 1 << 17}, UNSUPPORTED),
+    ({"xs": 1 << 21}, UNSUPPORTED), ({"K": 1 << 21}, UNSUPPORTED), ({"M": 1 << 21}, UNSUPPORTED), ({"groups": 1 << 17}, UNSUPPORTED),
 ])
 def test_c_grouped_linear_refuses(kw, status):
     assert _linear(**kw) == status
