@@ -59,7 +59,7 @@ struct GroupedArgs {
 
 // How the weights' gradient is summed, from the call's sizes alone.
 struct GradWPlan {
-  bool large;         // 256 x 256 tiles, else 128 x 128
+  int tile;           // 256, 128 or 64 outputs on a side
   int64_t chunk;      // as above
   int64_t slots;
 };
@@ -67,17 +67,18 @@ inline GradWPlan plan_grad_w(int64_t rows, int64_t groups, int64_t K, int64_t M,
   const auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((K + t - 1) / t); };
   // Large tiles are a fifth faster, but need some for each CU: groups differ in
   // size, and the last round leaves CUs idle.  (16384 rows in 8 groups of very
-  // different sizes, 1024 x 4096, bf16: 512 large tiles 320 us, 2048 small ones 196.)
-  GradWPlan p{groups * tiles(256) >= 1024, 0, 0};
-  const int64_t t = tiles(128);
-  if (!p.large && groups * t < 512 && rows > 0) {
-    // too few tiles for the chip: chunks of rows, about one for each place
-    const int64_t least = dtype == TBE_F32 ? 128 : 256;
-    const int64_t want = (rows * t + 511) / 512;
-    p.chunk = std::max(least, (want + 63) / 64 * 64);
-    // a group of n > chunk rows has at most 2 n / chunk chunks
-    p.slots = rows > p.chunk ? 2 * rows / p.chunk : 0;
-  }
+  // different sizes, 1024 x 4096, bf16: 512 large tiles 320 us, 2048 small ones 170.)
+  if (groups * tiles(256) >= 1024) return {256, 0, 0};
+  if (groups * tiles(128) >= 512 || rows == 0) return {128, 0, 0};
+  // Too few tiles for the chip: chunks of rows, about one for each place.  Where
+  // those of 128 outputs would be short, 64: 8191 rows in 5 groups, 250 x 130, fp32,
+  // 148 chunk tiles of 128 25 us, 828 of 64 20 us.
+  GradWPlan p{rows * tiles(128) < 512 * 256 ? 64 : 128, 0, 0};
+  const int64_t places = p.tile == 64 ? 1024 : 512, least = dtype == TBE_F32 ? 128 : 256;
+  const int64_t want = (rows * tiles(p.tile) + places - 1) / places;
+  p.chunk = std::max(least, (want + 63) / 64 * 64);
+  // a group of n > chunk rows has at most 2 n / chunk chunks
+  p.slots = rows > p.chunk ? 2 * rows / p.chunk : 0;
   return p;
 }
 
@@ -136,38 +137,39 @@ __device__ __forceinline__ void band_order(int64_t q, int64_t na, int64_t nb, Ti
 }
 
 // Row tiles of TB rows, `na` tiles along the other index; false where the
-// workgroup has none.  Every wave works it out for itself: 64 groups at a time.
+// workgroup has none.  Every wave works it out for itself: 64 groups at a time,
+// and with no more than that from one read of the offsets.
 template <int TB>
 __device__ bool find_row_tile(const GroupedArgs& a, int64_t na, Tile* t) {
   const int lane = lane_id();
+  uint32_t lo = 0, rows = 0, tiles = 0, incl = 0;  // of the lane's group
+  const auto take = [&](int64_t g0) {
+    lo = rows = 0;
+    if (g0 + lane < a.groups) {
+      const int64_t first = group_offset(a, g0 + lane), n = group_offset(a, g0 + lane + 1) - first;
+      lo = static_cast<uint32_t>(first);
+      rows = n > 0 ? static_cast<uint32_t>(n) : 0u;
+    }
+    tiles = (rows + TB - 1) / TB;
+    incl = wave_inclusive_sum(tiles);
+  };
   int64_t total = 0;
   for (int64_t g0 = 0; g0 < a.groups; g0 += 64) {
-    int64_t n = 0;
-    if (g0 + lane < a.groups) {
-      n = group_offset(a, g0 + lane + 1) - group_offset(a, g0 + lane);
-      n = n > 0 ? (n + TB - 1) / TB : 0;
-    }
-    total += __builtin_amdgcn_readlane(wave_inclusive_sum(static_cast<uint32_t>(n)), 63);
+    take(g0);
+    total += __builtin_amdgcn_readlane(incl, 63);
   }
   total *= na;
   if (static_cast<int64_t>(blockIdx.x) >= total) return false;
   int64_t q = xcd_contiguous_block(static_cast<int>(blockIdx.x), static_cast<int>(total));
   for (int64_t g0 = 0; g0 < a.groups; g0 += 64) {
-    int64_t lo = 0, n = 0;
-    if (g0 + lane < a.groups) {
-      lo = group_offset(a, g0 + lane);
-      n = group_offset(a, g0 + lane + 1) - lo;
-      n = n > 0 ? n : 0;
-    }
-    const uint32_t tiles = static_cast<uint32_t>((n + TB - 1) / TB);
-    const uint32_t incl = wave_inclusive_sum(tiles);
+    if (a.groups > 64) take(g0);
     const uint64_t past = __ballot(static_cast<int64_t>(incl) * na > q);
     if (past) {
       const int l = __builtin_ctzll(past);
       const int64_t before = __builtin_amdgcn_readlane(incl - tiles, l);
       t->group = g0 + l;
-      t->first = static_cast<int64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(lo), l));
-      t->end = t->first + __builtin_amdgcn_readlane(static_cast<uint32_t>(n), l);
+      t->first = __builtin_amdgcn_readlane(lo, l);
+      t->end = t->first + __builtin_amdgcn_readlane(rows, l);
       band_order(q - before * na, na, __builtin_amdgcn_readlane(tiles, l), t);
       return true;
     }
@@ -775,6 +777,7 @@ __global__ __launch_bounds__(kBlock) void grouped_join(GroupedArgs a, int64_t bl
   if (e0 < all) {
     f32x4 sum = {};
     const int n = all - e0 < 4 ? static_cast<int>(all - e0) : 4;
+#pragma unroll 8
     for (int64_t c = 0; c < mine; ++c) {
       const float* p = a.parts + (slot + c) * all + e0;
       if (n == 4) {
@@ -789,6 +792,7 @@ __global__ __launch_bounds__(kBlock) void grouped_join(GroupedArgs a, int64_t bl
     const int64_t m = block * kBlock + threadIdx.x;
     if (m < a.M) {
       float sum = 0.0f;
+#pragma unroll 8
       for (int64_t c = 0; c < mine; ++c) sum += a.bias_parts[(slot + c) * a.M + m];
       store_one<ST>(a.db, g * a.M + m, sum);
     }
@@ -853,8 +857,9 @@ hipError_t launch_rows(const GroupedArgs& a, hipStream_t s) {
 
 template <int ST>
 hipError_t launch_grad_w(const GroupedArgs& a, const GradWPlan& plan, hipStream_t s) {
-  hipError_t e = plan.large ? launch_product<ST, kGradW, Large>(a, s)
-                            : launch_product<ST, kGradW, Medium>(a, s);
+  hipError_t e = plan.tile == 256   ? launch_product<ST, kGradW, Large>(a, s)
+                 : plan.tile == 128 ? launch_product<ST, kGradW, Medium>(a, s)
+                                    : launch_product<ST, kGradW, Square>(a, s);
   if (e != hipSuccess || plan.slots == 0) return e;
   const int64_t blocks = ceil_div(std::max(ceil_div(a.M * a.K, 4), a.M), kBlock);
   hipLaunchKernelGGL((grouped_join<ST>), dim3(static_cast<unsigned>(blocks * a.groups)), dim3(kBlock),
