@@ -23,25 +23,31 @@ struct Gates {
 };
 
 // sigmoid(g) and sigmoid(-g) from one exponential of -|g|: neither overflows
-// nor loses the smaller one to cancellation.  exp(-|g|) = 2^t (1 + r ln 2) with
-// t + r = -|g| log2 e, r what the product's rounding left out; the reciprocal
-// gets one Newton step.  Both are good to some 2^-23 relative; expf and two
-// divisions cost three times as much and made the backward pass wait for them.
-template <bool SIGMOID>
+// nor loses the smaller one to cancellation.  exp(-|g|) = 2^t (1 + r) with
+// t + r / ln 2 = -|g| log2 e, r what t leaves out.  bf16 gates have 8 bits, so t
+// is exact with a log2 e of 16; others take the product's rounding back with two
+// fused operations.  The reciprocal is the hardware's, good to a step of 2^-23,
+// as is the exponential.
+template <int ST, bool SIGMOID>
 __device__ __forceinline__ Gates gates(float g) {
   if constexpr (!SIGMOID) return {g, 1.0f};
-  constexpr double kLog2e = 1.4426950408889634074;
-  constexpr float kHigh = static_cast<float>(kLog2e);
-  constexpr float kLow = static_cast<float>(kLog2e - static_cast<double>(kHigh));
-  const float m = fabsf(g) > 128.0f ? -128.0f : -fabsf(g);  // infinities stay out of r, NaN passes
-  const float t = m * kHigh;
-  const float r = fmaf(m, kLow, fmaf(m, kHigh, -t));
+  constexpr double kLog2e = 1.4426950408889634074, kLn2 = 0.69314718055994530942;
+  // infinities stay out of r, NaN passes
+  const float m = __builtin_elementwise_maximum(-fabsf(g), -128.0f);
+  float t, r;
+  if constexpr (ST == kBF16) {
+    constexpr float kHigh = 47274.0f / 32768.0f;
+    t = m * kHigh;
+    r = m * static_cast<float>((kLog2e - static_cast<double>(kHigh)) * kLn2);
+  } else {
+    constexpr float kHigh = static_cast<float>(kLog2e);
+    constexpr float kLow = static_cast<float>(kLog2e - static_cast<double>(kHigh));
+    t = m * kHigh;
+    r = fmaf(m, kLow, fmaf(m, kHigh, -t)) * static_cast<float>(kLn2);
+  }
   const float p = __builtin_amdgcn_exp2f(t);
-  const float z = fmaf(p, r * 0.69314718f, p);
-  const float d = 1.0f + z;
-  float hi = __builtin_amdgcn_rcpf(d);
-  hi = fmaf(fmaf(-d, hi, 1.0f), hi, hi);
-  const float lo = z * hi;
+  const float z = fmaf(p, r, p);
+  const float hi = __builtin_amdgcn_rcpf(1.0f + z), lo = z * hi;
   return g >= 0.0f ? Gates{hi, lo} : Gates{lo, hi};
 }
 
@@ -66,7 +72,7 @@ __global__ __launch_bounds__(kBlock) void step_kernel(const void* x, int64_t x_s
     StoredVec<ST, 4> hv;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const Gates t = gates<SIGMOID>(static_cast<float>(gv[k]));
+      const Gates t = gates<ST, SIGMOID>(static_cast<float>(gv[k]));
       v[k] = t.a * v[k] + t.b * static_cast<float>(xv[k]);
       hv[k] = static_cast<typename Stored<ST>::type>(v[k]);
     }
@@ -75,7 +81,7 @@ __global__ __launch_bounds__(kBlock) void step_kernel(const void* x, int64_t x_s
     return;
   }
   for (int k = 0; c + k < dim; ++k) {
-    const Gates t = gates<SIGMOID>(load_one<ST>(gate, s * gate_stride + c + k));
+    const Gates t = gates<ST, SIGMOID>(load_one<ST>(gate, s * gate_stride + c + k));
     const float v0 = state ? state[s * state_stride + c + k] : 0.0f;
     const float v = t.a * v0 + t.b * load_one<ST>(x, s * x_stride + c + k);
     next[out + k] = v;
@@ -301,13 +307,13 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
   const int64_t k = STEP > 0 ? tile : w.tiles - 1 - tile, group = k / kGroup;
   const int in_group = static_cast<int>(k % kGroup);
   const bool first = k == 0, last = in_group == kGroup - 1;
-  // the tile's pair: wave by wave in scan order
+  // the tile's pair, which the first wave publishes: wave by wave in scan order
   float A[V], B[V];
   bool reset = first;
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
 #pragma unroll 2
-  for (int q = 0; q < W; ++q) {
+  for (int q = 0; q < (wave == 0 ? W : 0); ++q) {
     const int i = STEP > 0 ? q : W - 1 - q;
     const bool r = sh.resets[i] != 0u;
     reset |= r;
@@ -599,24 +605,41 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
   const uint32_t first = static_cast<uint32_t>(__ballot(starts >= 0));
   const uint32_t last = static_cast<uint32_t>(__ballot(ends >= 0));
   // state_i = first ? u_i : k_i state_{i-1} + u_i, the state before a first token being in its u
-  float k[T][V], u[T][V], A[V], B[V], init[4][V];
+  float k[T][V], u[T][V], A[V], B[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+  // A span in the middle of a sequence, T tokens long, has nothing to choose.
+  const bool plain = first == 0u && tokens == T;
+  if (plain) {
 #pragma unroll
-  for (int i = 0; i < T; ++i) {
-    const bool f = first >> i & 1u;
-    if (i % 4 == 0)  // initial states of four tokens at a time: few spans have more starts
-      load_marked<V, 4>(a.initial, a.initial_stride, first >> i & 15u, starts, i, c, a.dim, at32, init);
+    for (int i = 0; i < T; ++i)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const Gates t = gates<SIGMOID>(static_cast<float>(g[i][v]));
-      const bool in = i < tokens;
-      k[i][v] = in ? t.a : 1.0f;
-      const float in_x = t.b * static_cast<float>(x[i][v]);
-      u[i][v] = f ? fmaf(t.a, init[i % 4][v], in_x) : in ? in_x : 0.0f;
-      settle(k[i][v]), settle(u[i][v]);
-      B[v] = f ? u[i][v] : fmaf(k[i][v], B[v], u[i][v]);
-      A[v] *= k[i][v];
+      for (int v = 0; v < V; ++v) {
+        const Gates t = gates<ST, SIGMOID>(static_cast<float>(g[i][v]));
+        k[i][v] = t.a;
+        u[i][v] = t.b * static_cast<float>(x[i][v]);
+        settle(k[i][v]), settle(u[i][v]);
+        B[v] = fmaf(k[i][v], B[v], u[i][v]);
+        A[v] *= k[i][v];
+      }
+  } else {
+    float init[4][V];
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      const bool f = first >> i & 1u;
+      if (i % 4 == 0)  // initial states of four tokens at a time: few spans have more starts
+        load_marked<V, 4>(a.initial, a.initial_stride, first >> i & 15u, starts, i, c, a.dim, at32, init);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Gates t = gates<ST, SIGMOID>(static_cast<float>(g[i][v]));
+        const bool in = i < tokens;
+        k[i][v] = in ? t.a : 1.0f;
+        const float in_x = t.b * static_cast<float>(x[i][v]);
+        u[i][v] = f ? fmaf(t.a, init[i % 4][v], in_x) : in ? in_x : 0.0f;
+        settle(k[i][v]), settle(u[i][v]);
+        B[v] = f ? u[i][v] : fmaf(k[i][v], B[v], u[i][v]);
+        A[v] *= k[i][v];
+      }
     }
   }
 #pragma unroll
@@ -636,7 +659,7 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
       if (!mine) continue;
       v[q] = a.initial ? a.initial[s * a.initial_stride + c0 + q] : 0.0f;
       for (int64_t t = offset_at(a, s); t < end; ++t) {
-        const Gates n = gates<SIGMOID>(load_one<ST>(a.gate, t * a.gate_stride + c0 + q));
+        const Gates n = gates<ST, SIGMOID>(load_one<ST>(a.gate, t * a.gate_stride + c0 + q));
         v[q] = fmaf(n.a, v[q], n.b * load_one<ST>(a.x, t * a.x_stride + c0 + q));
       }
     }
@@ -646,6 +669,17 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
                                          a.dim);
   const Buffer h = span_buffer<ST>(a.h, a.dim, t0, tokens, c, a.dim);
   const uint32_t step = static_cast<uint32_t>(a.dim) * bytes;
+  if (plain && last == 0u) {
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      if (i % kCarry == 0 && a.carry)
+        store_row<kF32, V>(carry, at32 + i / kCarry * static_cast<uint32_t>(a.dim) * 4, state);
+#pragma unroll
+      for (int v = 0; v < V; ++v) state[v] = fmaf(k[i][v], state[v], u[i][v]);
+      store_row<ST, V>(h, at + i * step, state);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < T; ++i) {
     const bool f = first >> i & 1u;
@@ -697,33 +731,58 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
   // lam_i = up_i + (last ? 0 : mu_{i+1}), mu_i = a_i lam_i, the gradient of a final
   // state being in its up; dgate_i = q_i lam_i with q_i of the state before token i
   float ka[T][V], kb[T][V], q[T][V], up[T][V], A[V], B[V];
-  load_marked<V, T>(a.initial, a.initial_stride, first, starts, 0, c, a.dim, at32, q);
-  load_marked<V, T>(a.grad_final, a.grad_final_stride, last, ends, 0, c, a.dim, at32, up);
-#pragma unroll
-  for (int i = 0; i < T; ++i) {
-    const bool f = first >> i & 1u;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const Gates t = gates<SIGMOID>(static_cast<float>(g[i][v]));
-      const bool in = i < tokens;
-      ka[i][v] = in ? t.a : 1.0f;
-      kb[i][v] = t.b;
-      const float before = f ? q[i][v] : state[v], xi = static_cast<float>(x[i][v]);
-      state[v] = fmaf(t.a, before, t.b * xi);  // as the forward pass rounds it
-      q[i][v] = SIGMOID ? (before - xi) * (t.a * t.b) : before;
-      up[i][v] += static_cast<float>(dh[i][v]);
-      settle(ka[i][v]), settle(kb[i][v]), settle(q[i][v]), settle(up[i][v]);
-    }
-  }
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+  // A span in the middle of a sequence, T tokens long, has nothing to choose.
+  const bool plain = (first | last) == 0u && tokens == T;
+  if (plain) {
 #pragma unroll
-  for (int i = T - 1; i >= 0; --i) {
-    const bool l = last >> i & 1u;
+    for (int i = 0; i < T; ++i)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      B[v] = ka[i][v] * (l ? up[i][v] : up[i][v] + B[v]);
-      A[v] *= ka[i][v];
+      for (int v = 0; v < V; ++v) {
+        const Gates t = gates<ST, SIGMOID>(static_cast<float>(g[i][v]));
+        ka[i][v] = t.a;
+        kb[i][v] = t.b;
+        const float before = state[v], xi = static_cast<float>(x[i][v]);
+        state[v] = fmaf(t.a, before, t.b * xi);  // as the forward pass rounds it
+        q[i][v] = SIGMOID ? (before - xi) * (t.a * t.b) : before;
+        up[i][v] = static_cast<float>(dh[i][v]);
+        settle(ka[i][v]), settle(kb[i][v]), settle(q[i][v]), settle(up[i][v]);
+      }
+#pragma unroll
+    for (int i = T - 1; i >= 0; --i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        B[v] = ka[i][v] * (up[i][v] + B[v]);
+        A[v] *= ka[i][v];
+      }
+  } else {
+    load_marked<V, T>(a.initial, a.initial_stride, first, starts, 0, c, a.dim, at32, q);
+    load_marked<V, T>(a.grad_final, a.grad_final_stride, last, ends, 0, c, a.dim, at32, up);
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      const bool f = first >> i & 1u;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Gates t = gates<ST, SIGMOID>(static_cast<float>(g[i][v]));
+        const bool in = i < tokens;
+        ka[i][v] = in ? t.a : 1.0f;
+        kb[i][v] = t.b;
+        const float before = f ? q[i][v] : state[v], xi = static_cast<float>(x[i][v]);
+        state[v] = fmaf(t.a, before, t.b * xi);  // as the forward pass rounds it
+        q[i][v] = SIGMOID ? (before - xi) * (t.a * t.b) : before;
+        up[i][v] += static_cast<float>(dh[i][v]);
+        settle(ka[i][v]), settle(kb[i][v]), settle(q[i][v]), settle(up[i][v]);
+      }
+    }
+#pragma unroll
+    for (int i = T - 1; i >= 0; --i) {
+      const bool l = last >> i & 1u;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        B[v] = ka[i][v] * (l ? up[i][v] : up[i][v] + B[v]);
+        A[v] *= ka[i][v];
+      }
     }
   }
 #pragma unroll
@@ -745,7 +804,7 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
       v[q] = a.grad_final ? a.grad_final[s * a.grad_final_stride + c0 + q] : 0.0f;
       for (int64_t t = offset_at(a, s + 1) - 1; t >= begin; --t) {
         const float up = a.grad_h ? load_one<ST>(a.grad_h, t * a.grad_h_stride + c0 + q) : 0.0f;
-        v[q] = gates<SIGMOID>(load_one<ST>(a.gate, t * a.gate_stride + c0 + q)).a * (up + v[q]);
+        v[q] = gates<ST, SIGMOID>(load_one<ST>(a.gate, t * a.gate_stride + c0 + q)).a * (up + v[q]);
       }
     }
   });
@@ -754,6 +813,22 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
   const Buffer dgs = span_buffer<ST>(a.dgate, a.dgate_stride, t0, tokens, c, a.dim);
   const uint32_t dx_step = static_cast<uint32_t>(a.dx_stride) * bytes;
   const uint32_t dg_step = static_cast<uint32_t>(a.dgate_stride) * bytes;
+  if (plain) {
+#pragma unroll
+    for (int i = T - 1; i >= 0; --i) {
+      float dx[V], dg[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float lam = up[i][v] + mu[v];
+        dx[v] = kb[i][v] * lam;
+        dg[v] = lam * q[i][v];
+        mu[v] = ka[i][v] * lam;
+      }
+      store_row<ST, V>(dxs, at + i * dx_step, dx);
+      store_row<ST, V>(dgs, at + i * dg_step, dg);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = T - 1; i >= 0; --i) {
     const bool l = last >> i & 1u;
