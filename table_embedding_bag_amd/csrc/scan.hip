@@ -161,7 +161,7 @@ struct ScanWork {
   Published tile;    // [tiles, dim]: a pair or a state
   Published group;   // [groups, dim]: a pair, then a state
   int64_t tiles, rows;  // rows: of all published ones, tiles first
-  int32_t channel_blocks;
+  uint32_t channel_blocks;
   uint32_t max_polls;
 };
 
@@ -582,13 +582,25 @@ __device__ __forceinline__ void store_row(Buffer rows, uint32_t off, const float
   RowWord<ST, V>::store(__builtin_bit_cast(typename RowWord<ST, V>::type, o), rows, off);
 }
 
+// Which tile (in scan order) and channels a workgroup takes.  Workgroups go round
+// robin to the XCDs: an XCD takes all the channels of each eighth tile.
+struct Place {
+  int64_t tile;
+  uint32_t channels;
+};
+__device__ __forceinline__ Place place_of(const ScanWork& w) {
+  const uint32_t eight = blockIdx.x / 8, row = eight / w.channel_blocks;
+  return {static_cast<int64_t>(row) * 8 + blockIdx.x % 8, eight - row * w.channel_blocks};
+}
+
 template <int ST, int V, bool SIGMOID, int W, int T>
 __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) {
   __shared__ TileShared<V, W, T> sh;
-  const uint32_t order = blockIdx.x;
-  const int64_t tile = order / w.channel_blocks;
+  const Place place = place_of(w);
+  if (place.tile >= w.tiles) return;
+  const int64_t tile = place.tile;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c = static_cast<int64_t>(order % w.channel_blocks) * (64 * V), c0 = c + lane * V;
+  const int64_t c = static_cast<int64_t>(place.channels) * (64 * V), c0 = c + lane * V;
   const bool mine = c0 < a.dim;  // V divides dim
   constexpr int bytes = StorageTraits<ST>::bytes;
   const uint32_t at = mine ? lane * V * bytes : kOutside, at32 = mine ? lane * V * 4 : kOutside;
@@ -698,10 +710,11 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
 template <int ST, int V, bool SIGMOID, int W, int T>
 __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWork w) {
   __shared__ TileShared<V, W, T> sh;
-  const uint32_t order = blockIdx.x;
-  const int64_t tile = w.tiles - 1 - order / w.channel_blocks;
+  const Place place = place_of(w);
+  if (place.tile >= w.tiles) return;
+  const int64_t tile = w.tiles - 1 - place.tile;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c = static_cast<int64_t>(order % w.channel_blocks) * (64 * V), c0 = c + lane * V;
+  const int64_t c = static_cast<int64_t>(place.channels) * (64 * V), c0 = c + lane * V;
   const bool mine = c0 < a.dim;  // V divides dim
   constexpr int bytes = StorageTraits<ST>::bytes;
   const uint32_t at = mine ? lane * V * bytes : kOutside, at32 = mine ? lane * V * 4 : kOutside;
@@ -861,7 +874,7 @@ int waves_of(int64_t tokens, int64_t seqs) { return tokens < seqs * 256 ? kFewWa
 
 template <int ST, int V, bool SIGMOID, int W>
 hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, bool back, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(w.tiles * w.channel_blocks));
+  const dim3 grid(static_cast<unsigned>((w.tiles + 7) / 8 * 8 * w.channel_blocks));
   if (back)
     hipLaunchKernelGGL((scan_tiles_back<ST, V, SIGMOID, W, kBackSpan>), grid, dim3(64 * W), 0, s, a,
                        w);
@@ -919,7 +932,7 @@ hipError_t launch_scan(ScanArgs a, const tbe_scan_input* in, bool back, void* wo
   ScanWork w{};
   w.tiles = tiles_of(a.tokens, a.seqs, back);
   const int v = lane_channels(in, a);
-  w.channel_blocks = static_cast<int32_t>((a.dim + 64 * v - 1) / (64 * v));
+  w.channel_blocks = static_cast<uint32_t>((a.dim + 64 * v - 1) / (64 * v));
   w.rows = w.tiles + groups_of(w.tiles);
   char* p = static_cast<char*>(workspace);
   w.marks = reinterpret_cast<int2*>(p);
@@ -956,8 +969,9 @@ tbe_status check_sizes(int64_t tokens, int64_t seqs, int64_t dim, int32_t dtype)
   if (tokens < 0 || seqs < 0 || dim < 1 || !known_dtype(dtype)) return TBE_ERR_INVALID_ARGUMENT;
   if (seqs == 0 && tokens > 0) return TBE_ERR_INVALID_ARGUMENT;
   if (tokens >= kMax || seqs >= kMax || dim > kMaxRow) return TBE_ERR_UNSUPPORTED;
-  // 512 threads for 64 tokens of 64 channels at most
-  if ((tokens + 63) / 64 * ((dim + 63) / 64) >= (int64_t{1} << 23)) return TBE_ERR_UNSUPPORTED;
+  // 512 threads for 64 tokens of 64 channels at most, tiles rounded up to 8
+  if ((tokens + 511) / 512 * 8 * ((dim + 63) / 64) >= (int64_t{1} << 23))
+    return TBE_ERR_UNSUPPORTED;
   return TBE_OK;
 }
 
