@@ -248,7 +248,8 @@ __device__ int64_t ranked_group(const GroupedArgs& a, int64_t r) {
 // One operand of a tile: where its chunks come from and which exist.
 //   KMAJ: `free` rows of the tile at base + r * stride, the summed index along them.
 //   else: rows of the summed index at base + k * stride, `free` columns along them.
-template <int ST, bool KMAJ, int R, int NW, bool DIRECT, int RB>
+//   AHEAD slices are held in registers where they come that way.
+template <int ST, bool KMAJ, int R, int NW, bool DIRECT, int RB, int AHEAD>
 struct Operand {
   static constexpr int bytes = StorageTraits<ST>::bytes;
   static constexpr int EL = 16 / bytes;            // values in a chunk
@@ -264,10 +265,10 @@ struct Operand {
   int32_t free, depth;       // bounds of the free index from the tile's start, of the summed one
   uint32_t off[NL];
   uint32_t column[NL];
-  u32x4 held[NL];
-  uint32_t more[SHIFT ? NL : 1];  // the word after
+  u32x4 held[AHEAD][NL];
+  uint32_t more[AHEAD][SHIFT ? NL : 1];  // the word after
   uint32_t skew;                  // bytes from the aligned word before base to base
-  uint32_t shift = 0;             // bit i: the chunk held starts between words
+  uint32_t shift[AHEAD] = {};     // bit i: the chunk held starts between words
   const char* from;  // the slice aimed at
   uint32_t records;
   int32_t left;
@@ -325,29 +326,31 @@ struct Operand {
                 lds + (i * NW + wave) * 1024);
   }
 
-  // Through registers: the load of the i-th chunk of the slice aimed at, ...
-  __device__ __forceinline__ void fetch(int i) {
+  // Through registers: the load of the i-th chunk of the slice aimed at into the
+  // slice held at h, ...
+  __device__ __forceinline__ void fetch(int i, int h) {
     const auto rows = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0,
                                                         static_cast<int>(records), kBufferFlags);
     uint32_t o = static_cast<int32_t>(column[i]) < left ? off[i] : kOutside;
     if constexpr (SHIFT) {
-      more[i] = __builtin_amdgcn_raw_buffer_load_b32(rows, (o & ~3u) + 16, 0, 0);
-      shift = (shift & ~(1u << i)) | (o >> 1 & 1u) << i;
+      more[h][i] = __builtin_amdgcn_raw_buffer_load_b32(rows, (o & ~3u) + 16, 0, 0);
+      shift[h] = (shift[h] & ~(1u << i)) | (o >> 1 & 1u) << i;
       o &= ~3u;
     }
-    held[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, o, 0, 0));
+    held[h][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, o, 0, 0));
   }
-  // ... and its write into the slice at `to`.
-  __device__ __forceinline__ void put(int i, unsigned char* to, int wave, int lane) const {
-    u32x4 v = held[i];
+  // ... and its write into the slice at `to`, when the slice AHEAD after it is aimed at.
+  __device__ __forceinline__ void put(int i, int h, unsigned char* to, int wave, int lane) const {
+    u32x4 v = held[h][i];
     if constexpr (SHIFT) {
-      const uint32_t by = (shift >> i & 1u) * 16;
+      const uint32_t by = (shift[h] >> i & 1u) * 16;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        v[j] = __builtin_amdgcn_alignbit(j < 3 ? held[i][j < 3 ? j + 1 : 0] : more[i], held[i][j], by);
+        v[j] = __builtin_amdgcn_alignbit(j < 3 ? held[h][i][j < 3 ? j + 1 : 0] : more[h][i],
+                                         held[h][i][j], by);
     }
     if constexpr (!DIRECT && KMAJ) {
-      const int32_t held_left = left + BK;  // the slice held is the one before that aimed at
+      const int32_t held_left = left + AHEAD * BK;
       if (held_left < BK) {  // the last: nothing past the summed index's end
         const int32_t room = (held_left - static_cast<int32_t>(column[i])) * bytes * 8;  // bits
 #pragma unroll
@@ -489,11 +492,15 @@ __device__ __forceinline__ void wait_loads() {
 template <int ST, Product P, typename S, bool DIRECT>
 __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
   constexpr bool kAKmaj = P == kForward, kBKmaj = P != kGradW;
-  using OpA = Operand<ST, kAKmaj, S::TA, S::NW, DIRECT, S::RB>;
-  using OpB = Operand<ST, kBKmaj, S::TB, S::NW, DIRECT, S::RB>;
+  // Slices past LDS's two in registers: one where a slice's products take long enough
+  // for a load to arrive, three where tiles are small.
+  constexpr bool kThroughLds = DIRECT && S::NS > 2;
+  constexpr int kAhead = !kThroughLds && S::NS > 2 ? 3 : 1, kBuffers = kThroughLds ? S::NS : 2;
+  using OpA = Operand<ST, kAKmaj, S::TA, S::NW, DIRECT, S::RB, kAhead>;
+  using OpB = Operand<ST, kBKmaj, S::TB, S::NW, DIRECT, S::RB, kAhead>;
   constexpr int BK = OpA::BK, KK = S::RB / 32;  // of a slice: values, steps of 32 bytes
   constexpr int bytes = StorageTraits<ST>::bytes;
-  __shared__ __align__(1024) unsigned char lds[S::NS * S::stage];
+  __shared__ __align__(1024) unsigned char lds[kBuffers * S::stage];
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t cols = P == kForward ? a.M : a.K;      // of the output: A's free index
@@ -592,7 +599,7 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
     if constexpr (P == kGradW && p == n - 1)
       if (sums) add_columns(fb[kk & 1]);
   };
-  if constexpr (DIRECT && S::NS > 2) {
+  if constexpr (kThroughLds) {
     // Of the NS buffers one is read, NS - 2 are in flight and one, read before, is
     // being filled; slices past the end load nothing, but count.  A step's loads,
     // the reads of the next step's fragments and its products take turns: loads all
@@ -645,35 +652,39 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
   } else {
     // While slice s is read from its buffer, the registers' slice s + 1 goes into the
     // other one, chunk by chunk, and each chunk's register takes its load of slice
-    // s + 2 at once: a load has one slice's products to arrive.  All writes come
-    // before the last step, which reads the next slice's first fragments.
-    auto fetch = [&](int i) {
-      if (i < OpA::NL) oa.fetch(i < OpA::NL ? i : 0);
-      else ob.fetch(i < OpA::NL ? 0 : i - OpA::NL);
+    // s + 1 + kAhead at once: a load has kAhead slices' products to arrive.  All writes
+    // come before the last step, which reads the next slice's first fragments.
+    auto fetch = [&](int i, int h) {
+      if (i < OpA::NL) oa.fetch(i < OpA::NL ? i : 0, h);
+      else ob.fetch(i < OpA::NL ? 0 : i - OpA::NL, h);
     };
-    auto put = [&](int i, unsigned char* to) {
-      if (i < OpA::NL) oa.put(i < OpA::NL ? i : 0, to, wave, lane);
-      else ob.put(i < OpA::NL ? 0 : i - OpA::NL, to + S::TA * S::RB, wave, lane);
+    auto put = [&](int i, int h, unsigned char* to) {
+      if (i < OpA::NL) oa.put(i < OpA::NL ? i : 0, h, to, wave, lane);
+      else ob.put(i < OpA::NL ? 0 : i - OpA::NL, h, to + S::TA * S::RB, wave, lane);
     };
-    oa.aim(0);
-    ob.aim(0);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) fetch(i);
-    oa.aim(BK);
-    ob.aim(BK);
+    for (int h = 0; h < kAhead; ++h) {
+      oa.aim(h * BK);
+      ob.aim(h * BK);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) fetch(i, h);
+    }
+    oa.aim(kAhead * BK);
+    ob.aim(kAhead * BK);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      put(i, lds);
-      fetch(i);
+      put(i, 0, lds);
+      fetch(i, 0);
     }
     __syncthreads();
 #pragma unroll
     for (int f = 0; f < kFragments; ++f) read(lds, 0, f, fa[0], fb[0]);
-    for (int32_t s = 0; s < slices; ++s) {
+    auto slice = [&](int32_t s, auto h_) {
+      constexpr int h = h_;
       const unsigned char* at = lds + (s & 1) * S::stage;
       unsigned char* next = lds + ((s + 1) & 1) * S::stage;
-      oa.aim((s + 2) * BK);
-      ob.aim((s + 2) * BK);
+      oa.aim((s + 1 + kAhead) * BK);
+      ob.aim((s + 1 + kAhead) * BK);
       repeat<0, KK>([&](auto kk_) {
         constexpr int kk = kk_;
         constexpr int kFrom = kk == KK - 1 ? kLoads : kk * kLoads / (KK - 1);
@@ -686,13 +697,18 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
         }
         repeat<0, kParts>([&](auto p_) {
           if constexpr (kFrom + p_ < kTo) {
-            put(kFrom + p_, next);
-            fetch(kFrom + p_);
+            put(kFrom + p_, h, next);
+            fetch(kFrom + p_, h);
           }
           part(p_, std::integral_constant<int, kParts>{}, kk_, kk == KK - 1 ? next : at);
         });
       });
-    }
+    };
+    for (int32_t s = 0; s < slices; s += kAhead)
+      repeat<0, kAhead>([&](auto r_) {
+        constexpr int r = r_;
+        if (r == 0 || s + r < slices) slice(s + r, std::integral_constant<int, (r + 1) % kAhead>{});
+      });
   }
 
 #pragma unroll
@@ -777,16 +793,19 @@ __global__ __launch_bounds__(kBlock) void grouped_join(GroupedArgs a, int64_t bl
   if (e0 < all) {
     f32x4 sum = {};
     const int n = all - e0 < 4 ? static_cast<int>(all - e0) : 4;
+    const float* p = a.parts + slot * all + e0;
+    if (n == 4) {
 #pragma unroll 8
-    for (int64_t c = 0; c < mine; ++c) {
-      const float* p = a.parts + (slot + c) * all + e0;
-      if (n == 4) {
-        sum += load_vec<kF32, 4>(p, 0);
-      } else {
-        for (int j = 0; j < n; ++j) sum[j] += p[j];
-      }
+      for (int64_t c = 0; c < mine; ++c) sum += load_vec<kF32, 4>(p, c * all);
+      StoredVec<ST, 4> out;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out[j] = static_cast<typename Stored<ST>::type>(sum[j]);
+      store_vec<ST, 4>(a.dw, g * all + e0, out);
+    } else {
+      for (int64_t c = 0; c < mine; ++c)
+        for (int j = 0; j < n; ++j) sum[j] += p[c * all + j];
+      for (int j = 0; j < n; ++j) store_one<ST>(a.dw, g * all + e0 + j, sum[j]);
     }
-    for (int j = 0; j < n; ++j) store_one<ST>(a.dw, g * all + e0 + j, sum[j]);
   }
   if (a.db) {
     const int64_t m = block * kBlock + threadIdx.x;
