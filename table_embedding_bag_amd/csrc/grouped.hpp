@@ -140,7 +140,7 @@ __device__ __forceinline__ void band_order(int64_t q, int64_t na, int64_t nb, Ti
 // workgroup has none.  Every wave works it out for itself: 64 groups at a time,
 // and with no more than that from one read of the offsets.
 template <int TB>
-__device__ bool find_row_tile(const GroupedArgs& a, int64_t na, Tile* t) {
+__device__ bool find_row_tile(const GroupedArgs& a, uint32_t id, int64_t na, Tile* t) {
   const int lane = lane_id();
   uint32_t lo = 0, rows = 0, tiles = 0, incl = 0;  // of the lane's group
   const auto take = [&](int64_t g0) {
@@ -159,8 +159,8 @@ __device__ bool find_row_tile(const GroupedArgs& a, int64_t na, Tile* t) {
     total += __builtin_amdgcn_readlane(incl, 63);
   }
   total *= na;
-  if (static_cast<int64_t>(blockIdx.x) >= total) return false;
-  int64_t q = xcd_contiguous_block(static_cast<int>(blockIdx.x), static_cast<int>(total));
+  if (static_cast<int64_t>(id) >= total) return false;
+  int64_t q = xcd_contiguous_block(static_cast<int>(id), static_cast<int>(total));
   for (int64_t g0 = 0; g0 < a.groups; g0 += 64) {
     if (a.groups > 64) take(g0);
     const uint64_t past = __ballot(static_cast<int64_t>(incl) * na > q);
@@ -489,18 +489,22 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// LDS's buffers: for slices that come by registers two.
+template <typename S, bool DIRECT>
+constexpr int kLdsBytes = (DIRECT && S::NS > 2 ? S::NS : 2) * S::stage;
+
+// Tile `id` of a product.
 template <int ST, Product P, typename S, bool DIRECT>
-__global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
+__device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, unsigned char* lds) {
   constexpr bool kAKmaj = P == kForward, kBKmaj = P != kGradW;
   // Slices past LDS's two in registers: one where a slice's products take long enough
   // for a load to arrive, three where tiles are small.
   constexpr bool kThroughLds = DIRECT && S::NS > 2;
-  constexpr int kAhead = !kThroughLds && S::NS > 2 ? 3 : 1, kBuffers = kThroughLds ? S::NS : 2;
+  constexpr int kAhead = !kThroughLds && S::NS > 2 ? 3 : 1;
   using OpA = Operand<ST, kAKmaj, S::TA, S::NW, DIRECT, S::RB, kAhead>;
   using OpB = Operand<ST, kBKmaj, S::TB, S::NW, DIRECT, S::RB, kAhead>;
   constexpr int BK = OpA::BK, KK = S::RB / 32;  // of a slice: values, steps of 32 bytes
   constexpr int bytes = StorageTraits<ST>::bytes;
-  __shared__ __align__(1024) unsigned char lds[kBuffers * S::stage];
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t cols = P == kForward ? a.M : a.K;      // of the output: A's free index
@@ -511,8 +515,8 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
     // A group's (or chunk's) tiles spread over all XCDs, each taking a contiguous
     // part of them; groups with the most rows come first, so that short ones fill
     // the gaps at the end.
-    const int64_t nb = (a.M + S::TB - 1) / S::TB, tiles = na * nb, unit = blockIdx.x / tiles;
-    const int64_t q = xcd_contiguous_block(static_cast<int>(blockIdx.x - unit * tiles),
+    const int64_t nb = (a.M + S::TB - 1) / S::TB, tiles = na * nb, unit = id / tiles;
+    const int64_t q = xcd_contiguous_block(static_cast<int>(id - unit * tiles),
                                            static_cast<int>(tiles));
     if (a.chunk) {
       Unit u;
@@ -527,7 +531,7 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
     }
     band_order(q, na, nb, &t);
   } else {
-    if (!find_row_tile<S::TB>(a, na, &t)) return;
+    if (!find_row_tile<S::TB>(a, id, na, &t)) return;
   }
   const int64_t a0 = t.ta * S::TA, b0 = t.tb * S::TB;
   const int64_t out_rows = P == kGradW ? a.M - b0 : t.end - t.first - b0;
@@ -769,6 +773,22 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
   }
 }
 
+template <int ST, Product P, typename S, bool DIRECT>
+__global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
+  __shared__ __align__(1024) unsigned char lds[kLdsBytes<S, DIRECT>];
+  product<ST, P, S, DIRECT>(a, blockIdx.x, lds);
+}
+
+// Both gradients' products where their tiles have one shape: the second's fill the
+// CUs that the first's last round leaves idle.  `first` workgroups, a multiple of
+// the XCDs, have the weights'.
+template <int ST, typename S, bool DIRECT>
+__global__ __launch_bounds__(S::threads) void grouped_gradients(GroupedArgs a, uint32_t first) {
+  __shared__ __align__(1024) unsigned char lds[kLdsBytes<S, DIRECT>];
+  if (blockIdx.x < first) product<ST, kGradW, S, DIRECT>(a, blockIdx.x, lds);
+  else product<ST, kGradX, S, DIRECT>(a, blockIdx.x - first, lds);
+}
+
 // The chunks' sums of a group, first chunk first, to its gradients.
 template <int ST>
 __global__ __launch_bounds__(kBlock) void grouped_join(GroupedArgs a, int64_t blocks) {
@@ -843,19 +863,37 @@ __global__ __launch_bounds__(1024) void grouped_bias_grad(GroupedArgs a) {
 
 inline int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
-template <int ST, Product P, typename S>
-hipError_t launch_product(const GroupedArgs& a, hipStream_t s) {
+// Workgroups of a product.
+template <Product P, typename S>
+int64_t workgroups(const GroupedArgs& a) {
   const int64_t na = ceil_div(P == kForward ? a.M : a.K, S::TA);
   // a group's last row tile (or chunk) may be partial: at most one more for each group
   const int64_t units = P != kGradW ? a.rows / S::TB + std::min(a.groups, a.rows)
                         : a.chunk   ? a.rows / a.chunk + a.groups
                                     : a.groups;
-  const int64_t nb = P == kGradW ? ceil_div(a.M, S::TB) : 1;
-  const dim3 grid(static_cast<unsigned>(na * nb * units));
+  return na * units * (P == kGradW ? ceil_div(a.M, S::TB) : 1);
+}
+
+template <int ST, Product P, typename S>
+hipError_t launch_product(const GroupedArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(workgroups<P, S>(a)));
   if (a.direct)
     hipLaunchKernelGGL((grouped_product<ST, P, S, true>), grid, dim3(S::threads), 0, s, a);
   else
     hipLaunchKernelGGL((grouped_product<ST, P, S, false>), grid, dim3(S::threads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int ST, typename S>
+hipError_t launch_gradients(const GroupedArgs& a, hipStream_t s) {
+  const int64_t first = (workgroups<kGradW, S>(a) + 7) / 8 * 8;
+  const dim3 grid(static_cast<unsigned>(first + workgroups<kGradX, S>(a)));
+  if (a.direct)
+    hipLaunchKernelGGL((grouped_gradients<ST, S, true>), grid, dim3(S::threads), 0, s, a,
+                       static_cast<uint32_t>(first));
+  else
+    hipLaunchKernelGGL((grouped_gradients<ST, S, false>), grid, dim3(S::threads), 0, s, a,
+                       static_cast<uint32_t>(first));
   return hipGetLastError();
 }
 
@@ -864,45 +902,59 @@ using Medium = Shape<128, 128, 2, 2, 2, 128>;
 using Square = Shape<64, 64, 2, 2, 4, 128>;
 using Narrow = Shape<128, 32, 4, 1, 4, 128>;
 
+// The tiles of a product over rows, by their outputs along the columns: 32 stands
+// for Narrow.
+inline int row_tile(const GroupedArgs& a, int64_t cols) {
+  const auto tiles = [&](int64_t t) { return (a.rows / t + a.groups) * ceil_div(cols, t); };
+  if (a.rows <= a.groups * 32) return 32;
+  if (tiles(256) >= 1024) return 256;
+  return tiles(128) >= 1024 ? 128 : 64;
+}
+
 template <int ST, Product P>
 hipError_t launch_rows(const GroupedArgs& a, hipStream_t s) {
-  const int64_t cols = P == kForward ? a.M : a.K;
-  const auto tiles = [&](int64_t t) { return (a.rows / t + a.groups) * ceil_div(cols, t); };
-  if (a.rows <= a.groups * 32) return launch_product<ST, P, Narrow>(a, s);
-  if (tiles(256) >= 1024) return launch_product<ST, P, Large>(a, s);
-  if (tiles(128) >= 1024) return launch_product<ST, P, Medium>(a, s);
-  return launch_product<ST, P, Square>(a, s);
+  const int tile = row_tile(a, P == kForward ? a.M : a.K);
+  return tile == 256   ? launch_product<ST, P, Large>(a, s)
+         : tile == 128 ? launch_product<ST, P, Medium>(a, s)
+         : tile == 64  ? launch_product<ST, P, Square>(a, s)
+                       : launch_product<ST, P, Narrow>(a, s);
 }
 
 template <int ST>
-hipError_t launch_grad_w(const GroupedArgs& a, const GradWPlan& plan, hipStream_t s) {
-  hipError_t e = plan.tile == 256   ? launch_product<ST, kGradW, Large>(a, s)
-                 : plan.tile == 128 ? launch_product<ST, kGradW, Medium>(a, s)
-                                    : launch_product<ST, kGradW, Square>(a, s);
-  if (e != hipSuccess || plan.slots == 0) return e;
-  const int64_t blocks = ceil_div(std::max(ceil_div(a.M * a.K, 4), a.M), kBlock);
-  hipLaunchKernelGGL((grouped_join<ST>), dim3(static_cast<unsigned>(blocks * a.groups)), dim3(kBlock),
-                     0, s, a, blocks);
-  return hipGetLastError();
-}
-
-template <int ST>
-hipError_t launch_grouped(const GroupedArgs& a, bool backward, hipStream_t s) {
-  if (!backward) return launch_rows<ST, kForward>(a, s);
+hipError_t launch_backward(const GroupedArgs& a, hipStream_t s) {
+  constexpr int32_t dtype = ST;
+  const bool dx = a.dx && a.rows > 0;
   hipError_t e = hipSuccess;
-  if (a.dx && a.rows > 0) e = launch_rows<ST, kGradX>(a, s);
-  if (e != hipSuccess) return e;
   if (a.dw) {
-    constexpr int32_t dtype = ST;
-    return launch_grad_w<ST>(a, plan_grad_w(a.rows, a.groups, a.K, a.M, dtype), s);
+    const GradWPlan plan = plan_grad_w(a.rows, a.groups, a.K, a.M, dtype);
+    const bool both = dx && row_tile(a, a.K) == plan.tile;
+    if (dx && !both) e = launch_rows<ST, kGradX>(a, s);
+    if (e != hipSuccess) return e;
+    e = plan.tile == 256   ? (both ? launch_gradients<ST, Large>(a, s)
+                                   : launch_product<ST, kGradW, Large>(a, s))
+        : plan.tile == 128 ? (both ? launch_gradients<ST, Medium>(a, s)
+                                   : launch_product<ST, kGradW, Medium>(a, s))
+                           : (both ? launch_gradients<ST, Square>(a, s)
+                                   : launch_product<ST, kGradW, Square>(a, s));
+    if (e != hipSuccess || plan.slots == 0) return e;
+    const int64_t blocks = ceil_div(std::max(ceil_div(a.M * a.K, 4), a.M), kBlock);
+    hipLaunchKernelGGL((grouped_join<ST>), dim3(static_cast<unsigned>(blocks * a.groups)),
+                       dim3(kBlock), 0, s, a, blocks);
+    return hipGetLastError();
   }
-  if (a.db) {
+  if (dx) e = launch_rows<ST, kGradX>(a, s);
+  if (e == hipSuccess && a.db) {
     hipLaunchKernelGGL((grouped_bias_grad<ST>),
                        dim3(static_cast<unsigned>(ceil_div(a.M, 64)), static_cast<unsigned>(a.groups)),
                        dim3(1024), 0, s, a);
     e = hipGetLastError();
   }
   return e;
+}
+
+template <int ST>
+hipError_t launch_grouped(const GroupedArgs& a, bool backward, hipStream_t s) {
+  return backward ? launch_backward<ST>(a, s) : launch_rows<ST, kForward>(a, s);
 }
 
 }  // namespace
