@@ -399,7 +399,7 @@ tbe_status tbe_scan_step(const void* x, int64_t x_stride, const void* gate, int6
  * offsets[s+1] of x and gate ([tokens, dim]); offsets [seqs + 1] start at 0
  * and end at tokens.  initial: fp32 [seqs, dim], the state before each first
  * token (NULL: zeros; stride 0: one row for all).  tokens and seqs are
- * below 2^31 - 1, dim and the strides of rows at most 2^24, tokens rounded up
+ * below 2^31 - 1, dim and the strides of rows at most 2^23, tokens rounded up
  * to 512 and dim rounded up to 64 have a product below 2^35.
  * max_polls: how often a part of a sequence looks for the state of the part
  * before it until it works that state out by itself (0: 2^16; below 0: never

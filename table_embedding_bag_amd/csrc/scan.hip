@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "layers.hpp"
 
@@ -252,6 +253,12 @@ __device__ int64_t sequence_before(const ScanArgs& a, int64_t token) {
   return lo - 1;
 }
 
+// Waves in a tile: 4, or 8 where sequences span tiles.  Fewer wait less for each
+// other (8192 sequences of about 20 x 256 bf16: 64 and 100 us with 4, 70 and 113
+// with 8), more make the chain of tiles shorter (4 of 16384 x 1024 bf16: 127 and
+// 227 us with 8, 164 and 314 with 4).
+constexpr int kFewWaves = 4, kManyWaves = 8;
+
 // What the waves of a tile share.
 template <int V, int W, int T>
 struct TileShared {
@@ -343,13 +350,14 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
   if (first || (STEP > 0 ? sh.resets[0] & 1u : sh.resets[W - 1] >> (T - 1) & 1u)) return;
 
   // The tiles before this one in the group, nearest first, up to the nearest that
-  // knows its state.  The nearest alone is looked at first: with short sequences
-  // it does, and with long ones looking at all at once gains nothing.
+  // knows its state.  Where sequences are short (few waves), the nearest alone is
+  // looked at first, and mostly does; where they are long, all at once (4 of 16384 x
+  // 1024 bf16: 112 and 198 us instead of 114 and 206).
   uint32_t polls = 0;
   int depth = 0;        // tiles taken
   bool known = false, given_up = false;
   while (depth < in_group && !known && !given_up) {
-    const int n = depth == 0 ? 1 : in_group;
+    const int n = depth == 0 && W == kFewWaves ? 1 : in_group;
     for (int e = depth + wave; e < n; e += W) {
       Entry<V> x;
       Kind kind;
@@ -536,22 +544,31 @@ struct Word<8> {
 template <int ST, int V>
 using RowWord = Word<StorageTraits<ST>::bytes * V>;
 
-// The span's rows from column `c` (the workgroup's first) of `base`; a lane's V
-// channels are at byte `lane_off` (kOutside: none).
+// The span's rows from column `c` (the workgroup's first) of `base`, a descriptor
+// for each, made in scalar registers: one for them all needs each row's offset in
+// a vector register of its own.  A lane's V channels are at byte `lane_off`
+// (kOutside: none).
+struct Span {
+  const char* base;
+  uint32_t step, bytes;  // between rows, of a row
+  int tokens;
+  __device__ __forceinline__ Buffer row(int i) const {
+    return buffer(base + static_cast<uint64_t>(step) * i, i < tokens ? bytes : 0u);
+  }
+};
 template <int ST>
-__device__ __forceinline__ Buffer span_buffer(const void* base, int64_t stride, int64_t t0,
-                                              int tokens, int64_t c, int64_t dim) {
+__device__ __forceinline__ Span span(const void* base, int64_t stride, int64_t t0, int tokens,
+                                     int64_t c, int64_t dim) {
   constexpr int b = StorageTraits<ST>::bytes;
-  return buffer(static_cast<const char*>(base) + (t0 * stride + c) * b,
-                tokens > 0 && base ? ((tokens - 1) * stride + dim - c) * b : 0);
+  return {static_cast<const char*>(base) + (t0 * stride + c) * b, static_cast<uint32_t>(stride * b),
+          static_cast<uint32_t>((dim - c) * b), base ? tokens : 0};
 }
 template <int ST, int V, int T>
-__device__ __forceinline__ void load_span(Buffer rows, int64_t stride, uint32_t lane_off,
+__device__ __forceinline__ void load_span(const Span& rows, uint32_t lane_off,
                                           StoredVec<ST, V> (&out)[T]) {
-  const uint32_t step = static_cast<uint32_t>(stride) * StorageTraits<ST>::bytes;
 #pragma unroll
   for (int i = 0; i < T; ++i)
-    out[i] = __builtin_bit_cast(StoredVec<ST, V>, RowWord<ST, V>::load(rows, lane_off + i * step));
+    out[i] = __builtin_bit_cast(StoredVec<ST, V>, RowWord<ST, V>::load(rows.row(i), lane_off));
 }
 // The rows of `base` of the sequences whose bits are set in mask (list: lane at +
 // i holds the sequence of token i), 0 for the others.
@@ -593,6 +610,34 @@ __device__ __forceinline__ Place place_of(const ScanWork& w) {
   return {static_cast<int64_t>(row) * 8 + blockIdx.x % 8, eight - row * w.channel_blocks};
 }
 
+// Tokens in a wave's span, and whether the backward pass works its gates out again
+// after the join instead of keeping them.  It holds twice as much for each token as
+// the forward pass; without the gates, rows of 2 bytes need half of that.  Where
+// sequences are long and the wait for the join is more than half of a tile's time,
+// spans of 16 halve the number of waits (4 of 16384 x 1024 bf16: 198 -> 170 us);
+// the forward pass with spans of 32 and gates worked out again went from 112 to 136.
+constexpr int kForwardSpan = 16;
+constexpr int back_span(int waves) { return waves == kManyWaves ? 16 : 8; }
+template <int ST>
+constexpr bool gates_again(int waves) {
+  return waves == kManyWaves && StorageTraits<ST>::bytes == 2;
+}
+
+// A row's values anew: what was computed from them before is not kept for later.
+template <int ST, int V>
+__device__ __forceinline__ void renew(StoredVec<ST, V>& row) {
+  using W = typename RowWord<ST, V>::type;
+  W w = __builtin_bit_cast(W, row);
+  if constexpr (sizeof(W) == 2) {
+    uint32_t wide = w;
+    asm volatile("" : "+v"(wide));
+    w = static_cast<W>(wide);
+  } else {
+    asm volatile("" : "+v"(w));
+  }
+  row = __builtin_bit_cast(StoredVec<ST, V>, w);
+}
+
 template <int ST, int V, bool SIGMOID, int W, int T>
 __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) {
   __shared__ TileShared<V, W, T> sh;
@@ -610,50 +655,40 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
   // First of all: their answer does not wait for the rows' then.
   const int2 marks = lane < tokens ? w.marks[t0 + lane] : make_int2(-1, -1);
   StoredVec<ST, V> x[T], g[T];
-  load_span<ST, V, T>(span_buffer<ST>(a.gate, a.gate_stride, t0, tokens, c, a.dim), a.gate_stride, at, g);
-  load_span<ST, V, T>(span_buffer<ST>(a.x, a.x_stride, t0, tokens, c, a.dim), a.x_stride, at, x);
+  load_span<ST, V, T>(span<ST>(a.gate, a.gate_stride, t0, tokens, c, a.dim), at, g);
+  load_span<ST, V, T>(span<ST>(a.x, a.x_stride, t0, tokens, c, a.dim), at, x);
   if (threadIdx.x < W) sh.group_kind[threadIdx.x] = kAbsent;
   const int32_t starts = marks.x, ends = marks.y;
   const uint32_t first = static_cast<uint32_t>(__ballot(starts >= 0));
   const uint32_t last = static_cast<uint32_t>(__ballot(ends >= 0));
   // state_i = first ? u_i : k_i state_{i-1} + u_i, the state before a first token being in its u
   float k[T][V], u[T][V], A[V], B[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
   // A span in the middle of a sequence, T tokens long, has nothing to choose.
   const bool plain = first == 0u && tokens == T;
-  if (plain) {
-#pragma unroll
-    for (int i = 0; i < T; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Gates t = gates<ST, SIGMOID>(static_cast<float>(g[i][v]));
-        k[i][v] = t.a;
-        u[i][v] = t.b * static_cast<float>(x[i][v]);
-        settle(k[i][v]), settle(u[i][v]);
-        B[v] = fmaf(k[i][v], B[v], u[i][v]);
-        A[v] *= k[i][v];
-      }
-  } else {
+  auto reduce = [&](auto plain_) {
+    constexpr bool kPlain = plain_;
     float init[4][V];
 #pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+#pragma unroll
     for (int i = 0; i < T; ++i) {
-      const bool f = first >> i & 1u;
-      if (i % 4 == 0)  // initial states of four tokens at a time: few spans have more starts
+      const bool f = !kPlain && (first >> i & 1u), in = kPlain || i < tokens;
+      if (!kPlain && i % 4 == 0)  // initial states of four tokens at a time: few spans have more starts
         load_marked<V, 4>(a.initial, a.initial_stride, first >> i & 15u, starts, i, c, a.dim, at32, init);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Gates t = gates<ST, SIGMOID>(static_cast<float>(g[i][v]));
-        const bool in = i < tokens;
-        k[i][v] = in ? t.a : 1.0f;
         const float in_x = t.b * static_cast<float>(x[i][v]);
+        k[i][v] = in ? t.a : 1.0f;
         u[i][v] = f ? fmaf(t.a, init[i % 4][v], in_x) : in ? in_x : 0.0f;
         settle(k[i][v]), settle(u[i][v]);
         B[v] = f ? u[i][v] : fmaf(k[i][v], B[v], u[i][v]);
         A[v] *= k[i][v];
       }
     }
-  }
+  };
+  if (plain) reduce(std::true_type{});
+  else reduce(std::false_type{});
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     sh.A[wave][lane * V + v] = A[v];
@@ -677,34 +712,26 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
     }
   });
   wave_start<V, W, T, 1>(sh, wave, lane, state);
-  const Buffer carry = span_buffer<kF32>(a.carry, a.dim, t0 / kCarry, (tokens + kCarry - 1) / kCarry, c,
+  const Span carry = span<kF32>(a.carry, a.dim, t0 / kCarry, (tokens + kCarry - 1) / kCarry, c,
                                          a.dim);
-  const Buffer h = span_buffer<ST>(a.h, a.dim, t0, tokens, c, a.dim);
-  const uint32_t step = static_cast<uint32_t>(a.dim) * bytes;
-  if (plain && last == 0u) {
+  const Span h = span<ST>(a.h, a.dim, t0, tokens, c, a.dim);
+  auto run = [&](auto plain_) {
+    constexpr bool kPlain = plain_;
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-      if (i % kCarry == 0 && a.carry)
-        store_row<kF32, V>(carry, at32 + i / kCarry * static_cast<uint32_t>(a.dim) * 4, state);
+      const bool f = !kPlain && (first >> i & 1u);
+      if (i % kCarry == 0 && a.carry) store_row<kF32, V>(carry.row(i / kCarry), at32, state);
 #pragma unroll
-      for (int v = 0; v < V; ++v) state[v] = fmaf(k[i][v], state[v], u[i][v]);
-      store_row<ST, V>(h, at + i * step, state);
+      for (int v = 0; v < V; ++v) state[v] = f ? u[i][v] : fmaf(k[i][v], state[v], u[i][v]);
+      store_row<ST, V>(h.row(i), at, state);
+      if (!kPlain && (last >> i & 1u)) {
+        const int64_t s = __builtin_amdgcn_readlane(ends, i);
+        store_row<kF32, V>(span<kF32>(a.final, a.dim, s, 1, c, a.dim).row(0), at32, state);
+      }
     }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < T; ++i) {
-    const bool f = first >> i & 1u;
-    if (i % kCarry == 0 && a.carry)
-      store_row<kF32, V>(carry, at32 + i / kCarry * static_cast<uint32_t>(a.dim) * 4, state);
-#pragma unroll
-    for (int v = 0; v < V; ++v) state[v] = f ? u[i][v] : fmaf(k[i][v], state[v], u[i][v]);
-    store_row<ST, V>(h, at + i * step, state);
-    if (last >> i & 1u) {
-      const int64_t s = __builtin_amdgcn_readlane(ends, i);
-      store_row<kF32, V>(span_buffer<kF32>(a.final, a.dim, s, 1, c, a.dim), at32, state);
-    }
-  }
+  };
+  if (plain && last == 0u) run(std::true_type{});
+  else run(std::false_type{});
 }
 
 template <int ST, int V, bool SIGMOID, int W, int T>
@@ -724,16 +751,14 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
   // First of all: their answer does not wait for the rows' then.
   const int2 marks = lane < tokens ? w.marks[t0 + lane] : make_int2(-1, -1);
   StoredVec<ST, V> x[T], g[T], dh[T];
-  load_span<ST, V, T>(span_buffer<ST>(a.gate, a.gate_stride, t0, tokens, c, a.dim), a.gate_stride, at, g);
-  load_span<ST, V, T>(span_buffer<ST>(a.x, a.x_stride, t0, tokens, c, a.dim), a.x_stride, at, x);
-  load_span<ST, V, T>(span_buffer<ST>(a.grad_h, a.grad_h_stride, t0, tokens, c, a.dim), a.grad_h_stride,
-                   at, dh);
+  load_span<ST, V, T>(span<ST>(a.gate, a.gate_stride, t0, tokens, c, a.dim), at, g);
+  load_span<ST, V, T>(span<ST>(a.x, a.x_stride, t0, tokens, c, a.dim), at, x);
+  load_span<ST, V, T>(span<ST>(a.grad_h, a.grad_h_stride, t0, tokens, c, a.dim), at, dh);
   float state[V];
   {
     const auto r = __builtin_bit_cast(
         StoredVec<kF32, V>,
-        RowWord<kF32, V>::load(span_buffer<kF32>(a.carried, a.dim, t0 / kCarry, tokens > 0, c, a.dim),
-                               at32));
+        RowWord<kF32, V>::load(span<kF32>(a.carried, a.dim, t0 / kCarry, tokens > 0, c, a.dim).row(0), at32));
 #pragma unroll
     for (int v = 0; v < V; ++v) state[v] = r[v];
   }
@@ -743,61 +768,49 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
   const uint32_t last = static_cast<uint32_t>(__ballot(ends >= 0));
   // lam_i = up_i + (last ? 0 : mu_{i+1}), mu_i = a_i lam_i, the gradient of a final
   // state being in its up; dgate_i = q_i lam_i with q_i of the state before token i
-  float ka[T][V], kb[T][V], q[T][V], up[T][V], A[V], B[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+  // The span's pair is summed in the order of its tokens: mu_0 = sum_i (a_0 .. a_i) up_i
+  // up to the first last token.
+  constexpr bool kAgain = gates_again<ST>(W);
+  constexpr int kMarked = kAgain ? 4 : T;  // tokens whose marked rows are loaded together
+  float ka[kAgain ? 1 : T][V], kb[kAgain ? 1 : T][V], up[kAgain ? 1 : T][V], q[T][V], A[V], B[V];
+  float final_up[kMarked][V];
   // A span in the middle of a sequence, T tokens long, has nothing to choose.
   const bool plain = (first | last) == 0u && tokens == T;
-  if (plain) {
+  auto load_final = [&](int i) {
+    load_marked<V, kMarked>(a.grad_final, a.grad_final_stride, last >> i & ((1u << kMarked) - 1u), ends,
+                            i, c, a.dim, at32, final_up);
+  };
+  auto reduce = [&](auto plain_) {
+    constexpr bool kPlain = plain_;
+    float init[kMarked][V];
 #pragma unroll
-    for (int i = 0; i < T; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Gates t = gates<ST, SIGMOID>(static_cast<float>(g[i][v]));
-        ka[i][v] = t.a;
-        kb[i][v] = t.b;
-        const float before = state[v], xi = static_cast<float>(x[i][v]);
-        state[v] = fmaf(t.a, before, t.b * xi);  // as the forward pass rounds it
-        q[i][v] = SIGMOID ? (before - xi) * (t.a * t.b) : before;
-        up[i][v] = static_cast<float>(dh[i][v]);
-        settle(ka[i][v]), settle(kb[i][v]), settle(q[i][v]), settle(up[i][v]);
-      }
-#pragma unroll
-    for (int i = T - 1; i >= 0; --i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        B[v] = ka[i][v] * (up[i][v] + B[v]);
-        A[v] *= ka[i][v];
-      }
-  } else {
-    load_marked<V, T>(a.initial, a.initial_stride, first, starts, 0, c, a.dim, at32, q);
-    load_marked<V, T>(a.grad_final, a.grad_final_stride, last, ends, 0, c, a.dim, at32, up);
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-      const bool f = first >> i & 1u;
+      const bool f = !kPlain && (first >> i & 1u), in = kPlain || i < tokens;
+      const bool passed = !kPlain && (last & ((1u << i) - 1u)) != 0u;
+      if (!kPlain && i % kMarked == 0) {
+        load_marked<V, kMarked>(a.initial, a.initial_stride, first >> i & ((1u << kMarked) - 1u),
+                                starts, i, c, a.dim, at32, init);
+        load_final(i);
+      }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Gates t = gates<ST, SIGMOID>(static_cast<float>(g[i][v]));
-        const bool in = i < tokens;
-        ka[i][v] = in ? t.a : 1.0f;
-        kb[i][v] = t.b;
-        const float before = f ? q[i][v] : state[v], xi = static_cast<float>(x[i][v]);
+        const float before = f ? init[i % kMarked][v] : state[v], xi = static_cast<float>(x[i][v]);
+        float at_ = in ? t.a : 1.0f, bt = t.b, ut = static_cast<float>(dh[i][v]);
+        if (!kPlain) ut += final_up[i % kMarked][v];
         state[v] = fmaf(t.a, before, t.b * xi);  // as the forward pass rounds it
         q[i][v] = SIGMOID ? (before - xi) * (t.a * t.b) : before;
-        up[i][v] += static_cast<float>(dh[i][v]);
-        settle(ka[i][v]), settle(kb[i][v]), settle(q[i][v]), settle(up[i][v]);
+        settle(at_), settle(bt), settle(q[i][v]), settle(ut);
+        if constexpr (!kAgain) ka[i][v] = at_, kb[i][v] = bt, up[i][v] = ut;
+        A[v] *= at_;
+        B[v] = passed ? B[v] : fmaf(A[v], ut, B[v]);
       }
     }
-#pragma unroll
-    for (int i = T - 1; i >= 0; --i) {
-      const bool l = last >> i & 1u;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        B[v] = ka[i][v] * (l ? up[i][v] : up[i][v] + B[v]);
-        A[v] *= ka[i][v];
-      }
-    }
-  }
+  };
+  if (plain) reduce(std::true_type{});
+  else reduce(std::false_type{});
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     sh.A[wave][lane * V + v] = A[v];
@@ -822,61 +835,53 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
     }
   });
   wave_start<V, W, T, -1>(sh, wave, lane, mu);
-  const Buffer dxs = span_buffer<ST>(a.dx, a.dx_stride, t0, tokens, c, a.dim);
-  const Buffer dgs = span_buffer<ST>(a.dgate, a.dgate_stride, t0, tokens, c, a.dim);
-  const uint32_t dx_step = static_cast<uint32_t>(a.dx_stride) * bytes;
-  const uint32_t dg_step = static_cast<uint32_t>(a.dgate_stride) * bytes;
-  if (plain) {
+  const Span dxs = span<ST>(a.dx, a.dx_stride, t0, tokens, c, a.dim);
+  const Span dgs = span<ST>(a.dgate, a.dgate_stride, t0, tokens, c, a.dim);
+  if constexpr (kAgain) {
+#pragma unroll
+    for (int i = 0; i < T; ++i) renew<ST, V>(g[i]), renew<ST, V>(dh[i]);
+  }
+  auto run = [&](auto plain_) {
+    constexpr bool kPlain = plain_;
 #pragma unroll
     for (int i = T - 1; i >= 0; --i) {
+      const bool l = !kPlain && (last >> i & 1u), in = kPlain || i < tokens;
+      if (!kPlain && kAgain && i % kMarked == kMarked - 1) load_final(i - kMarked + 1);
       float dx[V], dg[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float lam = up[i][v] + mu[v];
-        dx[v] = kb[i][v] * lam;
+        float at_, bt, ut;
+        if constexpr (kAgain) {
+          const Gates t = gates<ST, SIGMOID>(static_cast<float>(g[i][v]));
+          at_ = in ? t.a : 1.0f, bt = t.b, ut = static_cast<float>(dh[i][v]);
+          if (!kPlain) ut += final_up[i % kMarked][v];
+        } else {
+          at_ = ka[i][v], bt = kb[i][v], ut = up[i][v];
+        }
+        const float lam = l ? ut : ut + mu[v];
+        dx[v] = bt * lam;
         dg[v] = lam * q[i][v];
-        mu[v] = ka[i][v] * lam;
+        mu[v] = at_ * lam;
       }
-      store_row<ST, V>(dxs, at + i * dx_step, dx);
-      store_row<ST, V>(dgs, at + i * dg_step, dg);
+      store_row<ST, V>(dxs.row(i), at, dx);
+      store_row<ST, V>(dgs.row(i), at, dg);
+      if (!kPlain && a.dinitial && (first >> i & 1u)) {
+        const int64_t s = __builtin_amdgcn_readlane(starts, i);
+        store_row<kF32, V>(span<kF32>(a.dinitial, a.dim, s, 1, c, a.dim).row(0), at32, mu);
+      }
     }
-    return;
-  }
-#pragma unroll
-  for (int i = T - 1; i >= 0; --i) {
-    const bool l = last >> i & 1u;
-    float dx[V], dg[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float lam = l ? up[i][v] : up[i][v] + mu[v];
-      dx[v] = kb[i][v] * lam;
-      dg[v] = lam * q[i][v];
-      mu[v] = ka[i][v] * lam;
-    }
-    store_row<ST, V>(dxs, at + i * dx_step, dx);
-    store_row<ST, V>(dgs, at + i * dg_step, dg);
-    if (a.dinitial && (first >> i & 1u)) {
-      const int64_t s = __builtin_amdgcn_readlane(starts, i);
-      store_row<kF32, V>(span_buffer<kF32>(a.dinitial, a.dim, s, 1, c, a.dim), at32, mu);
-    }
-  }
+  };
+  if (plain) run(std::true_type{});
+  else run(std::false_type{});
 }
 
-// Tokens in a wave's span.  The backward pass holds twice as much for each token:
-// its spans are as short as the carry's rows.
-constexpr int kForwardSpan = 16, kBackSpan = kCarry;
-// Waves in a tile: 4, or 8 where sequences span tiles.  Fewer wait less for each
-// other (8192 sequences of about 20 x 256 bf16: 64 and 100 us with 4, 70 and 113
-// with 8), more make the chain of tiles shorter (4 of 16384 x 1024 bf16: 127 and
-// 227 us with 8, 164 and 314 with 4).
-constexpr int kFewWaves = 4, kManyWaves = 8;
 int waves_of(int64_t tokens, int64_t seqs) { return tokens < seqs * 256 ? kFewWaves : kManyWaves; }
 
 template <int ST, int V, bool SIGMOID, int W>
 hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, bool back, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>((w.tiles + 7) / 8 * 8 * w.channel_blocks));
   if (back)
-    hipLaunchKernelGGL((scan_tiles_back<ST, V, SIGMOID, W, kBackSpan>), grid, dim3(64 * W), 0, s, a,
+    hipLaunchKernelGGL((scan_tiles_back<ST, V, SIGMOID, W, back_span(W)>), grid, dim3(64 * W), 0, s, a,
                        w);
   else
     hipLaunchKernelGGL((scan_tiles<ST, V, SIGMOID, W, kForwardSpan>), grid, dim3(64 * W), 0, s, a, w);
@@ -909,7 +914,8 @@ int lane_channels(const tbe_scan_input* in, const ScanArgs& a) {
 }
 
 int64_t tiles_of(int64_t tokens, int64_t seqs, bool back) {
-  const int64_t n = waves_of(tokens, seqs) * (back ? kBackSpan : kForwardSpan);
+  const int w = waves_of(tokens, seqs);
+  const int64_t n = w * (back ? back_span(w) : kForwardSpan);
   return (tokens + n - 1) / n;
 }
 
@@ -919,7 +925,8 @@ int64_t groups_of(int64_t tiles) { return (tiles + kGroup - 1) / kGroup; }
 
 // The workspace: marks, pairs and states of tiles and groups.
 size_t workspace_bytes_of(int64_t tokens, int64_t seqs, int64_t dim) {
-  static_assert(kBackSpan <= kForwardSpan, "the backward pass has the more tiles");
+  static_assert(back_span(kFewWaves) <= kForwardSpan && back_span(kManyWaves) <= kForwardSpan,
+                "the forward pass has no more tiles");
   const int64_t tiles = tiles_of(tokens, seqs, true);
   const size_t words = static_cast<size_t>((tiles + groups_of(tiles)) * dim);
   return up256(static_cast<size_t>(tokens) * 8) + up256(words * 8) + up256(words * 4);
@@ -960,8 +967,8 @@ hipError_t launch_scan(ScanArgs a, const tbe_scan_input* in, bool back, void* wo
                 : launch_tiles<kBF16, 1>(a, w, in->gate_kind, back, s);
 }
 
-// A span's rows lie within a buffer descriptor's reach.
-constexpr int64_t kMaxRow = int64_t{1} << 24;
+// A row lies within a buffer descriptor's reach.
+constexpr int64_t kMaxRow = int64_t{1} << 23;
 
 // Sizes a call can take: 31-bit tokens and sequences, 2^32 threads in a launch.
 tbe_status check_sizes(int64_t tokens, int64_t seqs, int64_t dim, int32_t dtype) {
@@ -969,7 +976,7 @@ tbe_status check_sizes(int64_t tokens, int64_t seqs, int64_t dim, int32_t dtype)
   if (tokens < 0 || seqs < 0 || dim < 1 || !known_dtype(dtype)) return TBE_ERR_INVALID_ARGUMENT;
   if (seqs == 0 && tokens > 0) return TBE_ERR_INVALID_ARGUMENT;
   if (tokens >= kMax || seqs >= kMax || dim > kMaxRow) return TBE_ERR_UNSUPPORTED;
-  // 512 threads for 64 tokens of 64 channels at most, tiles rounded up to 8
+  // 256 threads for 32 tokens of 64 channels at most, tiles rounded up to 8
   if ((tokens + 511) / 512 * 8 * ((dim + 63) / 64) >= (int64_t{1} << 23))
     return TBE_ERR_UNSUPPORTED;
   return TBE_OK;

@@ -297,3 +297,13 @@ def test_graph_replays_match_eager_calls():
         torch.cuda.synchronize()
         for name in want:
             assert torch.equal(out[name], want[name]), (i, name)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "decay"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim", [64, 67, 200])
+def test_short_sequences_within_spans_of_long_ones(dim, dtype, kind):
+    """Several sequences start and end inside one wave's tokens, among ones that span many tiles."""
+    lengths = [2100, 3, 0, 1, 4, 2, 2, 1, 0, 1900, 15, 16, 1, 2500, 0]
+    Problem(lengths, dim, DTYPES[dtype], kind, seed=21, halves=True, index=torch.int32).check()
+    Problem(lengths, dim, DTYPES[dtype], kind, seed=22, initial=False, grads=False).check()
