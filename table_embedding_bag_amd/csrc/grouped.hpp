@@ -524,6 +524,7 @@ __device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, unsig
       t.group = u.group, t.first = u.first, t.end = u.end, slot = u.slot;
       if (slot >= a.slots) return;  // groups that overlap: bad offsets
     } else {
+      if (unit >= a.groups) return;  // where workgroups are rounded up to the XCDs
       t.group = ranked_group(a, unit);
       t.first = group_offset(a, t.group);
       t.end = group_offset(a, t.group + 1);

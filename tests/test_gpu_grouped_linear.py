@@ -255,3 +255,26 @@ def test_graph_replays_match_eager_calls():
         torch.cuda.synchronize()
         for name in want:
             assert torch.equal(out[name], want[name]), (i, name)
+
+
+@pytest.mark.parametrize("name,G,N,K,M,dtype", [("128", 75, 23200, 128, 896, "bf16"), ("128", 75, 23200, 128, 896, "fp32"),
+                                                ("256", 41, 42000, 1280, 1280, "bf16")])
+def test_both_gradients_in_workgroups_rounded_up(name, G, N, K, M, dtype):
+    """The gradients' products in one launch, where the first's workgroups (75 x 7, 41 x 25) are no
+    multiple of 8 and the ones that fill it up have nothing to do."""
+    print(f"[grouped] rounded up {name} {dtype}", flush=True)
+    g = np.random.default_rng(22)
+    p = Problem(g.multinomial(N, np.full(G, 1 / G)), K, M, DTYPES[dtype], seed=23)
+    dx, dw, db = tbe.grouped_linear_backward(p.x, p.w, p.offsets, p.grad, bias=True)
+    for i in (0, G // 2, G - 1):
+        r = slice(int(p.off[i]), int(p.off[i + 1]))
+        x, w, dy = p.x[r].double(), p.w[i].double(), p.grad[r].double().contiguous()
+        n = r.stop - r.start
+        for what, mine, want, size, terms in (
+                ("dx", dx[r], dy @ w, dy.abs() @ w.abs(), M),
+                ("dw", dw[i], dy.t().contiguous() @ x, dy.abs().t().contiguous() @ x.abs(), n),
+                ("db", db[i], dy.sum(0), dy.abs().sum(0), n)):
+            off = (mine.double() - want).abs()
+            bound = (terms + 2) * ref.U32 * size
+            bound = bound + ref.half_step(p.dtype) * (want.abs() + bound) + ref.TINY[p.dtype]
+            assert (off <= bound).all(), (what, i, float((off / bound).max()))
