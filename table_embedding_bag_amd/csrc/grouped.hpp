@@ -898,18 +898,28 @@ hipError_t launch_gradients(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Tiles of 256 x 256 feed the matrix cores with the fewest bytes: at 32768 x 4096 ->
+// 4096 bf16 they run at 1.1 PFLOP/s of random values and 1.5 of zeros, so it is the
+// power that bounds them (four waves of 128 x 128 a tile, slices of half the length,
+// four slices by LDS, or 256 x 128 with two workgroups a CU: 1.03 to 1.5 ms instead of
+// 1.0).
 using Large = Shape<256, 256, 2, 4, 2, 128>;
 using Medium = Shape<128, 128, 2, 2, 2, 128>;
 using Square = Shape<64, 64, 2, 2, 4, 128>;
 using Narrow = Shape<128, 32, 4, 1, 4, 128>;
 
 // The tiles of a product over rows, by their outputs along the columns: 32 stands
-// for Narrow.
+// for Narrow, for groups of few rows, whose weights' reading is what counts (64 rows
+// over 64 groups, 512 -> 2048 bf16: 18 us, 21 with the others; 4096 rows: 35 with 128,
+// 41 with 64).  Large tiles need several rounds of the CUs (16384 rows in 8 groups,
+// 1024 -> 4096 bf16, 1152 of 256: 162 us, 177 with 128; 4096 -> 1024, 288 of 256: 183 and
+// 172; 32768 x 4096 -> 4096: 1.0 and 1.2 ms), tiles of 128 one (1024 -> 1024: 8192 rows,
+// 576 of them, 32 us, 41 with 64; 4096 rows, 320, 22 and 24; 2048 rows -> 512, 96, 14 and 11).
 inline int row_tile(const GroupedArgs& a, int64_t cols) {
   const auto tiles = [&](int64_t t) { return (a.rows / t + a.groups) * ceil_div(cols, t); };
   if (a.rows <= a.groups * 32) return 32;
   if (tiles(256) >= 1024) return 256;
-  return tiles(128) >= 1024 ? 128 : 64;
+  return tiles(128) >= 256 ? 128 : 64;
 }
 
 template <int ST, Product P>
