@@ -11,6 +11,7 @@
 // 64 bit products for four elements.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "layers.hpp"
@@ -53,68 +54,59 @@ __device__ __forceinline__ uint4 philox(uint64_t counter, uint64_t seed) {
   return make_uint4(c0, c1, c2, c3);
 }
 
-// A thread takes U groups of E elements (16 bytes); groups start at multiples
-// of E in the packed numbering, so that they are whole Philox blocks whatever
-// the row length.  PACKED: all rows lie end to end, element n is at n.
-template <int ST, bool RESIDUAL, bool PACKED, int U>
+// A thread takes a group of E elements (16 bytes); groups start at multiples of E
+// in the packed numbering, so that they are whole Philox blocks whatever the row
+// length.  PACKED: all rows lie end to end, element n is at n.  One group a thread:
+// four, their loads in flight together, were slower at every size (2048 x 128 fp32
+// 3.0 -> 3.8 us, 32768 x 4096 bf16 with a residual 143 -> 151 and its gradient 93 ->
+// 103; 143 and 93 us are 5.6 and 5.8 TB/s, what a copy reaches: memory bounds it).
+template <int ST, bool RESIDUAL, bool PACKED>
 __global__ __launch_bounds__(kBlock) void dropout_map(DropoutArgs a) {
   constexpr int E = 16 / StorageTraits<ST>::bytes;
-  const int64_t groups = (a.n + E - 1) / E;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kBlock * U) + threadIdx.x;
-  StoredVec<ST, E> v[U], res[U];
-  int64_t row[U], col[U];
-  bool whole[U];  // the group's E elements lie in one row
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t g = first + u * kBlock;
+  const int64_t groups = (a.n + E - 1) / E, step = static_cast<int64_t>(gridDim.x) * kBlock;
+  for (int64_t g = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; g < groups; g += step) {
     const int64_t n0 = g * E;
-    row[u] = 0;
-    col[u] = n0;
-    whole[u] = g < groups && n0 + E <= a.n;
+    int64_t row = 0, col = n0;
+    bool whole = n0 + E <= a.n;  // the group's E elements lie in one row
     if constexpr (!PACKED) {
       // n0 / cols: the reciprocal's quotient is at most one too large
       int64_t q = a.inverse ? static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(n0), a.inverse))
                             : n0;
       if (q * a.cols > n0) --q;
-      row[u] = q;
-      col[u] = n0 - q * a.cols;
-      whole[u] = whole[u] && col[u] + E <= a.cols;
+      row = q;
+      col = n0 - q * a.cols;
+      whole = whole && col + E <= a.cols;
     }
-    if (whole[u]) {
-      v[u] = load_vec<ST, E>(a.x, row[u] * a.x_stride + col[u]);
-      if constexpr (RESIDUAL) res[u] = load_vec<ST, E>(a.residual, row[u] * a.r_stride + col[u]);
+    StoredVec<ST, E> v, res;
+    if (whole) {
+      v = load_vec<ST, E>(a.x, row * a.x_stride + col);
+      if constexpr (RESIDUAL) res = load_vec<ST, E>(a.residual, row * a.r_stride + col);
     }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t g = first + u * kBlock;
-    if (g >= groups) continue;
     uint32_t w[E];
 #pragma unroll
     for (int b = 0; b < E / 4; ++b) {
       const uint4 p = philox(a.offset + static_cast<uint64_t>(g * (E / 4) + b), a.seed);
       w[4 * b] = p.x, w[4 * b + 1] = p.y, w[4 * b + 2] = p.z, w[4 * b + 3] = p.w;
     }
-    if (whole[u]) {
+    if (whole) {
       StoredVec<ST, E> out;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const bool kept = w[i] >= a.least && !a.none;
-        float f = kept ? static_cast<float>(v[u][i]) * a.scale : 0.0f;
-        if constexpr (RESIDUAL) f += static_cast<float>(res[u][i]);
+        float f = kept ? static_cast<float>(v[i]) * a.scale : 0.0f;
+        if constexpr (RESIDUAL) f += static_cast<float>(res[i]);
         out[i] = static_cast<typename Stored<ST>::type>(f);
       }
-      store_vec<ST, E>(a.y, row[u] * a.y_stride + col[u], out);
+      store_vec<ST, E>(a.y, row * a.y_stride + col, out);
     } else {  // the matrix's last elements, or a group that runs over a row's end
-      int64_t r = row[u], c = col[u];
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        if (g * E + i >= a.n) break;
+        if (n0 + i >= a.n) break;
         const bool kept = w[i] >= a.least && !a.none;
-        float f = kept ? load_one<ST>(a.x, r * a.x_stride + c) * a.scale : 0.0f;
-        if constexpr (RESIDUAL) f += load_one<ST>(a.residual, r * a.r_stride + c);
-        store_one<ST>(a.y, r * a.y_stride + c, f);
-        if (++c == a.cols) c = 0, ++r;
+        float f = kept ? load_one<ST>(a.x, row * a.x_stride + col) * a.scale : 0.0f;
+        if constexpr (RESIDUAL) f += load_one<ST>(a.residual, row * a.r_stride + col);
+        store_one<ST>(a.y, row * a.y_stride + col, f);
+        if (++col == a.cols) col = 0, ++row;
       }
     }
   }
@@ -124,18 +116,10 @@ template <int ST, bool RESIDUAL, bool PACKED>
 hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s) {
   constexpr int E = 16 / StorageTraits<ST>::bytes;
   const int64_t groups = (a.n + E - 1) / E;
-  // One group a thread until the chip is full, then four (their loads in flight
-  // together).
-  constexpr int U = 4;
-  if (groups >= int64_t{kBlock} * U * 2048) {
-    const int64_t blocks = (groups + kBlock * U - 1) / (kBlock * U);
-    hipLaunchKernelGGL((dropout_map<ST, RESIDUAL, PACKED, U>), dim3(static_cast<unsigned>(blocks)),
-                       dim3(kBlock), 0, s, a);
-  } else {
-    const int64_t blocks = (groups + kBlock - 1) / kBlock;
-    hipLaunchKernelGGL((dropout_map<ST, RESIDUAL, PACKED, 1>), dim3(static_cast<unsigned>(blocks)),
-                       dim3(kBlock), 0, s, a);
-  }
+  // at most 2^31 threads in a launch
+  const int64_t blocks = std::min<int64_t>((groups + kBlock - 1) / kBlock, (int64_t{1} << 31) / kBlock);
+  hipLaunchKernelGGL((dropout_map<ST, RESIDUAL, PACKED>), dim3(static_cast<unsigned>(blocks)),
+                     dim3(kBlock), 0, s, a);
   return hipGetLastError();
 }
 
@@ -161,7 +145,7 @@ extern "C" tbe_status tbe_dropout(const void* x, int64_t x_stride, const void* r
   const size_t e = dtype_bytes(dtype);
   if (!aligned_to(x, e) || !aligned_to(y, e) || (residual && !aligned_to(residual, e)))
     return TBE_ERR_INVALID_ARGUMENT;
-  if (rows > (int64_t{1} << 35) / cols) return TBE_ERR_UNSUPPORTED;  // 2^32 threads in a launch
+  if (rows > (int64_t{1} << 35) / cols) return TBE_ERR_UNSUPPORTED;
   DropoutArgs a{};
   a.x = x;
   a.residual = residual;
