@@ -8,6 +8,14 @@
 //   dinitial = a_0 lam_0
 // and the step that takes one token for each sequence.  States are fp32;
 // h, dx and dg are rounded once, to the rows' type.
+//
+// Every input is read and every output written once, 16 bytes a token and channel
+// of 16-bit rows for both directions, and memory would bound that: 4 sequences of
+// 16384 x 1024 bf16 move 1.0 GB, 194 us at a copy's 5.2 TB/s.  They take 271 us (3.7
+// TB/s), 8192 of about 20 x 256 175 us (4.1).  A tile waits 6 of its 11 us for the
+// states before it (reads and writes between XCDs, about a microsecond each way),
+// and of the rest about half is arithmetic: some 30 vector instructions a token and
+// channel forwards, 50 backwards.  With short sequences the wait is 3 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -54,6 +62,8 @@ __device__ __forceinline__ Gates gates(float g) {
 
 // --- one token for each sequence ---------------------------------------------
 
+// Four channels a thread, everything read and written once: 2048 x 128 fp32 take
+// 3.1 us, most of it the launch; 10 us a call with what the host does for it.
 template <int ST, bool SIGMOID>
 __global__ __launch_bounds__(kBlock) void step_kernel(const void* x, int64_t x_stride,
                                                       const void* gate, int64_t gate_stride,
@@ -254,9 +264,10 @@ __device__ int64_t sequence_before(const ScanArgs& a, int64_t token) {
 }
 
 // Waves in a tile: 4, or 8 where sequences span tiles.  Fewer wait less for each
-// other (8192 sequences of about 20 x 256 bf16: 64 and 100 us with 4, 70 and 113
-// with 8), more make the chain of tiles shorter (4 of 16384 x 1024 bf16: 127 and
-// 227 us with 8, 164 and 314 with 4).
+// other (8192 sequences of about 20 x 256 bf16: 63 and 104 us with 4, 76 and 144
+// with 8; 2048 of 1-32 x 100 fp32: 13 and 18, 14 and 22), more make the chain of
+// tiles shorter (4 of 16384 x 1024 bf16: 111 and 165 us with 8, 126 and 235 with 4;
+// 256 of 256 x 512: 49 and 81, 53 and 93; 256 of 128 x 512: both 28 and 46).
 constexpr int kFewWaves = 4, kManyWaves = 8;
 
 // What the waves of a tile share.
@@ -902,7 +913,9 @@ hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, int32_t kind, bool
 }
 
 // Channels a lane: two neighbours of 16-bit rows, where every row starts at an
-// even element and a wave's 128 channels are not mostly past the end.
+// even element and a wave's 128 channels are not mostly past the end (8192
+// sequences of about 20 x 256 bf16, both directions: 168 us, 179 with one; 4 of 16384
+// x 1024: 284 and 288).
 int lane_channels(const tbe_scan_input* in, const ScanArgs& a) {
   if (in->dtype == TBE_F32 || a.dim <= 64 || a.dim % 2) return 1;
   const auto even = [](const void* p, int64_t stride) { return aligned_to(p, 4) && stride % 2 == 0; };
