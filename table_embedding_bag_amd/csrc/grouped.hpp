@@ -498,9 +498,10 @@ template <int ST, Product P, typename S, bool DIRECT>
 __device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, unsigned char* lds) {
   constexpr bool kAKmaj = P == kForward, kBKmaj = P != kGradW;
   // Slices past LDS's two in registers: one where a slice's products take long enough
-  // for a load to arrive, three where tiles are small.
+  // for a load to arrive, two where tiles are small (three take longer to start: 8191 x
+  // 250 -> 130 fp32, both directions, 53 us instead of 51).
   constexpr bool kThroughLds = DIRECT && S::NS > 2;
-  constexpr int kAhead = !kThroughLds && S::NS > 2 ? 3 : 1;
+  constexpr int kAhead = !kThroughLds && S::NS > 2 ? 2 : 1;
   using OpA = Operand<ST, kAKmaj, S::TA, S::NW, DIRECT, S::RB, kAhead>;
   using OpB = Operand<ST, kBKmaj, S::TB, S::NW, DIRECT, S::RB, kAhead>;
   constexpr int BK = OpA::BK, KK = S::RB / 32;  // of a slice: values, steps of 32 bytes
@@ -914,17 +915,20 @@ using Narrow = Shape<128, 32, 4, 1, 4, 128>;
 // 41 with 64).  Large tiles need several rounds of the CUs (16384 rows in 8 groups,
 // 1024 -> 4096 bf16, 1152 of 256: 162 us, 177 with 128; 4096 -> 1024, 288 of 256: 183 and
 // 172; 32768 x 4096 -> 4096: 1.0 and 1.2 ms), tiles of 128 one (1024 -> 1024: 8192 rows,
-// 576 of them, 32 us, 41 with 64; 4096 rows, 320, 22 and 24; 2048 rows -> 512, 96, 14 and 11).
-inline int row_tile(const GroupedArgs& a, int64_t cols) {
+// 576 of them, 32 us, 41 with 64; 4096 rows, 320, 22 and 24; 2048 rows -> 512, 96, 14 and 11);
+// of fp32, whose products take 16 times as long, as many as large ones (1266 rows in 2
+// groups, 384 -> 4032, 352 of them, 61 us, 56 with 64).
+template <int ST>
+int row_tile(const GroupedArgs& a, int64_t cols) {
   const auto tiles = [&](int64_t t) { return (a.rows / t + a.groups) * ceil_div(cols, t); };
   if (a.rows <= a.groups * 32) return 32;
   if (tiles(256) >= 1024) return 256;
-  return tiles(128) >= 256 ? 128 : 64;
+  return tiles(128) >= (ST == kF32 ? 1024 : 256) ? 128 : 64;
 }
 
 template <int ST, Product P>
 hipError_t launch_rows(const GroupedArgs& a, hipStream_t s) {
-  const int tile = row_tile(a, P == kForward ? a.M : a.K);
+  const int tile = row_tile<ST>(a, P == kForward ? a.M : a.K);
   return tile == 256   ? launch_product<ST, P, Large>(a, s)
          : tile == 128 ? launch_product<ST, P, Medium>(a, s)
          : tile == 64  ? launch_product<ST, P, Square>(a, s)
@@ -938,7 +942,7 @@ hipError_t launch_backward(const GroupedArgs& a, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (a.dw) {
     const GradWPlan plan = plan_grad_w(a.rows, a.groups, a.K, a.M, dtype);
-    const bool both = dx && row_tile(a, a.K) == plan.tile;
+    const bool both = dx && row_tile<ST>(a, a.K) == plan.tile;
     if (dx && !both) e = launch_rows<ST, kGradX>(a, s);
     if (e != hipSuccess) return e;
     e = plan.tile == 256   ? (both ? launch_gradients<ST, Large>(a, s)
