@@ -12,7 +12,7 @@
 // PFLOP/s): five rounds of large tiles where 4.4 would do, and tiles of 128 that LDS
 // bounds.  With few rows the weights' reading counts: 64 rows over 64 groups, 512 ->
 // 2048, 18 us (4.7 TB/s of the weights that have rows).  Small ones are a few
-// latencies: 8191 x 250 -> 130 fp32, both directions, 49 us in three launches.
+// latencies: 8191 x 250 -> 130 fp32, both directions, 48 us in three launches.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -29,10 +29,10 @@ hipError_t launch(const GroupedArgs& a, int32_t dtype, bool backward, hipStream_
                             : launch_grouped_bf16(a, backward, s);
 }
 
-// Rows that are whole 16-byte chunks at aligned addresses.
-bool chunked(const void* p, int64_t stride, int64_t width, int32_t dtype) {
+RowLayout layout_of(const void* p, int64_t stride, int64_t width, int32_t dtype) {
   const int64_t b = dtype_bytes(dtype);
-  return aligned_to(p, 16) && stride * b % 16 == 0 && width * b % 16 == 0;
+  if (aligned_to(p, 16) && stride * b % 16 == 0 && width * b % 16 == 0) return kChunkRows;
+  return aligned_to(p, 4) && stride * b % 4 == 0 ? kWordRows : kOddRows;
 }
 
 // Longest rows and strides: 256 of them lie within a buffer descriptor's reach.
@@ -103,7 +103,8 @@ tbe_status tbe_grouped_linear(const void* x, int64_t x_stride, const void* weigh
   a.y = y;
   a.y_stride = y_stride;
   a.index64 = index_dtype == TBE_I64;
-  a.direct = chunked(x, x_stride, in_features, dtype) && chunked(weight, in_features, in_features, dtype);
+  a.layout = std::min(layout_of(x, x_stride, in_features, dtype),
+                      layout_of(weight, in_features, in_features, dtype));
   return launch(a, dtype, false, static_cast<hipStream_t>(stream)) == hipSuccess
              ? TBE_OK
              : TBE_ERR_HIP;
@@ -155,9 +156,9 @@ tbe_status tbe_grouped_linear_backward(const void* x, int64_t x_stride, const vo
     a.bias_parts = a.parts + plan.slots * out_features * in_features;
   }
   a.index64 = index_dtype == TBE_I64;
-  a.direct = chunked(x, x_stride, in_features, dtype) &&
-             chunked(weight, in_features, in_features, dtype) &&
-             chunked(grad, grad_stride, out_features, dtype);
+  a.layout = std::min({layout_of(x, x_stride, in_features, dtype),
+                       layout_of(weight, in_features, in_features, dtype),
+                       layout_of(grad, grad_stride, out_features, dtype)});
   return launch(a, dtype, true, static_cast<hipStream_t>(stream)) == hipSuccess
              ? TBE_OK
              : TBE_ERR_HIP;

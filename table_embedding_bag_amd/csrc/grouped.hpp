@@ -20,14 +20,14 @@
 //   free-major  row k of the slice at k * (tile width), 16-bit chunks c at slot
 //               c ^ 4 (k & 3): the transposing LDS read takes 4 rows x 16 columns
 //               for each 16 lanes, and this spreads the rows over the banks.
-// Slices come by one of two ways.  Through registers, a slice ahead of LDS: the
-// registers are a third buffer beside LDS's two, so a load has a whole slice's
+// Slices come by one of two ways.  Through registers, a slice or two ahead of LDS:
+// the registers are buffers beside LDS's two, so a load has a whole slice's
 // products to arrive.  Or, where tiles are small and memory is what counts, from
 // memory to LDS directly, several slices ahead (aligned operands only).
 // All loads are buffer loads, whose descriptor's bounds give zeros past the rows'
-// and the group's ends.  Where rows are not whole aligned chunks, a chunk is
-// loaded as the aligned words it lies in and shifted into place, and what
-// follows a row's end is masked in the last slice.
+// and the group's ends.  Where rows are not whole aligned chunks, what follows a
+// row's end is masked in the last slice; where they start between words, a chunk
+// is loaded as the aligned words it lies in and shifted into place.
 #pragma once
 
 #include <type_traits>
@@ -35,6 +35,10 @@
 #include "layers.hpp"
 
 namespace tbe {
+
+// Rows of operands: of whole 16-byte chunks at aligned addresses; starting at
+// multiples of 4 bytes; or, of 2-byte values, at any.
+enum RowLayout { kOddRows, kWordRows, kChunkRows };
 
 struct GroupedArgs {
   int64_t rows, groups, K, M;  // K = in_features, M = out_features
@@ -49,7 +53,7 @@ struct GroupedArgs {
   void* db;
   int64_t x_stride, y_stride, grad_stride, dx_stride;
   int32_t index64;
-  int32_t direct;      // every operand's rows are whole, aligned 16-byte chunks
+  int32_t layout;      // kOddRows, kWordRows or kChunkRows, of every operand
   // The weights' gradient: groups of more than chunk rows are summed in chunks
   // (0: never), whose sums go to parts [slots][M * K] and bias_parts [slots][M].
   int64_t chunk, slots;
@@ -249,14 +253,16 @@ __device__ int64_t ranked_group(const GroupedArgs& a, int64_t r) {
 //   KMAJ: `free` rows of the tile at base + r * stride, the summed index along them.
 //   else: rows of the summed index at base + k * stride, `free` columns along them.
 //   AHEAD slices are held in registers where they come that way.
-template <int ST, bool KMAJ, int R, int NW, bool DIRECT, int RB, int AHEAD>
+template <int ST, bool KMAJ, int R, int NW, int LAYOUT, int RB, int AHEAD>
 struct Operand {
+  static constexpr bool DIRECT = LAYOUT == kChunkRows;
   static constexpr int bytes = StorageTraits<ST>::bytes;
   static constexpr int EL = 16 / bytes;            // values in a chunk
   static constexpr int BK = RB / bytes;     // summed values in a slice
   static constexpr int CPR = KMAJ ? RB / 16 : R * bytes / 16;  // chunks in a row
   static constexpr int NL = R * RB / 16 / (64 * NW);     // chunks a thread
-  static constexpr bool SHIFT = !DIRECT && bytes == 2;  // rows may start between words
+  static constexpr bool SHIFT = LAYOUT == kOddRows;     // rows may start between words
+  static_assert(!SHIFT || bytes == 2);
   static constexpr int kFragmentReads = KMAJ ? 1 : bytes == 2 ? 2 : 4;
   static_assert(NL >= 1, "every thread has a chunk");
 
@@ -313,7 +319,7 @@ struct Operand {
     if constexpr (KMAJ) extent = (free - 1) * stride + static_cast<int64_t>(left) * bytes;
     else extent = ((left < BK ? left : BK) - 1) * stride + static_cast<int64_t>(free) * bytes;
     // up to the end of the word that holds the last value
-    if constexpr (SHIFT) extent = (extent + skew + 3) & ~int64_t{3};
+    if constexpr (!DIRECT && bytes == 2) extent = (extent + skew + 3) & ~int64_t{3};
     records = left > 0 ? static_cast<uint32_t>(extent) : 0u;
   }
   // ... and, directly, the load of the thread's i-th chunk of it into the slice at `to`.
@@ -490,20 +496,20 @@ __device__ __forceinline__ void wait_loads() {
 }
 
 // LDS's buffers: for slices that come by registers two.
-template <typename S, bool DIRECT>
-constexpr int kLdsBytes = (DIRECT && S::NS > 2 ? S::NS : 2) * S::stage;
+template <typename S, int LAYOUT>
+constexpr int kLdsBytes = (LAYOUT == kChunkRows && S::NS > 2 ? S::NS : 2) * S::stage;
 
 // Tile `id` of a product.
-template <int ST, Product P, typename S, bool DIRECT>
+template <int ST, Product P, typename S, int LAYOUT>
 __device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, unsigned char* lds) {
   constexpr bool kAKmaj = P == kForward, kBKmaj = P != kGradW;
   // Slices past LDS's two in registers: one where a slice's products take long enough
   // for a load to arrive, two where tiles are small (three take longer to start: 8191 x
   // 250 -> 130 fp32, both directions, 53 us instead of 51).
-  constexpr bool kThroughLds = DIRECT && S::NS > 2;
+  constexpr bool kThroughLds = LAYOUT == kChunkRows && S::NS > 2;
   constexpr int kAhead = !kThroughLds && S::NS > 2 ? 2 : 1;
-  using OpA = Operand<ST, kAKmaj, S::TA, S::NW, DIRECT, S::RB, kAhead>;
-  using OpB = Operand<ST, kBKmaj, S::TB, S::NW, DIRECT, S::RB, kAhead>;
+  using OpA = Operand<ST, kAKmaj, S::TA, S::NW, LAYOUT, S::RB, kAhead>;
+  using OpB = Operand<ST, kBKmaj, S::TB, S::NW, LAYOUT, S::RB, kAhead>;
   constexpr int BK = OpA::BK, KK = S::RB / 32;  // of a slice: values, steps of 32 bytes
   constexpr int bytes = StorageTraits<ST>::bytes;
 
@@ -775,20 +781,20 @@ __device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, unsig
   }
 }
 
-template <int ST, Product P, typename S, bool DIRECT>
+template <int ST, Product P, typename S, int LAYOUT>
 __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
-  __shared__ __align__(1024) unsigned char lds[kLdsBytes<S, DIRECT>];
-  product<ST, P, S, DIRECT>(a, blockIdx.x, lds);
+  __shared__ __align__(1024) unsigned char lds[kLdsBytes<S, LAYOUT>];
+  product<ST, P, S, LAYOUT>(a, blockIdx.x, lds);
 }
 
 // Both gradients' products where their tiles have one shape: the second's fill the
 // CUs that the first's last round leaves idle.  `first` workgroups, a multiple of
 // the XCDs, have the weights'.
-template <int ST, typename S, bool DIRECT>
+template <int ST, typename S, int LAYOUT>
 __global__ __launch_bounds__(S::threads) void grouped_gradients(GroupedArgs a, uint32_t first) {
-  __shared__ __align__(1024) unsigned char lds[kLdsBytes<S, DIRECT>];
-  if (blockIdx.x < first) product<ST, kGradW, S, DIRECT>(a, blockIdx.x, lds);
-  else product<ST, kGradX, S, DIRECT>(a, blockIdx.x - first, lds);
+  __shared__ __align__(1024) unsigned char lds[kLdsBytes<S, LAYOUT>];
+  if (blockIdx.x < first) product<ST, kGradW, S, LAYOUT>(a, blockIdx.x, lds);
+  else product<ST, kGradX, S, LAYOUT>(a, blockIdx.x - first, lds);
 }
 
 // The chunks' sums of a group, first chunk first, to its gradients.
@@ -876,13 +882,23 @@ int64_t workgroups(const GroupedArgs& a) {
   return na * units * (P == kGradW ? ceil_div(a.M, S::TB) : 1);
 }
 
+// f(the layout, known to the compiler).  (16384 rows in 8 groups, 1022 -> 1022 bf16,
+// forward: 67 us as odd rows, 60 as rows of words; 4094 -> 4094: 605 and 526; as chunks
+// 1024 -> 1024 42, 4096 -> 4096 469.)
+template <int ST, typename F>
+void with_layout(const GroupedArgs& a, F f) {
+  if (a.layout == kChunkRows) return f(std::integral_constant<int, kChunkRows>{});
+  if constexpr (StorageTraits<ST>::bytes == 2)
+    if (a.layout == kOddRows) return f(std::integral_constant<int, kOddRows>{});
+  f(std::integral_constant<int, kWordRows>{});
+}
+
 template <int ST, Product P, typename S>
 hipError_t launch_product(const GroupedArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(workgroups<P, S>(a)));
-  if (a.direct)
-    hipLaunchKernelGGL((grouped_product<ST, P, S, true>), grid, dim3(S::threads), 0, s, a);
-  else
-    hipLaunchKernelGGL((grouped_product<ST, P, S, false>), grid, dim3(S::threads), 0, s, a);
+  with_layout<ST>(a, [&](auto layout) {
+    hipLaunchKernelGGL((grouped_product<ST, P, S, layout>), grid, dim3(S::threads), 0, s, a);
+  });
   return hipGetLastError();
 }
 
@@ -890,12 +906,10 @@ template <int ST, typename S>
 hipError_t launch_gradients(const GroupedArgs& a, hipStream_t s) {
   const int64_t first = (workgroups<kGradW, S>(a) + 7) / 8 * 8;
   const dim3 grid(static_cast<unsigned>(first + workgroups<kGradX, S>(a)));
-  if (a.direct)
-    hipLaunchKernelGGL((grouped_gradients<ST, S, true>), grid, dim3(S::threads), 0, s, a,
+  with_layout<ST>(a, [&](auto layout) {
+    hipLaunchKernelGGL((grouped_gradients<ST, S, layout>), grid, dim3(S::threads), 0, s, a,
                        static_cast<uint32_t>(first));
-  else
-    hipLaunchKernelGGL((grouped_gradients<ST, S, false>), grid, dim3(S::threads), 0, s, a,
-                       static_cast<uint32_t>(first));
+  });
   return hipGetLastError();
 }
 

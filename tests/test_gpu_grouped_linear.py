@@ -278,3 +278,31 @@ def test_both_gradients_in_workgroups_rounded_up(name, G, N, K, M, dtype):
             bound = (terms + 2) * ref.U32 * size
             bound = bound + ref.half_step(p.dtype) * (want.abs() + bound) + ref.TINY[p.dtype]
             assert (off <= bound).all(), (what, i, float((off / bound).max()))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("sizes", list(SIZES))
+@pytest.mark.parametrize("K,M,wide", [(130, 134, 0), (2, 6, 2), (66, 258, 6), (262, 70, 4)])
+def test_rows_of_words(sizes, K, M, wide, dtype):
+    """Rows of 2-byte values that start at multiples of 4 bytes, but not of 16."""
+    print(f"[grouped] words {sizes} {K} {M} {wide} {dtype}", flush=True)
+    Problem(SIZES[sizes], K, M, DTYPES[dtype], seed=24, wide=wide).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_odd_columns_in_rows_of_words(dtype):
+    """An odd number of columns, whose last shares its word with what follows the row: that is NaN
+    here, and reaches no output."""
+    print(f"[grouped] odd columns {dtype}", flush=True)
+    p = Problem([70, 0, 3, 200], 34, 37, DTYPES[dtype], seed=25)
+    for name, cols in (("x", 34), ("grad", 37)):
+        buf = torch.full((p.N, 40 if name == "grad" else 34 + 4), float("nan"), dtype=p.dtype, device="cuda")
+        buf[:, :cols] = getattr(p, name)
+        setattr(p, name, buf[:, :cols])
+    p.check()
+
+
+@pytest.mark.parametrize("name,G,N,K,M", [("forward", 12, 12801, 262, 4098), ("dx", 12, 12801, 4098, 262),
+                                          ("dw", 64, 2600, 1042, 1038), ("128", 3, 16000, 1098, 1030)])
+def test_many_tiles_of_rows_of_words(name, G, N, K, M):
+    test_many_tiles(name, G, N, K, M, 0, "bf16")
