@@ -137,28 +137,17 @@ __device__ __forceinline__ int64_t group_offset(const GroupedArgs& a, int64_t g)
   return o < 0 ? 0 : (o > a.rows ? a.rows : o);
 }
 
-// Which tile of the groups' ragged tilings a workgroup takes.  Workgroups go
-// round robin to the XCDs; each XCD takes a contiguous range of tiles, and
-// within a group the tiles run in bands of 8 row tiles, so that what an XCD
-// works on at one time shares operand tiles in its L2.
+// Which tile of the groups' ragged tilings a workgroup takes.
 struct Tile {
   int64_t group, first, end;  // rows of the group
   int64_t ta, tb;             // tile numbers along A's and B's free index
 };
 
-__device__ __forceinline__ void band_order(int64_t q, int64_t na, int64_t nb, Tile* t) {
-  constexpr int64_t kBand = 8;
-  const int64_t band = q / (kBand * na), r = q - band * kBand * na;
-  const int64_t height = nb - band * kBand < kBand ? nb - band * kBand : kBand;
-  t->ta = r / height;
-  t->tb = band * kBand + r % height;
-}
-
 // Row tiles of TB rows, `na` tiles along the other index; false where the
 // workgroup has none.  Every wave works it out for itself: 64 groups at a time,
 // and with no more than that from one read of the offsets.
 template <int TB>
-__device__ bool find_row_tile(const GroupedArgs& a, uint32_t id, int64_t na, Tile* t) {
+__device__ bool find_row_tile(const GroupedArgs& a, uint32_t id, uint32_t blocks, int64_t na, Tile* t) {
   const int lane = lane_id();
   uint32_t lo = 0, rows = 0, tiles = 0, incl = 0;  // of the lane's group
   const auto take = [&](int64_t g0) {
@@ -176,9 +165,8 @@ __device__ bool find_row_tile(const GroupedArgs& a, uint32_t id, int64_t na, Til
     take(g0);
     total += __builtin_amdgcn_readlane(incl, 63);
   }
-  total *= na;
-  if (static_cast<int64_t>(id) >= total) return false;
-  int64_t q = xcd_contiguous_block(static_cast<int>(id), static_cast<int>(total));
+  int64_t q;
+  if (!tile_number(id, blocks, total * na, &q)) return false;
   for (int64_t g0 = 0; g0 < a.groups; g0 += 64) {
     if (a.groups > 64) take(g0);
     const uint64_t past = __ballot(static_cast<int64_t>(incl) * na > q);
@@ -188,7 +176,7 @@ __device__ bool find_row_tile(const GroupedArgs& a, uint32_t id, int64_t na, Til
       t->group = g0 + l;
       t->first = __builtin_amdgcn_readlane(lo, l);
       t->end = t->first + __builtin_amdgcn_readlane(rows, l);
-      band_order(q - before * na, na, __builtin_amdgcn_readlane(tiles, l), t);
+      band_order(q - before * na, na, __builtin_amdgcn_readlane(tiles, l), &t->ta, &t->tb);
       return true;
     }
     q -= static_cast<int64_t>(__builtin_amdgcn_readlane(incl, 63)) * na;
@@ -513,9 +501,10 @@ __device__ __forceinline__ void wait_loads() {
 template <typename S, int LAYOUT>
 constexpr int kLdsBytes = (LAYOUT == kChunkRows && S::NS > 2 ? S::NS : 2) * S::stage;
 
-// Tile `id` of a product.
+// The tile that workgroup `id` of a product's `blocks` takes.
 template <int ST, Product P, typename S, int LAYOUT>
-__device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, unsigned char* lds) {
+__device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, uint32_t blocks,
+                                        unsigned char* lds) {
   constexpr bool kAKmaj = P == kForward, kBKmaj = P != kGradW;
   // Slices past LDS's two in registers: one where a slice's products take long enough
   // for a load to arrive, two where tiles are small (three take longer to start: 8191 x
@@ -551,9 +540,9 @@ __device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, unsig
       t.end = group_offset(a, t.group + 1);
       if (t.end < t.first) t.end = t.first;
     }
-    band_order(q, na, nb, &t);
+    band_order(q, na, nb, &t.ta, &t.tb);
   } else {
-    if (!find_row_tile<S::TB>(a, id, na, &t)) return;
+    if (!find_row_tile<S::TB>(a, id, blocks, na, &t)) return;
   }
   const int64_t a0 = t.ta * S::TA, b0 = t.tb * S::TB;
   const int64_t out_rows = P == kGradW ? a.M - b0 : t.end - t.first - b0;
@@ -798,7 +787,7 @@ __device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, unsig
 template <int ST, Product P, typename S, int LAYOUT>
 __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
   __shared__ __align__(1024) unsigned char lds[kLdsBytes<S, LAYOUT>];
-  product<ST, P, S, LAYOUT>(a, blockIdx.x, lds);
+  product<ST, P, S, LAYOUT>(a, blockIdx.x, gridDim.x, lds);
 }
 
 // Both gradients' products where their tiles have one shape: the second's fill the
@@ -807,8 +796,8 @@ __global__ __launch_bounds__(S::threads) void grouped_product(GroupedArgs a) {
 template <int ST, typename S, int LAYOUT>
 __global__ __launch_bounds__(S::threads) void grouped_gradients(GroupedArgs a, uint32_t first) {
   __shared__ __align__(1024) unsigned char lds[kLdsBytes<S, LAYOUT>];
-  if (blockIdx.x < first) product<ST, kGradW, S, LAYOUT>(a, blockIdx.x, lds);
-  else product<ST, kGradX, S, LAYOUT>(a, blockIdx.x - first, lds);
+  if (blockIdx.x < first) product<ST, kGradW, S, LAYOUT>(a, blockIdx.x, first, lds);
+  else product<ST, kGradX, S, LAYOUT>(a, blockIdx.x - first, gridDim.x - first, lds);
 }
 
 // The chunks' sums of a group, first chunk first, to its gradients.

@@ -1,0 +1,67 @@
+"""Which tile each workgroup of the grouped linear layer takes, worked out on the CPU by the
+kernels' own arithmetic (csrc/tiles.hpp)."""
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(os.path.dirname(HERE), "table_embedding_bag_amd", "csrc")
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("tiles") / "tiles.so")
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", "-I" + CSRC, "-o", out,
+                           os.path.join(HERE, "grouped_tiles_host.cpp")])
+    lib = ctypes.CDLL(out)
+    lib.row_tiles.restype = ctypes.c_int64
+    return lib
+
+
+def _row_tiles(host, offsets, rows, cols, TB, TA, count=True):
+    """(workgroups with a tile, lowest row, highest row, times each tile was taken)"""
+    off = np.ascontiguousarray(offsets, dtype=np.int64)
+    groups, na = len(off) - 1, -(-cols // TA)
+    blocks = na * (rows // TB + min(groups, rows))      # as launched
+    c = np.clip(off, 0, rows)
+    tiles = int((-(-np.maximum(np.diff(c), 0) // TB) * na).sum())
+    taken = np.zeros(tiles, dtype=np.int32) if count else None
+    lo, hi = ctypes.c_int64(), ctypes.c_int64()
+    i64 = ctypes.c_int64
+    n = host.row_tiles(off.ctypes.data_as(ctypes.c_void_p), i64(groups), i64(rows), i64(blocks), i64(na),
+                       i64(TB), ctypes.byref(lo), ctypes.byref(hi),
+                       taken.ctypes.data_as(ctypes.c_void_p) if count else None)
+    return n, lo.value, hi.value, taken
+
+
+@pytest.mark.parametrize("TB,TA", [(256, 256), (128, 128), (64, 64), (32, 128)])
+def test_every_tile_is_taken_once(host, TB, TA):
+    r = np.random.default_rng(TB)
+    for groups, rows, cols in ((1, 1, 1), (3, 700, 300), (70, 5000, 520), (8, 8191, 1000), (200, 130, 129)):
+        off = np.concatenate([[0], np.cumsum(r.multinomial(rows, r.dirichlet(np.full(groups, 0.3))))])
+        n, lo, hi, taken = _row_tiles(host, off, rows, cols, TB, TA)
+        assert n == len(taken) and (taken == 1).all() and (lo, hi) == (0, rows - 1)
+
+
+def test_groups_that_overlap_by_more_than_the_launch_holds(host):
+    """4096 groups, every other one all of 131072 rows: 2^31 tiles of 32 rows x 128 columns, where
+    the launch has 2^21 workgroups."""
+    off = np.arange(4097) % 2 * 131072
+    n, lo, hi, _ = _row_tiles(host, off, 131072, 32768, 32, 128, count=False)
+    assert n == 0   # none is taken
+
+
+@pytest.mark.parametrize("TB,TA", [(256, 256), (64, 64), (32, 128)])
+def test_bad_offsets_stay_within_the_rows(host, TB, TA):
+    r = np.random.default_rng(TB + 1)
+    for i in range(60):
+        groups, rows = int(r.integers(1, 300)), int(r.integers(1, 9000))
+        spread = int(r.choice([rows, 4 * rows, 2 ** 62]))
+        off = r.integers(-spread, spread, groups + 1)
+        if i % 3 == 0:
+            off = np.arange(groups + 1) % 2 * rows
+        n, lo, hi, taken = _row_tiles(host, off, rows, int(r.integers(1, 3000)), TB, TA)
+        assert n >= 0 and lo >= 0 and hi < rows and (taken <= 1).all(), (i, groups, rows)
