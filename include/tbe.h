@@ -401,6 +401,11 @@ tbe_status tbe_scan_step(const void* x, int64_t x_stride, const void* gate, int6
  * token (NULL: zeros; stride 0: one row for all).  tokens and seqs are
  * below 2^31 - 1, dim and the strides of rows at most 2^23, tokens rounded up
  * to 512 and dim rounded up to 64 have a product below 2^35.
+ * States pass along a sequence through products of up to 1024 gates in fp32.
+ * Gates above 1 may take such a product past fp32's range: a state (or a
+ * gradient) of 0 stays 0, another may come out infinite or NaN where one token
+ * after another would not.  A product that underflows counts as 0; an infinite
+ * state times that is NaN.
  * max_polls: how often a part of a sequence looks for the state of the part
  * before it until it works that state out by itself (0: 2^16; below 0: never
  * looks): it changes the time and fp32 rounding, never what is computed. */

@@ -305,11 +305,26 @@ struct Entry {
     return __all(known) ? kState : __all(paired) ? kPair : kAbsent;
   }
 };
+// GROWS: gates may be above 1, and their products infinite.
+// The product of gates' products: 0 where either is, also beside an infinite one.  (A
+// gate that is itself infinite or NaN shows in B.)
+template <bool GROWS>
+__device__ __forceinline__ float times(float A, float a) {
+  return GROWS && (A == 0.0f || a == 0.0f) ? 0.0f : A * a;
+}
+// The state after tokens of which (A, B) is the pair.  B is the state they make of 0,
+// token after token, so 0 needs no product: 0 times an infinite A would be NaN.
+template <bool GROWS>
+__device__ __forceinline__ float after(float A, float state, float B) {
+  return GROWS && state == 0.0f ? B : fmaf(A, state, B);
+}
+template <bool GROWS>
+__device__ __forceinline__ float after(uint64_t pair, float state) {
+  return after<GROWS>(__uint_as_float(static_cast<uint32_t>(pair)), state,
+                      __uint_as_float(static_cast<uint32_t>(pair >> 32)));
+}
 __device__ __forceinline__ float pair_a(uint64_t p) {
   return __uint_as_float(static_cast<uint32_t>(p));
-}
-__device__ __forceinline__ float pair_b(uint64_t p) {
-  return __uint_as_float(static_cast<uint32_t>(p >> 32));
 }
 
 // A tile's start state per channel (the state after its predecessor in scan
@@ -317,7 +332,7 @@ __device__ __forceinline__ float pair_b(uint64_t p) {
 // k follows tile k - 1, -1 where it follows tile k + 1; tiles and groups are
 // numbered in scan order here.  walk(start) works the start state out from the
 // inputs, for waits that give up.
-template <int V, int W, int T, int STEP, typename Walk>
+template <int V, int W, int T, int STEP, bool GROWS, typename Walk>
 __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w, int64_t tile,
                                            int64_t c0, bool mine, TileShared<V, W, T>& sh,
                                            float (&start)[V], Walk walk) {
@@ -338,8 +353,8 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float wa = sh.A[i][lane * V + v], wb = sh.B[i][lane * V + v];
-      B[v] = r ? wb : fmaf(wa, B[v], wb);
-      A[v] *= wa;
+      B[v] = r ? wb : after<GROWS>(wa, B[v], wb);
+      A[v] = times<GROWS>(A[v], wa);
     }
   }
   const int64_t at = k * a.dim + c0, group_at = group * a.dim + c0;
@@ -405,13 +420,13 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const uint64_t p = sh.pair[e][lane * V + v];
-          gb[v] = fmaf(pair_a(p), gb[v], pair_b(p));
-          ga[v] *= pair_a(p);
+          gb[v] = after<GROWS>(p, gb[v]);
+          ga[v] = times<GROWS>(ga[v], pair_a(p));
         }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        gb[v] = fmaf(A[v], gb[v], B[v]);
-        ga[v] *= A[v];
+        gb[v] = after<GROWS>(A[v], gb[v], B[v]);
+        ga[v] = times<GROWS>(ga[v], A[v]);
         if (mine) st_pair(w.group.pairs + group_at + v, ga[v], gb[v]);
       }
     }
@@ -455,10 +470,10 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const uint64_t p = sh.group_pair[e][lane * V + v];
-          start[v] = fmaf(pair_a(p), start[v], pair_b(p));
+          start[v] = after<GROWS>(p, start[v]);
         }
 #pragma unroll
-      for (int v = 0; v < V; ++v) gb[v] = fmaf(ga[v], start[v], gb[v]);  // the group's end
+      for (int v = 0; v < V; ++v) gb[v] = after<GROWS>(ga[v], start[v], gb[v]);  // the group's end
     }
   }
   if (given_up) {
@@ -474,7 +489,7 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const uint64_t p = sh.pair[e][lane * V + v];
-        start[v] = fmaf(pair_a(p), start[v], pair_b(p));
+        start[v] = after<GROWS>(p, start[v]);
       }
   }
   if (wave == 0 && last && !reset) {
@@ -482,12 +497,12 @@ __device__ __forceinline__ void join_tiles(const ScanArgs& a, const ScanWork& w,
     for (int v = 0; v < V; ++v)
       if (mine)
         st_state(w.group.states + group_at + v,
-                 chained && !given_up ? gb[v] : fmaf(A[v], start[v], B[v]));
+                 chained && !given_up ? gb[v] : after<GROWS>(A[v], start[v], B[v]));
   }
 }
 
 // The state a wave starts from: the tile's, taken through the waves before it.
-template <int V, int W, int T, int STEP>
+template <int V, int W, int T, int STEP, bool GROWS>
 __device__ __forceinline__ void wave_start(const TileShared<V, W, T>& sh, int wave, int lane,
                                            float (&state)[V]) {
 #pragma unroll 2
@@ -498,7 +513,7 @@ __device__ __forceinline__ void wave_start(const TileShared<V, W, T>& sh, int wa
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float wb = sh.B[i][lane * V + v];
-        state[v] = r ? wb : fmaf(sh.A[i][lane * V + v], state[v], wb);
+        state[v] = r ? wb : after<GROWS>(sh.A[i][lane * V + v], state[v], wb);
       }
     }
   }
@@ -508,6 +523,15 @@ __device__ __forceinline__ void wave_start(const TileShared<V, W, T>& sh, int wa
 // operations on a span's values off until they are used, holds more than their
 // results in the meantime, and spills.
 __device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
+
+// Whether the products of all the wave's channels are finite.
+template <int V>
+__device__ __forceinline__ bool finite(const float (&A)[V]) {
+  bool f = true;
+#pragma unroll
+  for (int v = 0; v < V; ++v) f = f && __builtin_isfinite(A[v]);
+  return __all(f);
+}
 
 // A buffer descriptor: loads past `bytes` give 0, stores there are dropped.  The
 // spans' loads and stores go through these, so that no branch parts them and all
@@ -700,6 +724,16 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
   };
   if (plain) reduce(std::true_type{});
   else reduce(std::false_type{});
+  if constexpr (!SIGMOID) {
+    if (!finite(A)) {  // gates above 1 that pass fp32's range, maybe with one of 0 behind
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        A[v] = 1.0f;
+#pragma unroll
+        for (int i = 0; i < T; ++i) A[v] = times<true>(A[v], k[i][v]);
+      }
+    }
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     sh.A[wave][lane * V + v] = A[v];
@@ -708,7 +742,7 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
   if (lane == 0) sh.resets[wave] = first;
   __syncthreads();
   float state[V];
-  join_tiles<V, W, T, 1>(a, w, tile, c0, mine, sh, state, [&](float (&v)[V]) {
+  join_tiles<V, W, T, 1, !SIGMOID>(a, w, tile, c0, mine, sh, state, [&](float (&v)[V]) {
     // the sequence that the tile's first token goes on
     const int64_t end = tile * (W * T), s = sequence_before(a, end);
     if (s < 0 || s >= a.seqs) return;
@@ -722,7 +756,7 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles(ScanArgs a, ScanWork w) 
       }
     }
   });
-  wave_start<V, W, T, 1>(sh, wave, lane, state);
+  wave_start<V, W, T, 1, !SIGMOID>(sh, wave, lane, state);
   const Span carry = span<kF32>(a.carry, a.dim, t0 / kCarry, (tokens + kCarry - 1) / kCarry, c,
                                          a.dim);
   const Span h = span<ST>(a.h, a.dim, t0, tokens, c, a.dim);
@@ -822,6 +856,33 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
   };
   if (plain) reduce(std::true_type{});
   else reduce(std::false_type{});
+  // Gates above 1, whose products pass fp32's range, make terms of that sum infinite or
+  // NaN.  Then both once more, mu_0 token after token, from memory: rare, and registers
+  // are full.
+  if constexpr (!SIGMOID) {
+    if (!finite(A)) {
+      bool again[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        again[v] = mine && !__builtin_isfinite(A[v]);
+        if (again[v]) A[v] = 1.0f, B[v] = 0.0f;
+      }
+#pragma unroll 1
+      for (int i = tokens - 1; i >= 0; --i) {
+        const bool l = last >> i & 1u;
+        const int64_t t = t0 + i, s = __builtin_amdgcn_readlane(ends, i);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (!again[v]) continue;
+          float ut = a.grad_h ? load_one<ST>(a.grad_h, t * a.grad_h_stride + c0 + v) : 0.0f;
+          if (l && a.grad_final) ut += a.grad_final[s * a.grad_final_stride + c0 + v];
+          const float at_ = load_one<ST>(a.gate, t * a.gate_stride + c0 + v);
+          A[v] = times<true>(A[v], at_);
+          B[v] = at_ * (l ? ut : ut + B[v]);
+        }
+      }
+    }
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     sh.A[wave][lane * V + v] = A[v];
@@ -830,7 +891,7 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
   if (lane == 0) sh.resets[wave] = last;
   __syncthreads();
   float mu[V];
-  join_tiles<V, W, T, -1>(a, w, tile, c0, mine, sh, mu, [&](float (&v)[V]) {
+  join_tiles<V, W, T, -1, !SIGMOID>(a, w, tile, c0, mine, sh, mu, [&](float (&v)[V]) {
     // the sequence that the token after the tile goes on
     const int64_t begin = (tile + 1) * (W * T);
     const int64_t s = sequence_before(a, begin);
@@ -845,7 +906,7 @@ __global__ __launch_bounds__(64 * W, 4) void scan_tiles_back(ScanArgs a, ScanWor
       }
     }
   });
-  wave_start<V, W, T, -1>(sh, wave, lane, mu);
+  wave_start<V, W, T, -1, !SIGMOID>(sh, wave, lane, mu);
   const Span dxs = span<ST>(a.dx, a.dx_stride, t0, tokens, c, a.dim);
   const Span dgs = span<ST>(a.dgate, a.dgate_stride, t0, tokens, c, a.dim);
   if constexpr (kAgain) {

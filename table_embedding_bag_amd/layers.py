@@ -224,6 +224,10 @@ def scan_forward(x, gate, offsets, initial=None, gate_kind="sigmoid", need_carry
     (None: zeros).  gate_kind "sigmoid": a = sigmoid(gate), b = 1 - a; "decay": a = gate, b = 1.
     Returns (h [N, D] in x's type, final fp32 [S, D], carry): carry is what scan_backward needs
     (None without need_carry).  An empty sequence's final state is its initial one.
+
+    States pass along a sequence through products of up to 1024 gates in fp32.  Where gates above
+    1 take such a product past fp32's range, a state of 0 stays 0, another may come out infinite
+    or NaN where one token after another would not; the same holds for the gradients.
     """
     S, inp = _scan_input(x, gate, offsets, initial, gate_kind)
     device = _on_one_gpu(x, gate, offsets, initial)
