@@ -469,6 +469,31 @@ __device__ __forceinline__ void store_fragment(void* p, const f32x16& v, int64_t
   }
 }
 
+// A long sum in two floats: what each addition rounds off is exact in fp32 and added up
+// beside it, so that the sum is off by some half steps of itself whatever its length.
+// (One float's additions round one way once the sum is large: 32768 rows of 0.1 came out
+// 1.5e-4 off.)
+struct LongSum {
+  float sum = 0.0f, low = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float s = sum + v, from = s - sum;
+    low += (sum - (s - from)) + (v - from);
+    sum = s;
+  }
+  // An infinite sum leaves NaN in low.
+  __device__ __forceinline__ float value() const {
+    return __builtin_isfinite(low) ? sum + low : sum;
+  }
+};
+// The sum of a few values, two by two.
+template <int N>
+__device__ __forceinline__ float sum_of(const float (&v)[N]) {
+  static_assert(N == 4 || N == 8);
+  const float four = (v[0] + v[1]) + (v[2] + v[3]);
+  if constexpr (N == 4) return four;
+  else return four + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
 // The order of some instructions: reads and products in turn.  Left to itself the
 // compiler moves the reads behind the products, next to their use, and every
 // step starts with a wait for LDS.
@@ -587,13 +612,15 @@ __device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, uint3
   // The bias's gradient: the sums of operand B's columns (dy) over the rows, by the
   // waves that have them first, each lane half of the rows.
   const bool sums = P == kGradW && a.db && t.ta == 0 && wave % S::NA == 0;
-  float column_sum[S::WB] = {};
-  auto add_columns = [&](const u32x4 (&f)[S::WB]) {
+  LongSum column_sum[S::WB];
+  auto add_columns = [&](const u32x4 (&fragments)[S::WB]) {
 #pragma unroll
     for (int j = 0; j < S::WB; ++j) {
-      const auto v = __builtin_bit_cast(StoredVec<ST, 16 / bytes>, f[j]);
+      const auto v = __builtin_bit_cast(StoredVec<ST, 16 / bytes>, fragments[j]);
+      float f[16 / bytes];
 #pragma unroll
-      for (int e = 0; e < 16 / bytes; ++e) column_sum[j] += static_cast<float>(v[e]);
+      for (int e = 0; e < 16 / bytes; ++e) f[e] = static_cast<float>(v[e]);
+      column_sum[j].add(sum_of(f));
     }
   };
   // Part p of n of a step: reads of the next step's fragments and products of this
@@ -773,7 +800,7 @@ __device__ __forceinline__ void product(const GroupedArgs& a, uint32_t id, uint3
     if (sums) {
 #pragma unroll
       for (int j = 0; j < S::WB; ++j) {
-        const float v = column_sum[j] + __shfl_xor(column_sum[j], 32);
+        const float half = column_sum[j].value(), v = half + __shfl_xor(half, 32);
         const int64_t m = b0 + wb + 32 * j + lane;
         if (lane < 32 && m < a.M) {
           if (slot >= 0) a.bias_parts[slot * a.M + m] = v;
@@ -841,10 +868,10 @@ __global__ __launch_bounds__(kBlock) void grouped_join(GroupedArgs a, int64_t bl
   if (a.db) {
     const int64_t m = block * kBlock + threadIdx.x;
     if (m < a.M) {
-      float sum = 0.0f;
+      LongSum sum;
 #pragma unroll 8
-      for (int64_t c = 0; c < mine; ++c) sum += a.bias_parts[(slot + c) * a.M + m];
-      store_one<ST>(a.db, g * a.M + m, sum);
+      for (int64_t c = 0; c < mine; ++c) sum.add(a.bias_parts[(slot + c) * a.M + m]);
+      store_one<ST>(a.db, g * a.M + m, sum.value());
     }
   }
 }
@@ -858,17 +885,23 @@ __global__ __launch_bounds__(1024) void grouped_bias_grad(GroupedArgs a) {
   const int lane = lane_id(), w = threadIdx.x >> 6;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   const int64_t end = group_offset(a, g + 1);
-  float sum = 0.0f;
+  LongSum sum;
   if (c < a.M) {
-#pragma unroll 4
-    for (int64_t n = group_offset(a, g) + w; n < end; n += 16)
-      sum += load_one<ST>(a.grad, n * a.grad_stride + c);
+    int64_t n = group_offset(a, g) + w;
+    for (; n + 48 < end; n += 64) {
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = load_one<ST>(a.grad, (n + 16 * i) * a.grad_stride + c);
+      sum.add(sum_of(f));
+    }
+    for (; n < end; n += 16) sum.add(load_one<ST>(a.grad, n * a.grad_stride + c));
   }
-  part[w][lane] = sum;
+  part[w][lane] = sum.value();
   __syncthreads();
   if (w == 0 && c < a.M) {
-    for (int i = 1; i < 16; ++i) sum += part[i][lane];
-    store_one<ST>(a.db, g * a.M + c, sum);
+    LongSum all;
+    for (int i = 0; i < 16; ++i) all.add(part[i][lane]);
+    store_one<ST>(a.db, g * a.M + c, all.value());
   }
 }
 
