@@ -329,6 +329,8 @@ def grouped_linear_backward(x, weight, offsets, grad, bias=False, need_dx=True, 
     dx = x.new_empty((N, K)) if need_dx else None
     dw = x.new_empty((G, M, K)) if need_dweight else None
     db = x.new_empty((G, M)) if bias else None
+    if not need_dweight:   # the workspace is for the weights' chunks of rows alone
+        nw = 0
     ws = _workspace(nw, x)
     _call(device, "tbe_grouped_linear_backward", x.data_ptr(), xs, weight.data_ptr(), offsets.data_ptr(),
           _INDEX[offsets.dtype], grad.data_ptr(), gs, _p(dx), K, _p(dw), _p(db), N, G, K, M, _DTYPE[x.dtype],

@@ -61,3 +61,18 @@ def test_infinite_sums():
         keep = torch.ones(70, dtype=torch.bool)
         keep[[3, 5, 7]] = False
         assert (db[keep] == 5000).all()
+
+
+def test_no_workspace_without_the_weights_gradient():
+    """Sizes whose weights' gradient is summed in chunks of rows, with a workspace of megabytes."""
+    N, G, K, M = 20000, 2, 320, 256
+    assert tbe.layers._grouped_sizes(N, G, K, M, torch.float32)[1] > 1 << 20
+    x, w, grad = torch.ones(N, K, device="cuda"), torch.ones(G, M, K, device="cuda"), torch.ones(N, M, device="cuda")
+    off = torch.tensor([0, 7000, N], device="cuda")
+    tbe.grouped_linear_backward(x, w, off, grad, bias=True, need_dx=False, need_dweight=False)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    db = tbe.grouped_linear_backward(x, w, off, grad, bias=True, need_dx=False, need_dweight=False)[2]
+    assert torch.cuda.max_memory_allocated() - before <= 1 << 16
+    assert (db[0] == 7000).all() and (db[1] == 13000).all()
