@@ -32,6 +32,7 @@
 
 #include <type_traits>
 
+#include "grouped_plan.hpp"
 #include "layers.hpp"
 
 namespace tbe {
@@ -60,45 +61,6 @@ struct GroupedArgs {
   float* parts;
   float* bias_parts;
 };
-
-// How the weights' gradient is summed, from the call's sizes alone.
-struct GradWPlan {
-  int tile;           // 256, 128 or 64 outputs on a side
-  int64_t chunk;      // as above
-  int64_t slots;
-};
-// The time of so many equal tiles, in hundredths of a large one's of 2-byte rows.  A CU
-// has one tile of 256 at a time or two smaller ones, which take a fifth longer for the
-// same outputs, as LDS bounds them.  Of fp32 the matrix cores bound all, and the tiles
-// of a CU share them; small tiles are a tenth slower for the same outputs, and large
-// ones (16384 x 1024 -> 1024: 289 us, 257 with 128, 292 with 64).
-inline int64_t tile_rounds(int tile, int64_t tiles, int32_t dtype) {
-  if (dtype == TBE_F32) return (tiles + 255) / 256 * (tile == 256 ? 112 : tile == 128 ? 25 : 7);
-  if (tile == 256) return (tiles + 255) / 256 * 100;
-  return (tiles + 511) / 512 * (tile == 128 ? 62 : 31);
-}
-inline GradWPlan plan_grad_w(int64_t rows, int64_t groups, int64_t K, int64_t M, int32_t dtype) {
-  const auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((K + t - 1) / t); };
-  // Large tiles are a fifth faster, but need some for each CU: groups differ in
-  // size, and the last round leaves CUs idle.  (16384 rows in 8 groups of very
-  // different sizes, 1024 x 4096, bf16: 512 large tiles 320 us, 2048 small ones 170.)
-  // A single group's are all the same.
-  if (groups * tiles(256) >= 1024 ||
-      (groups == 1 && tiles(256) >= 128 &&
-       tile_rounds(256, tiles(256), dtype) < tile_rounds(128, tiles(128), dtype)))
-    return {256, 0, 0};
-  if (groups * tiles(128) >= 512 || rows == 0) return {128, 0, 0};
-  // Too few tiles for the chip: chunks of rows, about one for each place.  Where
-  // those of 128 outputs would be short, 64: 8191 rows in 5 groups, 250 x 130, fp32,
-  // 148 chunk tiles of 128 25 us, 828 of 64 20 us.
-  GradWPlan p{rows * tiles(128) < 512 * 256 ? 64 : 128, 0, 0};
-  const int64_t places = p.tile == 64 ? 1024 : 512, least = dtype == TBE_F32 ? 128 : 256;
-  const int64_t want = (rows * tiles(p.tile) + places - 1) / places;
-  p.chunk = std::max(least, (want + 63) / 64 * 64);
-  // a group of n > chunk rows has at most 2 n / chunk chunks
-  p.slots = rows > p.chunk ? 2 * rows / p.chunk : 0;
-  return p;
-}
 
 // The products of one call; defined for each type in its own file.
 hipError_t launch_grouped_f32(const GroupedArgs& a, bool backward, hipStream_t s);
@@ -905,8 +867,6 @@ __global__ __launch_bounds__(1024) void grouped_bias_grad(GroupedArgs a) {
   }
 }
 
-inline int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
-
 // Workgroups of a product.
 template <Product P, typename S>
 int64_t workgroups(const GroupedArgs& a) {
@@ -959,65 +919,34 @@ using Medium = Shape<128, 128, 2, 2, 2, 128>;
 using Square = Shape<64, 64, 2, 2, 4, 128>;
 using Narrow = Shape<128, 32, 4, 1, 4, 128>;
 
-// The tiles of a product over rows, by their outputs along the columns.  32 stands
-// for Narrow, for groups of few rows, whose weights' reading is what counts (64 rows
-// over 64 groups, 512 -> 2048 bf16: 18 us, 21 with the others; 4096 rows: 35 with 128,
-// 41 with 64).  Of the others the one with the fewest rounds of tiles by the time of a
-// round (tile_rounds), which agrees with these, in us (2-byte rows):
-//   16384 rows in 8 groups, 1024 -> 4096   256 162, 128 177
-//   16384 rows in 8 groups, 4096 -> 1024   256 183, 128 172
-//   8192 rows in 8 groups, 1024 -> 1024    256 30, 128 32, 64 41
-//   4096 rows in 8 groups, 1024 -> 1024    256 26, 128 22, 64 25
-//   2048 rows in 8 groups, 1024 -> 512     128 14, 64 11
-// and of fp32, 1266 rows in 2 groups, 384 -> 4032, 128 61, 64 55.
-template <int ST>
-int64_t row_rounds(const GroupedArgs& a, int64_t cols, int tile) {
-  constexpr int32_t dtype = ST;
-  // a group's last tile is half full on the average
-  const int64_t tiles = a.groups == 1 ? ceil_div(a.rows, tile) : a.rows / tile + a.groups / 2;
-  return tile_rounds(tile, tiles * ceil_div(cols, tile), dtype);
-}
-template <int ST>
-int row_tile(const GroupedArgs& a, int64_t cols) {
-  if (a.rows <= a.groups * 32) return 32;
-  const int64_t large = row_rounds<ST>(a, cols, 256), medium = row_rounds<ST>(a, cols, 128),
-                square = row_rounds<ST>(a, cols, 64);
-  return square <= medium && square <= large ? 64 : medium <= large ? 128 : 256;
-}
-
 template <int ST, Product P>
 hipError_t launch_rows(const GroupedArgs& a, hipStream_t s) {
-  const int tile = row_tile<ST>(a, P == kForward ? a.M : a.K);
-  return tile == 256   ? launch_product<ST, P, Large>(a, s)
-         : tile == 128 ? launch_product<ST, P, Medium>(a, s)
+  const int tile = row_tile(a.rows, a.groups, P == kForward ? a.M : a.K, ST);
+  if constexpr (ST != kF32)
+    if (tile == 256) return launch_product<ST, P, Large>(a, s);
+  return tile == 128   ? launch_product<ST, P, Medium>(a, s)
          : tile == 64  ? launch_product<ST, P, Square>(a, s)
                        : launch_product<ST, P, Narrow>(a, s);
 }
 
 template <int ST>
 hipError_t launch_backward(const GroupedArgs& a, hipStream_t s) {
-  constexpr int32_t dtype = ST;
   const bool dx = a.dx && a.rows > 0;
   hipError_t e = hipSuccess;
   if (a.dw) {
-    const GradWPlan plan = plan_grad_w(a.rows, a.groups, a.K, a.M, dtype);
-    // The one launch makes up for rows' tiles that take longer, where the weights' are
-    // few and the largest group's last ones run alone: up to half (8192 rows in 8 groups,
-    // 1024 -> 1024, 512 tiles, bf16: 55 us, 64 in two launches; fp32 4096 rows 165, 221),
-    // else a tenth (8192 rows, 1024 -> 4096 fp32, 2048 tiles: 1273 us, 1162 in two).
-    const int best = row_tile<ST>(a, a.K);
-    const int64_t own = row_rounds<ST>(a, a.K, plan.tile), least = row_rounds<ST>(a, a.K, best);
-    const int64_t tiles = a.groups * ceil_div(a.M, plan.tile) * ceil_div(a.K, plan.tile);
-    const bool both = dx && best != 32 && own * 20 <= least * (tiles < 1024 ? 30 : 22);
+    const BackwardPlan plan = plan_backward(a.rows, a.groups, a.K, a.M, dx, ST);
+    const bool both = plan.both;
     if (dx && !both) e = launch_rows<ST, kGradX>(a, s);
     if (e != hipSuccess) return e;
-    e = plan.tile == 256   ? (both ? launch_gradients<ST, Large>(a, s)
-                                   : launch_product<ST, kGradW, Large>(a, s))
-        : plan.tile == 128 ? (both ? launch_gradients<ST, Medium>(a, s)
-                                   : launch_product<ST, kGradW, Medium>(a, s))
-                           : (both ? launch_gradients<ST, Square>(a, s)
-                                   : launch_product<ST, kGradW, Square>(a, s));
-    if (e != hipSuccess || plan.slots == 0) return e;
+    const auto go = [&](auto shape) {
+      using S = decltype(shape);
+      return both ? launch_gradients<ST, S>(a, s) : launch_product<ST, kGradW, S>(a, s);
+    };
+    if constexpr (ST == kF32)
+      e = plan.w.tile == 128 ? go(Medium{}) : go(Square{});
+    else
+      e = plan.w.tile == 256 ? go(Large{}) : plan.w.tile == 128 ? go(Medium{}) : go(Square{});
+    if (e != hipSuccess || plan.w.slots == 0) return e;
     const int64_t blocks = ceil_div(std::max(ceil_div(a.M * a.K, 4), a.M), kBlock);
     hipLaunchKernelGGL((grouped_join<ST>), dim3(static_cast<unsigned>(blocks * a.groups)),
                        dim3(kBlock), 0, s, a, blocks);

@@ -1,9 +1,10 @@
-// The grouped linear layer's tile arithmetic (csrc/tiles.hpp) on the CPU: every workgroup of a
-// launch finds its tile of the groups' rows as the kernels do.
+// The grouped linear layer's tile arithmetic (csrc/tiles.hpp, csrc/grouped_plan.hpp) on the CPU:
+// which tiles a call takes, and the tile of the groups' rows that each workgroup of a launch finds.
 #include <algorithm>
 #include <cstdint>
 #include <vector>
 
+#include "grouped_plan.hpp"
 #include "tiles.hpp"
 
 extern "C" {
@@ -39,6 +40,23 @@ int64_t row_tiles(const int64_t* offsets, int64_t groups, int64_t rows, int64_t 
     if (taken) ++taken[before[g] + tb * na + ta];
   }
   return count;
+}
+
+// The tiles of a call's products: {forward, dx, dweight, its chunk, its slots, whether dx and
+// dweight share a launch}.
+void plan(int64_t rows, int64_t groups, int64_t K, int64_t M, int32_t dx, int32_t dtype, int64_t* out) {
+  const tbe::BackwardPlan b = tbe::plan_backward(rows, groups, K, M, dx != 0, dtype);
+  out[0] = tbe::row_tile(rows, groups, M, dtype);
+  out[1] = tbe::row_tile(rows, groups, K, dtype);
+  out[2] = b.w.tile;
+  out[3] = b.w.chunk;
+  out[4] = b.w.slots;
+  out[5] = b.both;
+}
+
+// The time of a product's tiles in hundredths of a large tile's.
+int64_t rounds(int64_t rows, int64_t groups, int64_t cols, int32_t tile, int32_t dtype) {
+  return tbe::row_rounds(rows, groups, cols, tile, dtype);
 }
 
 }  // extern "C"

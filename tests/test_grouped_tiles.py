@@ -1,5 +1,6 @@
 """Which tile each workgroup of the grouped linear layer takes, worked out on the CPU by the
 kernels' own arithmetic (csrc/tiles.hpp)."""
+import collections
 import ctypes
 import os
 import subprocess
@@ -8,16 +9,23 @@ import numpy as np
 import pytest
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-CSRC = os.path.join(os.path.dirname(HERE), "table_embedding_bag_amd", "csrc")
+ROOT = os.path.dirname(HERE)
+CSRC = os.path.join(ROOT, "table_embedding_bag_amd", "csrc")
+F32, F16, BF16 = 0, 1, 2
+Plan = collections.namedtuple("Plan", "forward dx dw chunk slots both")
 
 
 @pytest.fixture(scope="module")
 def host(tmp_path_factory):
     out = str(tmp_path_factory.mktemp("tiles") / "tiles.so")
-    subprocess.check_call(["g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", "-I" + CSRC, "-o", out,
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", "-I" + CSRC,
+                           "-I" + os.path.join(ROOT, "include"), "-o", out,
                            os.path.join(HERE, "grouped_tiles_host.cpp")])
     lib = ctypes.CDLL(out)
-    lib.row_tiles.restype = ctypes.c_int64
+    i64, i32 = ctypes.c_int64, ctypes.c_int32
+    lib.row_tiles.restype = lib.rounds.restype = i64
+    lib.rounds.argtypes = [i64, i64, i64, i32, i32]
+    lib.plan.argtypes = [i64, i64, i64, i64, i32, i32, ctypes.c_void_p]
     return lib
 
 
@@ -65,3 +73,33 @@ def test_bad_offsets_stay_within_the_rows(host, TB, TA):
             off = np.arange(groups + 1) % 2 * rows
         n, lo, hi, taken = _row_tiles(host, off, rows, int(r.integers(1, 3000)), TB, TA)
         assert n >= 0 and lo >= 0 and hi < rows and (taken <= 1).all(), (i, groups, rows)
+
+
+def _plan(host, rows, groups, K, M, dtype, dx=True):
+    out = (ctypes.c_int64 * 6)()
+    host.plan(rows, groups, K, M, dx, dtype, out)
+    return Plan(*out)
+
+
+def test_products_over_rows_take_the_tiles_of_the_fewest_rounds(host):
+    r = np.random.default_rng(9)
+    for _ in range(3000):
+        rows, groups = int(2 ** r.uniform(0, 17)), int(2 ** r.uniform(0, 8))
+        K, M = (int(2 ** r.uniform(0, 13)) for _ in range(2))
+        for dtype in (F32, F16, BF16):
+            p = _plan(host, rows, groups, K, M, dtype)
+            for tile, cols in ((p.forward, M), (p.dx, K)):
+                assert (tile == 32) == (rows <= 32 * groups)
+                for other in (64, 128) + (() if dtype == F32 else (256,)):
+                    assert tile == 32 or host.rounds(rows, groups, cols, tile, dtype) <= \
+                        host.rounds(rows, groups, cols, other, dtype)
+
+
+def test_fp32_takes_no_tiles_of_256(host):
+    """They are no faster than four of 128: the weights' gradient of several large groups too."""
+    r = np.random.default_rng(10)
+    for rows, groups, K, M in [(32768, 16, 4096, 4096), (32768, 16, 2048, 2048), (40000, 1, 8192, 8192)] + [
+            (int(2 ** r.uniform(5, 18)), int(2 ** r.uniform(0, 6)), int(2 ** r.uniform(8, 14)), int(2 ** r.uniform(8, 14)))
+            for _ in range(2000)]:
+        p = _plan(host, rows, groups, K, M, F32)
+        assert max(p.forward, p.dx, p.dw) <= 128, (rows, groups, K, M, p)
