@@ -30,9 +30,7 @@ hipError_t launch(const GroupedArgs& a, int32_t dtype, bool backward, hipStream_
 }
 
 RowLayout layout_of(const void* p, int64_t stride, int64_t width, int32_t dtype) {
-  const int64_t b = dtype_bytes(dtype);
-  if (aligned_to(p, 16) && stride * b % 16 == 0 && width * b % 16 == 0) return kChunkRows;
-  return aligned_to(p, 4) && stride * b % 4 == 0 ? kWordRows : kOddRows;
+  return row_layout(reinterpret_cast<uintptr_t>(p), stride, width, dtype_bytes(dtype));
 }
 
 // Longest rows and strides: 256 of them lie within a buffer descriptor's reach.

@@ -37,10 +37,6 @@
 
 namespace tbe {
 
-// Rows of operands: of whole 16-byte chunks at aligned addresses; starting at
-// multiples of 4 bytes; or, of 2-byte values, at any.
-enum RowLayout { kOddRows, kWordRows, kChunkRows };
-
 struct GroupedArgs {
   int64_t rows, groups, K, M;  // K = in_features, M = out_features
   const void* x;

@@ -11,6 +11,14 @@ namespace tbe {
 
 inline int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
+// Rows of operands: of whole 16-byte chunks at aligned addresses; starting at
+// multiples of 4 bytes; or, of 2-byte values, at any.
+enum RowLayout { kOddRows, kWordRows, kChunkRows };
+inline RowLayout row_layout(uintptr_t p, int64_t stride, int64_t width, int64_t bytes) {
+  if (p % 16 == 0 && stride * bytes % 16 == 0 && width * bytes % 16 == 0) return kChunkRows;
+  return p % 4 == 0 && stride * bytes % 4 == 0 ? kWordRows : kOddRows;
+}
+
 // The time of so many equal tiles, in hundredths of a large one's of 2-byte rows.  A CU
 // has one tile of 256 at a time or two smaller ones, which take a fifth longer for the
 // same outputs, as LDS bounds them.  Of fp32 the matrix cores bound all, and the tiles

@@ -54,6 +54,11 @@ void plan(int64_t rows, int64_t groups, int64_t K, int64_t M, int32_t dx, int32_
   out[5] = b.both;
 }
 
+// The layout of an operand's rows (0 odd, 1 words, 2 chunks).
+int32_t layout(uint64_t address, int64_t stride, int64_t width, int64_t bytes) {
+  return tbe::row_layout(static_cast<uintptr_t>(address), stride, width, bytes);
+}
+
 // The time of a product's tiles in hundredths of a large tile's.
 int64_t rounds(int64_t rows, int64_t groups, int64_t cols, int32_t tile, int32_t dtype) {
   return tbe::row_rounds(rows, groups, cols, tile, dtype);

@@ -8,6 +8,8 @@ import subprocess
 import numpy as np
 import pytest
 
+import grouped_cases
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(ROOT, "table_embedding_bag_amd", "csrc")
@@ -25,6 +27,7 @@ def host(tmp_path_factory):
     i64, i32 = ctypes.c_int64, ctypes.c_int32
     lib.row_tiles.restype = lib.rounds.restype = i64
     lib.rounds.argtypes = [i64, i64, i64, i32, i32]
+    lib.layout.argtypes = [ctypes.c_uint64, i64, i64, i64]
     lib.plan.argtypes = [i64, i64, i64, i64, i32, i32, ctypes.c_void_p]
     return lib
 
@@ -103,3 +106,28 @@ def test_fp32_takes_no_tiles_of_256(host):
             for _ in range(2000)]:
         p = _plan(host, rows, groups, K, M, F32)
         assert max(p.forward, p.dx, p.dw) <= 128, (rows, groups, K, M, p)
+
+
+@pytest.mark.parametrize("case", list(grouped_cases.cases()), ids=grouped_cases.name)
+def test_kernel_cases_take_the_tiles_they_name(host, case):
+    product, tile, chunked, layout, rows, groups, K, M, dtype = case
+    code, size = {"fp32": (F32, 4), "fp16": (F16, 2), "bf16": (BF16, 2)}[dtype]
+    p = _plan(host, rows, groups, K, M, code, dx=product == "both")
+    took = {"forward": p.forward, "dx": p.dx, "dw": p.dw, "both": p.dw}[product]
+    assert took == tile and p.both == (product == "both")
+    if product in ("dw", "both"):
+        assert (p.slots > 0) == chunked
+    operands = (K,) if product == "forward" else (K, M)
+    assert min(host.layout(4096, n, n, size) for n in operands) == layout
+
+
+def test_every_kernel_has_a_case():
+    """The kernels that are compiled: forward and dx with tiles of 256 (2-byte values alone), 128, 64
+    and 128 x 32, the weights' gradient and both gradients with the square ones."""
+    have = {(c[0], c[1], c[3], c[8]) for c in grouped_cases.cases()}
+    for dtype, layouts in (("fp32", (1, 2)), ("fp16", (0, 1, 2)), ("bf16", (0, 1, 2))):
+        square = (64, 128) if dtype == "fp32" else (64, 128, 256)
+        for layout in layouts:
+            for product in ("forward", "dx", "dw", "both"):
+                for tile in square + ((32,) if product in ("forward", "dx") else ()):
+                    assert (product, tile, layout, dtype) in have
