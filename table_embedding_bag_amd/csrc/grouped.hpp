@@ -145,13 +145,12 @@ __device__ bool find_row_tile(const GroupedArgs& a, uint32_t id, uint32_t blocks
 // 16 bytes a lane from a buffer to LDS at `lds` + 16 lane; zeros for offsets past
 // the buffer's end.  In assembly (it writes no register) because the compiler,
 // which cannot tell the slices apart, waits for all such loads before it reads
-// LDS with the transposing instruction; wait_loads() waits for them here.  (m0
-// is never kept by the compiler, which sets it before each use of its own.)
+// LDS with the transposing instruction; wait_loads() waits for them here.
 __device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t offset, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
       ::"s"(lds), "v"(offset), "s"(rsrc)
-      : "memory");
+      : "memory", "m0");
 }
 
 // Row chunk `unit` of the groups' chunks of a.chunk rows (an empty group has one):
