@@ -13,6 +13,7 @@ described in kimbodo.com/?p=28372, "What Happened".
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional, Sequence
 
@@ -29,9 +30,13 @@ __all__ = [
     "OPTION_LONG_RUN_THRESHOLD", "OPTION_PROFILE", "OPTION_SORT", "OPTION_SPIN_LIMIT",
     "OPTION_LDS_FORWARD",
     "EXPORTED_SYMBOLS", "GATE_SIGMOID", "GATE_DECAY",
-    "dropout", "dropout_backward", "scan_step", "scan_forward", "scan_backward",
-    "grouped_linear", "grouped_linear_backward",
 ]
+# Functions of layers.py, which is loaded on first use: its module needs torch, this one
+# alone does not.  A star import takes them where torch is installed.
+_LAYERS = ("dropout", "dropout_backward", "scan_step", "scan_forward", "scan_backward",
+           "grouped_linear", "grouped_linear_backward")
+if importlib.util.find_spec("torch"):
+    __all__ += _LAYERS
 
 F32, F16, BF16 = 0, 1, 2
 I32, I64 = 0, 1
@@ -420,14 +425,9 @@ class TBE:
             pass
 
 
-_LAYERS = ("dropout", "dropout_backward", "scan_step", "scan_forward", "scan_backward",
-           "grouped_linear", "grouped_linear_backward")
-
-
 def __getattr__(name):
-    """The layers on first use: their module needs torch, this one alone does not."""
+    """The layers on first use."""
     if name == "layers" or name in _LAYERS:
-        import importlib
         layers = importlib.import_module(".layers", __name__)
         value = layers if name == "layers" else getattr(layers, name)
         globals()[name] = value
