@@ -132,6 +132,9 @@ __device__ __forceinline__ int64_t offset_at(const ScanArgs& a, int64_t s) {
   return o < 0 ? 0 : (o > a.tokens ? a.tokens : o);
 }
 
+// A scan in one pass over tiles that look back at what earlier ones published (Merrill,
+// Garland, "Single-pass parallel prefix scan with decoupled look-back", 2016), in groups.
+//
 // The token axis is cut into tiles whatever the sequences: W waves of T tokens
 // each (a span), and 64 V channels, V neighbours a lane.  Within its span a wave
 // reduces the recurrence to "state out = A state in + B" per channel, the waves'

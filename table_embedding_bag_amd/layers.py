@@ -5,6 +5,9 @@ The functions check their arguments, allocate outputs and workspaces with torch 
 HIP kernels of ``libtbe.so`` (``include/tbe.h``) on the current stream of the tensors' GPU.
 Rows may be strided (a slice of a wider buffer); the elements of a row are adjacent.  Bad
 arguments raise ValueError, statuses of the library TBEError.
+
+torch's autograd does not see these calls: a tensor that requires gradients is taken like any
+other, results are not part of a graph, and each layer's backward function is called explicitly.
 """
 from __future__ import annotations
 
