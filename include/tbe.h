@@ -465,7 +465,8 @@ tbe_status tbe_grouped_linear(const void* x, int64_t x_stride, const void* weigh
 
 /* Its gradients: dx [rows, in_features], dweight and dbias (contiguous; empty
  * groups get zeros) from grad [rows, out_features].  Each of the three may be
- * NULL (not wanted); without dweight no workspace is needed. */
+ * NULL (not wanted); without dweight no workspace is needed.  dbias is summed in
+ * another order beside dweight than alone: the two may differ in rounding. */
 tbe_status tbe_grouped_linear_backward(const void* x, int64_t x_stride, const void* weight,
                                        const void* offsets, int32_t index_dtype, const void* grad,
                                        int64_t grad_stride, void* dx, int64_t dx_stride,

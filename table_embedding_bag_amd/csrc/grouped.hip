@@ -6,13 +6,15 @@
 // are fp32 and rounded once.
 //
 // Large products are bound by the matrix cores, and those by the card's power:
-// 32768 rows in 16 groups, 4096 -> 4096 bf16, forward and backward, take 3.0 ms (1.1
-// PFLOP/s; a library's product of the same sizes in equal groups runs at 1.1 to
+// 32768 rows in 16 groups, 4096 -> 4096 bf16, forward and backward, take 3.1 ms (1.06
+// PFLOP/s, the matrix cores busy in 65% and 59% of the cycles at the 1.7 GHz that random
+// values leave; a library's product of the same sizes in equal groups runs at 1.1 to
 // 1.2).  16384 rows in 8 groups of very different sizes, 1024 -> 4096, take 505 us (0.82
-// PFLOP/s): five rounds of large tiles where 4.4 would do, and tiles of 128 that LDS
-// bounds.  With few rows the weights' reading counts: 64 rows over 64 groups, 512 ->
-// 2048, 18 us (4.7 TB/s of the weights that have rows).  Small ones are a few
-// latencies: 8191 x 250 -> 130 fp32, both directions, 48 us in three launches.
+// PFLOP/s): five rounds of large tiles where 4.4 would do, and tiles of 128, which read
+// twice the LDS bytes for the same outputs.  With few rows the weights' reading counts: 64 rows over 64 groups, 512 ->
+// 2048, 19 us (4.6 TB/s of the weights that have rows).  Small ones are a few
+// latencies: 8191 x 250 -> 130 fp32, both directions, 49 us in three launches.
+// Times here and beside the kernels are of passes among others unless they say "kernel".
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

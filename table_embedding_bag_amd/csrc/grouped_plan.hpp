@@ -21,7 +21,7 @@ inline RowLayout row_layout(uintptr_t p, int64_t stride, int64_t width, int64_t 
 
 // The time of so many equal tiles, in hundredths of a large one's of 2-byte rows.  A CU
 // has one tile of 256 at a time or two smaller ones, which take a fifth longer for the
-// same outputs, as LDS bounds them.  Of fp32 the matrix cores bound all, and the tiles
+// same outputs, for which they read twice the LDS bytes.  Of fp32 the matrix cores bound all, and the tiles
 // of a CU share them; small tiles are a tenth slower for the same outputs.  Large ones
 // are no faster (both gradients of 32768 rows in 16 groups, 4096 -> 4096: 16.0 ms, 16.1
 // with 128; 8192 in 20, 2048 -> 2048: 1.20, 1.19) and leave more of the last round idle

@@ -11,7 +11,7 @@
 //
 // Every input is read and every output written once, 16 bytes a token and channel
 // of 16-bit rows for both directions, and memory would bound that: 4 sequences of
-// 16384 x 1024 bf16 move 1.0 GB, 194 us at a copy's 5.2 TB/s.  They take 271 us (3.7
+// 16384 x 1024 bf16 move 1.0 GB, 194 us at a copy's 5.2 TB/s.  They take 273 us (3.7
 // TB/s), 8192 of about 20 x 256 175 us (4.1).  A tile waits 6 of its 11 us for the
 // states before it (reads and writes between XCDs, about a microsecond each way),
 // and of the rest about half is arithmetic: some 30 vector instructions a token and
@@ -978,8 +978,8 @@ hipError_t launch_tiles(const ScanArgs& a, const ScanWork& w, int32_t kind, bool
 
 // Channels a lane: two neighbours of 16-bit rows, where every row starts at an
 // even element and a wave's 128 channels are not mostly past the end (8192
-// sequences of about 20 x 256 bf16, both directions: 168 us, 179 with one; 4 of 16384
-// x 1024: 284 and 288).
+// sequences of about 20 x 256 bf16 in packed rows, both directions: 173 us, 175 with
+// one; 4 of 16384 x 1024: 262 and 263).
 int lane_channels(const tbe_scan_input* in, const ScanArgs& a) {
   if (in->dtype == TBE_F32 || a.dim <= 64 || a.dim % 2) return 1;
   const auto even = [](const void* p, int64_t stride) { return aligned_to(p, 4) && stride % 2 == 0; };
