@@ -8,8 +8,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "tiles.hpp"
-
 namespace tbe {
 
 constexpr int kWave = 64;        // CDNA wavefront width
@@ -90,6 +88,15 @@ __device__ __forceinline__ uint64_t match_low_bits(uint64_t active, uint32_t v, 
     peers &= ~(bal ^ ((static_cast<uint64_t>(m) << 32) | m));
   }
   return peers;
+}
+
+// Workgroups are handed to the 8 XCDs of the chip round robin.  Renumber them
+// so that each XCD works on one contiguous range of logical work items (and so
+// keeps that range's data in its own L2).
+__device__ __forceinline__ int xcd_contiguous_block(int bid, int nblocks) {
+  const int xcd = bid & 7, pos = bid >> 3;
+  const int q = nblocks >> 3, r = nblocks & 7;
+  return xcd * q + (xcd < r ? xcd : r) + pos;
 }
 
 // bf16 / fp16 widening (exact) and narrowing (round to nearest even).

@@ -34,6 +34,7 @@
 
 #include "grouped_plan.hpp"
 #include "layers.hpp"
+#include "tiles.hpp"
 
 namespace tbe {
 

@@ -12,15 +12,6 @@
 
 namespace tbe {
 
-// Workgroups are handed to the 8 XCDs of the chip round robin.  Renumber them
-// so that each XCD works on one contiguous range of logical work items (and so
-// keeps that range's data in its own L2).
-TBE_HOST_DEVICE int xcd_contiguous_block(int bid, int nblocks) {
-  const int xcd = bid & 7, pos = bid >> 3;
-  const int q = nblocks >> 3, r = nblocks & 7;
-  return xcd * q + (xcd < r ? xcd : r) + pos;
-}
-
 // Tile number q of a group's na x nb tiles: bands of 8 along nb, so that what an XCD
 // works on at one time shares operand tiles in its L2.
 TBE_HOST_DEVICE void band_order(int64_t q, int64_t na, int64_t nb, int64_t* ta, int64_t* tb) {
@@ -34,10 +25,12 @@ TBE_HOST_DEVICE void band_order(int64_t q, int64_t na, int64_t nb, int64_t* ta, 
 // The number, of the `total` tiles of all groups, that workgroup id of `blocks` takes;
 // false where it has none.  A launch has a workgroup for every tile of groups that follow
 // each other: more tiles are of groups that overlap (bad offsets), and then no workgroup
-// takes one, as their numbers may pass every type here.
+// takes one, as their numbers may pass every type here.  Workgroups go round robin to the
+// 8 XCDs; each XCD takes a contiguous range of the tiles.
 TBE_HOST_DEVICE bool tile_number(uint32_t id, uint32_t blocks, int64_t total, int64_t* q) {
   if (static_cast<int64_t>(id) >= total || total > static_cast<int64_t>(blocks)) return false;
-  *q = xcd_contiguous_block(static_cast<int>(id), static_cast<int>(total));
+  const int64_t xcd = id % 8, rest = total % 8;
+  *q = xcd * (total / 8) + (xcd < rest ? xcd : rest) + id / 8;
   return true;
 }
 
