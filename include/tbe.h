@@ -474,6 +474,129 @@ tbe_status tbe_grouped_linear_backward(const void* x, int64_t x_stride, const vo
                                        int64_t in_features, int64_t out_features, int32_t dtype,
                                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* Layer norm of each row of x [rows, cols]: y = (x - m) r weight + bias, m the
+ * row's mean, r = 1 / sqrt(mean((x - m)^2) + eps); weight and bias [cols] in the
+ * rows' type (NULL: ones, zeros).  stats: fp32 [rows][2], 8-byte aligned, gets
+ * m and r of each row for the backward pass (NULL: not wanted).  y may be x
+ * itself (same stride) where no backward pass follows.  rows at most 2^30, cols
+ * at most 2^20, eps in [0, 1e30]. */
+tbe_status tbe_layer_norm(const void* x, int64_t x_stride, const void* weight, const void* bias,
+                          void* y, int64_t y_stride, float* stats, int64_t rows, int64_t cols,
+                          int32_t dtype, double eps, void* stream);
+
+/* Bytes of the workspace that dweight and dbias need. */
+tbe_status tbe_layer_norm_sizes(int64_t rows, int64_t cols, int32_t dtype, size_t* backward_bytes);
+
+/* Its gradients from that of y, grad [rows, cols]: dx [rows, cols], dweight and
+ * dbias [cols], each NULL where not wanted; without the latter two no workspace
+ * is needed.  weight: that of the forward call (NULL: ones).  dx may be grad
+ * itself (same stride).  No rows: dweight and dbias are zeros. */
+tbe_status tbe_layer_norm_backward(const void* x, int64_t x_stride, const float* stats,
+                                   const void* grad, int64_t grad_stride, const void* weight,
+                                   void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                                   int64_t rows, int64_t cols, int32_t dtype, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* Scores of experts from a row's logits, and groups' scores from their experts'. */
+typedef enum {
+  TBE_SCORES_SOFTMAX = 0,  /* over the row's experts */
+  TBE_SCORES_SIGMOID = 1   /* of each logit by itself */
+} tbe_scores;
+typedef enum {
+  TBE_GROUP_BEST = 0,     /* the best expert's */
+  TBE_GROUP_BEST_TWO = 1  /* the sum of the best two's (of the only one's) */
+} tbe_group_score;
+
+/* The choice of k experts for each row of logits [rows, experts].  Experts are
+ * chosen by score + bias (fp32 [experts]; NULL: none): first the top_groups
+ * best of `groups` groups of equally many consecutive experts by their
+ * group_score, then the k best experts of those.  The choice is that of exact
+ * arithmetic on the given values, down to differences of 64-bit rounding; of
+ * equal ones the lower index is better.  ids [rows][k]: the chosen experts, the
+ * best first; weights fp32 [rows][k]: their scores without the bias, divided by
+ * their sum where `renormalize` is not 0, times scale.  A NaN logit counts as
+ * -infinity, +infinity as the largest float; an expert whose logit is
+ * -infinity has the score 0 and, where chosen for want of others, the weight 0.
+ * experts at most 1024, groups and k at most 16, rows at most 2^25. */
+tbe_status tbe_route(const void* logits, int64_t logits_stride, const float* bias, int32_t* ids,
+                     float* weights, int64_t rows, int64_t experts, int64_t k, int64_t groups,
+                     int64_t top_groups, int32_t dtype, int32_t scores, int32_t group_score,
+                     int32_t renormalize, double scale, void* stream);
+
+/* The gradient of the weights with respect to the logits (the choice itself and
+ * the bias have none): dlogits [rows, experts] from grad fp32 [rows][k], ids
+ * being the forward call's (an id outside [0, experts) has no part). */
+tbe_status tbe_route_backward(const void* logits, int64_t logits_stride, const int32_t* ids,
+                              const float* grad, void* dlogits, int64_t dlogits_stride,
+                              int64_t rows, int64_t experts, int64_t k, int32_t dtype,
+                              int32_t scores, int32_t renormalize, double scale, void* stream);
+
+/* Bytes of the workspace of tbe_dispatch_plan (0: none). */
+tbe_status tbe_dispatch_plan_size(int64_t rows, int64_t k, int64_t experts,
+                                  size_t* workspace_bytes);
+
+/* Where each row's assignments go when rows are grouped by expert: ids [rows][k]
+ * (int32 or int64, contiguous); assignment n k + j gets places[n k + j], in the
+ * order of experts and, of one expert, of assignments; expert e has the places
+ * offsets[e] .. offsets[e + 1] (offsets: int64 [experts + 1], as
+ * tbe_grouped_linear takes them).  An id outside [0, experts) is left out:
+ * place -1.  experts at most 2048, k at most 64, rows * k below 2^31. */
+tbe_status tbe_dispatch_plan(const void* ids, int32_t index_dtype, int64_t rows, int64_t k,
+                             int64_t experts, int64_t* offsets, int32_t* places, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Rows to their places: out [rows * k, cols], out[places[n k + j]] = x[n]; rows
+ * from `total` on (on the device: offsets[experts]), which nobody has, are zeros.
+ * cols at most 2^20 here and below. */
+tbe_status tbe_dispatch(const void* x, int64_t x_stride, const int32_t* places,
+                        const int64_t* total, void* out, int64_t out_stride, int64_t rows,
+                        int64_t k, int64_t cols, int32_t dtype, void* stream);
+
+/* Rows back from their places: out[n] = residual[n] + sum over j of weights[n k + j]
+ * y[places[n k + j]] (weights NULL: ones; residual NULL: none).  y [rows * k,
+ * cols].  With the gradient of tbe_dispatch's output for y and neither weights
+ * nor residual it is the gradient of tbe_dispatch's x.  out may be the residual
+ * itself (same stride). */
+tbe_status tbe_combine(const void* y, int64_t y_stride, const int32_t* places,
+                       const float* weights, const void* residual, int64_t residual_stride,
+                       void* out, int64_t out_stride, int64_t rows, int64_t k, int64_t cols,
+                       int32_t dtype, void* stream);
+
+/* Its gradients from that of out, grad [rows, cols]: dy [rows * k, cols] (zeros
+ * from `total` on) and dweights fp32 [rows][k] (NULL: not wanted; 0 where the
+ * place is -1).  The residual's gradient is grad itself. */
+tbe_status tbe_combine_backward(const void* y, int64_t y_stride, const int32_t* places,
+                                const int64_t* total, const float* weights, const void* grad,
+                                int64_t grad_stride, void* dy, int64_t dy_stride, float* dweights,
+                                int64_t rows, int64_t k, int64_t cols, int32_t dtype, void* stream);
+
+/* Bytes of device workspace of the softmax loss's two calls. */
+tbe_status tbe_softmax_loss_sizes(int64_t rows, int64_t vocab, int64_t dim, int32_t dtype,
+                                  size_t* forward_bytes, size_t* backward_bytes);
+
+/* The softmax cross entropy of rows x [rows, dim] over the rows of a table
+ * [vocab, dim]: z = scale x table^T, lse[n] = ln sum_v exp(z[n, v]), loss[n] =
+ * lse[n] - z[n, targets[n]] (fp32).  The logits z are never kept.  A row whose
+ * target is outside [0, vocab) has none: its loss is 0, and it has no part in
+ * any gradient, whatever it holds.  scale: positive and finite.  rows at most
+ * 2^24, vocab at most 2^30, dim and strides at most 2^20, rows * dim at most
+ * 2^33, vocab * dim at most 2^36. */
+tbe_status tbe_softmax_loss(const void* x, int64_t x_stride, const void* table,
+                            int64_t table_stride, const void* targets, int32_t index_dtype,
+                            double scale, float* loss, float* lse, int64_t rows, int64_t vocab,
+                            int64_t dim, int32_t dtype, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Its gradients from those of the losses, grad fp32 [rows], and the forward
+ * call's lse: dx [rows, dim] and dtable [vocab, dim] (contiguous), each NULL
+ * where not wanted. */
+tbe_status tbe_softmax_loss_backward(const void* x, int64_t x_stride, const void* table,
+                                     int64_t table_stride, const void* targets,
+                                     int32_t index_dtype, double scale, const float* lse,
+                                     const float* grad, void* dx, void* dtable, int64_t rows,
+                                     int64_t vocab, int64_t dim, int32_t dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 const char* tbe_status_string(tbe_status status);
 int32_t tbe_abi_version(void);
 

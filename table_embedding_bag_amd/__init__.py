@@ -29,12 +29,16 @@ __all__ = [
     "FLAG_SPLIT_BAGS", "FLAG_COUNT_BACKWARD",
     "OPTION_LONG_RUN_THRESHOLD", "OPTION_PROFILE", "OPTION_SORT", "OPTION_SPIN_LIMIT",
     "OPTION_LDS_FORWARD",
-    "EXPORTED_SYMBOLS", "GATE_SIGMOID", "GATE_DECAY",
+    "EXPORTED_SYMBOLS", "GATE_SIGMOID", "GATE_DECAY", "SCORES_SOFTMAX", "SCORES_SIGMOID",
+    "GROUP_BEST", "GROUP_BEST_TWO",
 ]
 # Functions of layers.py, which is loaded on first use: its module needs torch, this one
 # alone does not.  A star import takes them where torch is installed.
 _LAYERS = ("dropout", "dropout_backward", "scan_step", "scan_forward", "scan_backward",
-           "grouped_linear", "grouped_linear_backward")
+           "grouped_linear", "grouped_linear_backward", "layer_norm", "layer_norm_backward",
+           "route", "route_backward", "DispatchPlan", "dispatch_plan", "dispatch",
+           "dispatch_backward", "combine", "combine_backward", "softmax_loss",
+           "softmax_loss_backward")
 if importlib.util.find_spec("torch"):
     __all__ += _LAYERS
 
@@ -48,6 +52,8 @@ FLAG_COUNT_BACKWARD = 32
 OPTION_LONG_RUN_THRESHOLD, OPTION_PROFILE, OPTION_SORT, OPTION_SPIN_LIMIT = 1, 2, 3, 4
 OPTION_LDS_FORWARD = 5
 GATE_SIGMOID, GATE_DECAY = 0, 1
+SCORES_SOFTMAX, SCORES_SIGMOID = 0, 1
+GROUP_BEST, GROUP_BEST_TWO = 0, 1
 STATIC_SCRATCH_BYTES = 64 << 20   # TBE_STATIC_SCRATCH_BYTES
 
 STATUS = {
@@ -64,6 +70,10 @@ EXPORTED_SYMBOLS = (
     "tbe_set_forward_scratch", "tbe_dropout", "tbe_scan_step", "tbe_scan_sizes",
     "tbe_scan_forward", "tbe_scan_backward", "tbe_grouped_linear_sizes", "tbe_grouped_linear",
     "tbe_grouped_linear_backward",
+    "tbe_layer_norm", "tbe_layer_norm_sizes", "tbe_layer_norm_backward", "tbe_route",
+    "tbe_route_backward", "tbe_dispatch_plan_size", "tbe_dispatch_plan", "tbe_dispatch",
+    "tbe_combine", "tbe_combine_backward", "tbe_softmax_loss_sizes", "tbe_softmax_loss",
+    "tbe_softmax_loss_backward",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -145,6 +155,21 @@ def load():
                                        P]
     lib.tbe_grouped_linear_backward.argtypes = [P, i64, P, P, i32, P, i64, P, i64, P, P, i64, i64,
                                                 i64, i64, i32, P, z, P]
+    f64 = ctypes.c_double
+    lib.tbe_layer_norm.argtypes = [P, i64, P, P, P, i64, P, i64, i64, i32, f64, P]
+    lib.tbe_layer_norm_sizes.argtypes = [i64, i64, i32, size_p]
+    lib.tbe_layer_norm_backward.argtypes = [P, i64, P, P, i64, P, P, i64, P, P, i64, i64, i32, P, z, P]
+    lib.tbe_route.argtypes = [P, i64, P, P, P, i64, i64, i64, i64, i64, i32, i32, i32, i32, f64, P]
+    lib.tbe_route_backward.argtypes = [P, i64, P, P, P, i64, i64, i64, i64, i32, i32, i32, f64, P]
+    lib.tbe_dispatch_plan_size.argtypes = [i64, i64, i64, size_p]
+    lib.tbe_dispatch_plan.argtypes = [P, i32, i64, i64, i64, P, P, P, z, P]
+    lib.tbe_dispatch.argtypes = [P, i64, P, P, P, i64, i64, i64, i64, i32, P]
+    lib.tbe_combine.argtypes = [P, i64, P, P, P, i64, P, i64, i64, i64, i64, i32, P]
+    lib.tbe_combine_backward.argtypes = [P, i64, P, P, P, P, i64, P, i64, P, i64, i64, i64, i32, P]
+    lib.tbe_softmax_loss_sizes.argtypes = [i64, i64, i64, i32, size_p, size_p]
+    lib.tbe_softmax_loss.argtypes = [P, i64, P, i64, P, i32, f64, P, P, i64, i64, i64, i32, P, z, P]
+    lib.tbe_softmax_loss_backward.argtypes = [P, i64, P, i64, P, i32, f64, P, P, P, P, i64, i64, i64, i32,
+                                              P, z, P]
     lib.tbe_abi_version.argtypes = []
     lib.tbe_abi_version.restype = i32
     for name in ("tbe_create", "tbe_forward", "tbe_backward_workspace_size", "tbe_backward_update",
@@ -153,7 +178,11 @@ def load():
                  "tbe_backward_update_no_alloc", "tbe_forward_scratch_size",
                  "tbe_set_forward_scratch", "tbe_dropout", "tbe_scan_step", "tbe_scan_sizes",
                  "tbe_scan_forward", "tbe_scan_backward", "tbe_grouped_linear_sizes",
-                 "tbe_grouped_linear", "tbe_grouped_linear_backward"):
+                 "tbe_grouped_linear", "tbe_grouped_linear_backward",
+                 "tbe_layer_norm", "tbe_layer_norm_sizes", "tbe_layer_norm_backward",
+                 "tbe_route", "tbe_route_backward", "tbe_dispatch_plan_size",
+                 "tbe_dispatch_plan", "tbe_dispatch", "tbe_combine", "tbe_combine_backward",
+                 "tbe_softmax_loss_sizes", "tbe_softmax_loss", "tbe_softmax_loss_backward"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

@@ -1,0 +1,418 @@
+// dispatch.hip -- rows to their experts and back.  Row n chose the experts ids[n][0 .. k);
+// assignment a = n k + j goes to a place in the order of (expert, a): places[a], a stable
+// counting sort; expert e then has the places offsets[e] .. offsets[e + 1].
+//   dispatch          rows[places[a]] = x[n]            (places of none: zeros)
+//   combine           y[n] = residual[n] + sum_j w[a] rows[places[a]]
+//   combine_backward  drows[places[a]] = w[a] dy[n],  dw[a] = <dy[n], rows[places[a]]>
+// and dispatch's gradient is a combine without weights.  An id outside [0, experts) goes
+// nowhere: place -1.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "layers.hpp"
+
+using namespace tbe;
+
+namespace {
+
+constexpr int kMaxExperts = 2048;
+constexpr int64_t kTile = 4096;      // assignments a workgroup, or more:
+constexpr int64_t kMostTiles = 256;  // every workgroup reads all tiles' counts
+
+struct PlanArgs {
+  const void* ids;
+  int32_t index64, experts;
+  int64_t n;        // assignments
+  int64_t tile;     // of them a workgroup's, a multiple of kBlock
+  int64_t tiles;
+  uint32_t* counts; // [tiles][experts], or null with one tile
+  int64_t* offsets;
+  int32_t* places;
+  int32_t bits;     // of an expert's number
+};
+
+// The expert of an assignment, or -1.
+__device__ __forceinline__ int expert_of(const PlanArgs& a, int64_t i) {
+  const int64_t e = a.index64 ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
+  return e >= 0 && e < a.experts ? static_cast<int>(e) : -1;
+}
+
+__global__ __launch_bounds__(kBlock) void plan_count(PlanArgs a) {
+  __shared__ uint32_t count[kMaxExperts];
+  for (int e = threadIdx.x; e < a.experts; e += kBlock) count[e] = 0;
+  __syncthreads();
+  const int64_t from = blockIdx.x * a.tile, end = std::min(from + a.tile, a.n);
+  for (int64_t i = from + threadIdx.x; i < end; i += kBlock) {
+    const int e = expert_of(a, i);
+    if (e >= 0) atomicAdd(&count[e], 1u);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kBlock)
+    a.counts[static_cast<int64_t>(blockIdx.x) * a.experts + e] = count[e];
+}
+
+// A wave takes a quarter of the tile: counts it, finds where each expert's assignments of the
+// quarter start, and goes through it 64 at a time, equal ones in their order.
+__global__ __launch_bounds__(kBlock) void plan_place(PlanArgs a) {
+  __shared__ uint32_t next[kWavesPerBlock][kMaxExperts];
+  __shared__ uint32_t scratch[kWavesPerBlock];
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  for (int w = 0; w < kWavesPerBlock; ++w)
+    for (int e = threadIdx.x; e < a.experts; e += kBlock) next[w][e] = 0;
+  __syncthreads();
+  const int64_t quarter = a.tile / kWavesPerBlock;
+  const int64_t tile_end = std::min((blockIdx.x + int64_t{1}) * a.tile, a.n);
+  const int64_t from = blockIdx.x * a.tile + wave * quarter, end = std::min(from + quarter, tile_end);
+  for (int64_t i = from + lane; i < end; i += kWave) {
+    const int e = expert_of(a, i);
+    if (e >= 0) atomicAdd(&next[wave][e], 1u);
+  }
+  __syncthreads();
+  // starts: the experts before, the tiles before, the quarters before
+  uint32_t before_all = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += kBlock) {
+    const int e = e0 + threadIdx.x;
+    uint32_t mine = 0, before = 0, total = 0;
+    if (e < a.experts) {
+      for (int w = 0; w < kWavesPerBlock; ++w) mine += next[w][e];
+      total = mine;
+      if (a.counts) {
+        total = 0;
+#pragma unroll 8
+        for (int64_t t = 0; t < a.tiles; ++t) {
+          const uint32_t c = a.counts[t * a.experts + e];
+          total += c;
+          before += t < blockIdx.x ? c : 0u;
+        }
+      }
+    }
+    uint32_t sum;
+    const uint32_t start = before_all + block_exclusive_sum(total, scratch, &sum);
+    before_all += sum;
+    if (e < a.experts) {
+      uint32_t at = start + before;
+      for (int w = 0; w < kWavesPerBlock; ++w) {
+        const uint32_t c = next[w][e];
+        next[w][e] = at;
+        at += c;
+      }
+      if (blockIdx.x == 0) a.offsets[e] = start;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.experts] = before_all;
+  __syncthreads();
+  for (int64_t i0 = from; i0 < end; i0 += kWave) {
+    const int64_t i = i0 + lane;
+    const int e = i < end ? expert_of(a, i) : -1;
+    const uint64_t real = __ballot(e >= 0);
+    const uint64_t peers = match_low_bits(real, static_cast<uint32_t>(e), a.bits);
+    const uint32_t rank = popc_below(peers);
+    int place = -1;
+    if (e >= 0) {
+      place = static_cast<int>(next[wave][e] + rank);
+      if (rank + 1 == __popcll(peers)) next[wave][e] = place + 1;  // the last of them
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (i < end) a.places[i] = place;
+  }
+}
+
+struct MoveArgs {
+  const void* x;         // dispatch: [rows, cols]; combine: the experts' rows
+  const void* residual;  // or null
+  const void* grad;
+  const float* weights;  // [rows][k], or null: ones
+  const int32_t* places;
+  const int64_t* total;  // how many places are taken
+  void* out;
+  float* dweights;       // or null
+  int64_t x_stride, r_stride, g_stride, out_stride;
+  int64_t rows, cols, chunks;  // chunks of 16 bytes in a row
+  int32_t k;
+};
+
+template <int ST>
+struct Chunk {
+  static constexpr int E = 16 / StorageTraits<ST>::bytes;
+  StoredVec<ST, E> v = {};
+  // The chunk at column c of the row at element `at`; zeros past its end.
+  __device__ __forceinline__ void load(const void* base, int64_t at, int64_t c, int64_t cols) {
+    if (c + E <= cols) {
+      v = load_vec<ST, E>(base, at + c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (c + i < cols) v[i] = static_cast<const typename Stored<ST>::type*>(base)[at + c + i];
+    }
+  }
+  __device__ __forceinline__ void store(void* base, int64_t at, int64_t c, int64_t cols) const {
+    if (c + E <= cols) {
+      store_vec<ST, E>(base, at + c, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (c + i < cols) static_cast<typename Stored<ST>::type*>(base)[at + c + i] = v[i];
+    }
+  }
+};
+
+// The place of assignment i, or -1: a wrong one is none.
+__device__ __forceinline__ int64_t place_of(const MoveArgs& a, int64_t i) {
+  const int32_t p = a.places[i];
+  return p >= 0 && p < a.rows * a.k ? p : -1;
+}
+
+// A thread reads a chunk of a row once and writes it to the row's places.
+template <int ST>
+__global__ __launch_bounds__(kBlock) void dispatch_rows(MoveArgs a) {
+  constexpr int E = Chunk<ST>::E;
+  const int64_t all = a.rows * a.chunks, step = static_cast<int64_t>(gridDim.x) * kBlock;
+  const int64_t total = *a.total;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; q < all; q += step) {
+    const int64_t n = q / a.chunks, c = (q - n * a.chunks) * E;
+    Chunk<ST> v;
+    v.load(a.x, n * a.x_stride, c, a.cols);
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t p = place_of(a, n * a.k + j);
+      if (p >= 0) v.store(a.out, p * a.out_stride, c, a.cols);
+    }
+    // the places that nobody has
+    for (int j = 0; j < a.k; ++j)
+      if (n * a.k + j >= total) Chunk<ST>().store(a.out, (n * a.k + j) * a.out_stride, c, a.cols);
+  }
+}
+
+template <int ST>
+__global__ __launch_bounds__(kBlock) void combine_rows(MoveArgs a) {
+  constexpr int E = Chunk<ST>::E;
+  const int64_t all = a.rows * a.chunks, step = static_cast<int64_t>(gridDim.x) * kBlock;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; q < all; q += step) {
+    const int64_t n = q / a.chunks, c = (q - n * a.chunks) * E;
+    float sum[E] = {};
+    if (a.residual) {
+      Chunk<ST> r;
+      r.load(a.residual, n * a.r_stride, c, a.cols);
+#pragma unroll
+      for (int i = 0; i < E; ++i) sum[i] = static_cast<float>(r.v[i]);
+    }
+#pragma unroll 4
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t p = place_of(a, n * a.k + j);
+      if (p < 0) continue;
+      const float w = a.weights ? a.weights[n * a.k + j] : 1.0f;
+      Chunk<ST> v;
+      v.load(a.x, p * a.x_stride, c, a.cols);
+#pragma unroll
+      for (int i = 0; i < E; ++i) sum[i] += w * static_cast<float>(v.v[i]);
+    }
+    Chunk<ST> out;
+#pragma unroll
+    for (int i = 0; i < E; ++i) out.v[i] = static_cast<typename Stored<ST>::type>(sum[i]);
+    out.store(a.out, n * a.out_stride, c, a.cols);
+  }
+}
+
+// A wave has a row: its gradient, weighted, to the row's places, and the products with the
+// experts' rows there.
+template <int ST>
+__global__ __launch_bounds__(kBlock) void combine_gradients(MoveArgs a) {
+  constexpr int E = Chunk<ST>::E;
+  const int lane = lane_id();
+  const int64_t total = *a.total;
+  for (int64_t n = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); n < a.rows;
+       n += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t i = n * a.k + j, p = place_of(a, i);
+      const bool hole = i >= total;   // a place that nobody has
+      float dot = 0.0f;
+      const float w = p >= 0 ? a.weights[i] : 0.0f;
+      for (int64_t c = lane * E; c < a.cols; c += 64 * E) {
+        if (p >= 0) {
+          Chunk<ST> g, y, out;
+          g.load(a.grad, n * a.g_stride, c, a.cols);
+          if (a.dweights) {
+            y.load(a.x, p * a.x_stride, c, a.cols);
+#pragma unroll
+            for (int e = 0; e < E; ++e) dot += static_cast<float>(g.v[e]) * static_cast<float>(y.v[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            out.v[e] = static_cast<typename Stored<ST>::type>(w * static_cast<float>(g.v[e]));
+          out.store(a.out, p * a.out_stride, c, a.cols);
+        }
+        if (hole) Chunk<ST>().store(a.out, i * a.out_stride, c, a.cols);
+      }
+      if (a.dweights) {
+        for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
+        if (lane == 0) a.dweights[i] = dot;
+      }
+    }
+  }
+}
+
+constexpr int64_t kMaxCols = int64_t{1} << 20;
+
+int64_t tile_of(int64_t n) {
+  const int64_t each = (n + kMostTiles - 1) / kMostTiles;
+  return std::max(kTile, (each + kBlock - 1) / kBlock * kBlock);
+}
+
+size_t plan_bytes(int64_t n, int64_t experts) {
+  const int64_t tiles = (n + tile_of(n) - 1) / tile_of(n);
+  return tiles > 1 ? static_cast<size_t>(tiles) * experts * sizeof(uint32_t) : 0;
+}
+
+tbe_status check_plan(int64_t rows, int64_t k, int64_t experts) {
+  if (rows < 0 || k < 1 || experts < 1) return TBE_ERR_INVALID_ARGUMENT;
+  if (k > 64 || rows > ((int64_t{1} << 31) - 1) / k || experts > kMaxExperts) return TBE_ERR_UNSUPPORTED;
+  return TBE_OK;
+}
+
+tbe_status check_move(int64_t rows, int64_t k, int64_t cols, int32_t dtype) {
+  if (rows < 0 || k < 1 || cols < 1 || !known_dtype(dtype)) return TBE_ERR_INVALID_ARGUMENT;
+  if (k > 64 || rows > ((int64_t{1} << 31) - 1) / k || cols > kMaxCols) return TBE_ERR_UNSUPPORTED;
+  return TBE_OK;
+}
+
+MoveArgs move_args(const int32_t* places, int64_t rows, int64_t k, int64_t cols, int32_t dtype) {
+  MoveArgs a{};
+  a.places = places;
+  a.rows = rows;
+  a.k = static_cast<int32_t>(k);
+  a.cols = cols;
+  const int64_t e = 16 / dtype_bytes(dtype);
+  a.chunks = (cols + e - 1) / e;
+  return a;
+}
+
+dim3 grid_of(int64_t threads) {
+  return dim3(static_cast<unsigned>(std::min<int64_t>((threads + kBlock - 1) / kBlock, int64_t{1} << 22)));
+}
+
+}  // namespace
+
+extern "C" {
+
+tbe_status tbe_dispatch_plan_size(int64_t rows, int64_t k, int64_t experts, size_t* workspace_bytes) {
+  if (!workspace_bytes) return TBE_ERR_INVALID_ARGUMENT;
+  const tbe_status st = check_plan(rows, k, experts);
+  if (st == TBE_OK) *workspace_bytes = plan_bytes(rows * k, experts);
+  return st;
+}
+
+tbe_status tbe_dispatch_plan(const void* ids, int32_t index_dtype, int64_t rows, int64_t k, int64_t experts,
+                             int64_t* offsets, int32_t* places, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  const tbe_status st = check_plan(rows, k, experts);
+  if (st != TBE_OK) return st;
+  if (index_dtype != TBE_I32 && index_dtype != TBE_I64) return TBE_ERR_INVALID_ARGUMENT;
+  if (!offsets || !aligned_to(offsets, 8) || (rows > 0 && (!ids || !places)) || !aligned_to(places, 4) ||
+      !aligned_to(ids, index_dtype == TBE_I64 ? 8 : 4))
+    return TBE_ERR_INVALID_ARGUMENT;
+  PlanArgs a{};
+  a.ids = ids;
+  a.index64 = index_dtype == TBE_I64;
+  a.experts = static_cast<int32_t>(experts);
+  a.n = rows * k;
+  a.tile = tile_of(a.n);
+  a.tiles = std::max<int64_t>(1, (a.n + a.tile - 1) / a.tile);
+  a.offsets = offsets;
+  a.places = places;
+  while ((int64_t{1} << a.bits) < experts) ++a.bits;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a.tiles > 1) {
+    if (!workspace || !aligned_to(workspace, 256)) return TBE_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < plan_bytes(a.n, experts)) return TBE_ERR_WORKSPACE_TOO_SMALL;
+    a.counts = static_cast<uint32_t*>(workspace);
+    hipLaunchKernelGGL(plan_count, dim3(static_cast<unsigned>(a.tiles)), dim3(kBlock), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return TBE_ERR_HIP;
+  }
+  hipLaunchKernelGGL(plan_place, dim3(static_cast<unsigned>(a.tiles)), dim3(kBlock), 0, s, a);
+  return hipGetLastError() == hipSuccess ? TBE_OK : TBE_ERR_HIP;
+}
+
+tbe_status tbe_dispatch(const void* x, int64_t x_stride, const int32_t* places, const int64_t* total,
+                        void* out, int64_t out_stride, int64_t rows, int64_t k, int64_t cols, int32_t dtype,
+                        void* stream) {
+  const tbe_status st = check_move(rows, k, cols, dtype);
+  if (st != TBE_OK || rows == 0) return st;
+  const size_t e = dtype_bytes(dtype);
+  if (!x || !places || !total || !out || !aligned_to(x, e) || !aligned_to(out, e) || !aligned_to(places, 4) ||
+      !aligned_to(total, 8))
+    return TBE_ERR_INVALID_ARGUMENT;
+  if ((rows > 1 && x_stride < 0) || (rows * k > 1 && out_stride < cols)) return TBE_ERR_INVALID_ARGUMENT;
+  MoveArgs a = move_args(places, rows, k, cols, dtype);
+  a.x = x;
+  a.x_stride = x_stride;
+  a.total = total;
+  a.out = out;
+  a.out_stride = out_stride;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const dim3 grid = grid_of(rows * a.chunks);
+  if (dtype == TBE_F32) hipLaunchKernelGGL(dispatch_rows<kF32>, grid, dim3(kBlock), 0, s, a);
+  else if (dtype == TBE_F16) hipLaunchKernelGGL(dispatch_rows<kF16>, grid, dim3(kBlock), 0, s, a);
+  else hipLaunchKernelGGL(dispatch_rows<kBF16>, grid, dim3(kBlock), 0, s, a);
+  return hipGetLastError() == hipSuccess ? TBE_OK : TBE_ERR_HIP;
+}
+
+tbe_status tbe_combine(const void* y, int64_t y_stride, const int32_t* places, const float* weights,
+                       const void* residual, int64_t residual_stride, void* out, int64_t out_stride,
+                       int64_t rows, int64_t k, int64_t cols, int32_t dtype, void* stream) {
+  const tbe_status st = check_move(rows, k, cols, dtype);
+  if (st != TBE_OK || rows == 0) return st;
+  const size_t e = dtype_bytes(dtype);
+  if (!y || !places || !out || !aligned_to(y, e) || !aligned_to(out, e) || !aligned_to(residual, e) ||
+      !aligned_to(places, 4) || !aligned_to(weights, 4))
+    return TBE_ERR_INVALID_ARGUMENT;
+  if ((rows * k > 1 && y_stride < 0) || (rows > 1 && (out_stride < cols || (residual && residual_stride < 0))))
+    return TBE_ERR_INVALID_ARGUMENT;
+  MoveArgs a = move_args(places, rows, k, cols, dtype);
+  a.x = y;
+  a.x_stride = y_stride;
+  a.weights = weights;
+  a.residual = residual;
+  a.r_stride = residual_stride;
+  a.out = out;
+  a.out_stride = out_stride;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const dim3 grid = grid_of(rows * a.chunks);
+  if (dtype == TBE_F32) hipLaunchKernelGGL(combine_rows<kF32>, grid, dim3(kBlock), 0, s, a);
+  else if (dtype == TBE_F16) hipLaunchKernelGGL(combine_rows<kF16>, grid, dim3(kBlock), 0, s, a);
+  else hipLaunchKernelGGL(combine_rows<kBF16>, grid, dim3(kBlock), 0, s, a);
+  return hipGetLastError() == hipSuccess ? TBE_OK : TBE_ERR_HIP;
+}
+
+tbe_status tbe_combine_backward(const void* y, int64_t y_stride, const int32_t* places, const int64_t* total,
+                                const float* weights, const void* grad, int64_t grad_stride, void* dy,
+                                int64_t dy_stride, float* dweights, int64_t rows, int64_t k, int64_t cols,
+                                int32_t dtype, void* stream) {
+  const tbe_status st = check_move(rows, k, cols, dtype);
+  if (st != TBE_OK || rows == 0) return st;
+  const size_t e = dtype_bytes(dtype);
+  if (!places || !total || !weights || !grad || !dy || (dweights && !y) || !aligned_to(y, e) ||
+      !aligned_to(grad, e) || !aligned_to(dy, e) || !aligned_to(places, 4) || !aligned_to(total, 8) ||
+      !aligned_to(weights, 4) || !aligned_to(dweights, 4))
+    return TBE_ERR_INVALID_ARGUMENT;
+  if ((rows * k > 1 && (y_stride < 0 || dy_stride < cols)) || (rows > 1 && grad_stride < 0))
+    return TBE_ERR_INVALID_ARGUMENT;
+  MoveArgs a = move_args(places, rows, k, cols, dtype);
+  a.x = y;
+  a.x_stride = y_stride;
+  a.total = total;
+  a.weights = weights;
+  a.grad = grad;
+  a.g_stride = grad_stride;
+  a.out = dy;
+  a.out_stride = dy_stride;
+  a.dweights = dweights;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const dim3 grid = grid_of(rows * kWave);
+  if (dtype == TBE_F32) hipLaunchKernelGGL(combine_gradients<kF32>, grid, dim3(kBlock), 0, s, a);
+  else if (dtype == TBE_F16) hipLaunchKernelGGL(combine_gradients<kF16>, grid, dim3(kBlock), 0, s, a);
+  else hipLaunchKernelGGL(combine_gradients<kBF16>, grid, dim3(kBlock), 0, s, a);
+  return hipGetLastError() == hipSuccess ? TBE_OK : TBE_ERR_HIP;
+}
+
+}  // extern "C"

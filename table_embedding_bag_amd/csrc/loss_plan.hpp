@@ -1,0 +1,73 @@
+// loss_plan.hpp -- which tiles, pieces and splits the softmax loss takes, from a call's
+// sizes alone.  Plain C++, which compiles for a CPU alone too.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+#include "grouped_plan.hpp"
+
+namespace tbe {
+
+// Rows of the workspaces' matrices are whole 128-byte lines.
+inline int64_t padded_width(int64_t width, int64_t bytes) {
+  const int64_t line = 128 / bytes;
+  return ceil_div(width, line) * line;
+}
+
+// The forward pass: a workgroup has `tile` rows (32: tiles of 128 x 32) and `run`
+// consecutive tiles of the vocabulary; a row gets one partial sum of each segment.
+struct LossForwardPlan {
+  int tile;
+  int64_t tiles, run, segments;
+};
+inline LossForwardPlan plan_loss_forward(int64_t rows, int64_t vocab, int64_t K, int32_t dtype) {
+  LossForwardPlan p{};
+  p.tile = rows <= 32 ? 32 : row_tile(vocab, 1, rows, dtype);
+  const int64_t along_rows = ceil_div(rows, p.tile);
+  p.tiles = ceil_div(vocab, p.tile == 32 ? 128 : p.tile);
+  // workgroups for every place of the chip, twice over
+  const int64_t want = std::max<int64_t>(1, (p.tile == 256 ? 512 : 1024) / along_rows);
+  p.run = ceil_div(p.tiles, std::min(want, p.tiles));
+  p.segments = ceil_div(p.tiles, p.run);
+  return p;
+}
+
+// One gradient's product of a piece: outputs [out_rows, K], summed over `depth`.
+struct LossProductPlan {
+  int tile;
+  int64_t splits, each;  // parts of the summed index, values in each
+};
+inline LossProductPlan plan_loss_product(int64_t out_rows, int64_t K, int64_t depth, int32_t dtype) {
+  const auto tiles = [&](int64_t t) { return ceil_div(out_rows, t) * ceil_div(K, t); };
+  LossProductPlan p{};
+  p.tile = dtype != TBE_F32 && tiles(256) >= 128 ? 256 : 128;
+  const int64_t places = p.tile == 256 ? 256 : 512;
+  const int64_t want = std::max<int64_t>(1, places / tiles(p.tile));
+  p.each = std::max<int64_t>(512, ceil_div(ceil_div(depth, want), 64) * 64);
+  p.splits = ceil_div(depth, p.each);
+  return p;
+}
+
+// The backward pass goes over the vocabulary in pieces of `piece` rows of the table.
+struct LossBackwardPlan {
+  int tile;               // of the logits
+  int64_t piece, pieces;
+  int64_t width;          // of a row of the piece's gradients of the logits
+  LossProductPlan x, w;   // of a whole piece
+};
+inline LossBackwardPlan plan_loss_backward(int64_t rows, int64_t vocab, int64_t K, int32_t dtype) {
+  LossBackwardPlan p{};
+  const int64_t bytes = dtype == TBE_F32 ? 4 : 2;
+  const int64_t most = std::max<int64_t>(int64_t{1} << 10, (int64_t{256} << 20) / (rows * bytes));
+  const int64_t n = ceil_div(vocab, std::min<int64_t>(most, int64_t{1} << 18));
+  p.piece = std::min(vocab, ceil_div(ceil_div(vocab, n), 256) * 256);
+  p.pieces = ceil_div(vocab, p.piece);
+  p.width = padded_width(p.piece, bytes);
+  p.tile = std::max(64, row_tile(p.piece, 1, rows, dtype));
+  p.x = plan_loss_product(rows, K, p.piece, dtype);
+  p.w = plan_loss_product(p.piece, K, rows, dtype);
+  return p;
+}
+
+}  // namespace tbe

@@ -1,5 +1,7 @@
-"""Layers on looked-up rows: dropout, the gated linear recurrence over jagged sequences, and a
-linear layer for each of several ragged row groups, each with its gradient.
+"""Layers on looked-up rows: dropout, the gated linear recurrence over jagged sequences, a linear
+layer for each of several ragged row groups, layer norm, the choice of experts for each row, the
+rows' way to their experts and back, and the softmax loss over a table's rows, each with its
+gradient.
 
 The functions check their arguments, allocate outputs and workspaces with torch and call the
 HIP kernels of ``libtbe.so`` (``include/tbe.h``) on the current stream of the tensors' GPU.
@@ -13,16 +15,20 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import typing
 
 import torch
 
-from . import (BF16, F16, F32, GATE_DECAY, GATE_SIGMOID, I32, I64, _check, _ScanInput, load)
+from . import (BF16, F16, F32, GATE_DECAY, GATE_SIGMOID, GROUP_BEST, GROUP_BEST_TWO, I32, I64, SCORES_SIGMOID,
+               SCORES_SOFTMAX, _check, _ScanInput, load)
 
 _DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
 _U64 = (1 << 64) - 1
 _MAX_POLLS = 0   # tbe_scan_input.max_polls: the library's default
 _GATE = {"sigmoid": GATE_SIGMOID, "decay": GATE_DECAY}
+_SCORES = {"softmax": SCORES_SOFTMAX, "sigmoid": SCORES_SIGMOID}
+_GROUP_SCORE = {"max": GROUP_BEST, "top2": GROUP_BEST_TWO}
 
 
 def _fail(what):
@@ -339,3 +345,321 @@ def grouped_linear_backward(x, weight, offsets, grad, bias=False, need_dx=True, 
           _INDEX[offsets.dtype], grad.data_ptr(), gs, _p(dx), K, _p(dw), _p(db), N, G, K, M, _DTYPE[x.dtype],
           _p(ws), nw)
     return dx, dw, db
+
+
+# --- layer norm --------------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=256)
+def _norm_size(N, D, dtype):
+    n = ctypes.c_size_t(0)
+    _check(load().tbe_layer_norm_sizes(N, D, _DTYPE[dtype], ctypes.byref(n)), "tbe_layer_norm_sizes")
+    return n.value
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, need_stats=True, out=None):
+    """(x - mean) / sqrt(variance + eps) * weight + bias of each row of x [N, D].
+
+    weight, bias [D] in x's type (None: ones, zeros).  Returns (y [N, D] in x's type, stats):
+    stats (fp32 [N, 2], each row's mean and 1 / sqrt(variance + eps)) is what layer_norm_backward
+    needs (None without need_stats).  out may be x itself where no backward pass follows.
+    """
+    if not 0.0 <= eps <= 1e30:
+        _fail(f"eps must lie in [0, 1e30], got {eps}")
+    xs = _rows(x, "x")
+    N, D = x.shape
+    if D < 1:
+        _fail("rows must have at least one element")
+    if weight is not None:
+        _dense(weight, "weight", x.dtype, (D,))
+    if bias is not None:
+        _dense(bias, "bias", x.dtype, (D,))
+    ys = D if out is None else _out(out, "out", x.dtype, (N, D))
+    device = _on_one_gpu(x, weight, bias, out)
+    if out is None:
+        out = x.new_empty((N, D))
+    stats = x.new_empty((N, 2), dtype=torch.float32) if need_stats else None
+    _call(device, "tbe_layer_norm", x.data_ptr(), xs, _p(weight), _p(bias), out.data_ptr(), ys, _p(stats), N, D,
+          _DTYPE[x.dtype], eps)
+    return out, stats
+
+
+def layer_norm_backward(x, stats, grad, weight=None, bias=False, need_dx=True, out=None):
+    """Gradients (dx, dweight, dbias) of layer_norm, whose stats these are, from that of its
+    output, grad [N, D].
+
+    weight is the forward call's; dweight is None where there was none, dbias is computed where
+    ``bias`` is true, dx where need_dx is (into out, which may be grad itself, where given).
+    """
+    xs = _rows(x, "x")
+    N, D = x.shape
+    if D < 1:
+        _fail("rows must have at least one element")
+    if stats is None:
+        _fail("stats are those of a forward call with need_stats")
+    _dense(stats, "stats", torch.float32, (N, 2))
+    gs = _rows(grad, "grad", x.dtype, (N, D))
+    if weight is not None:
+        _dense(weight, "weight", x.dtype, (D,))
+    ds = D if out is None else _out(out, "out", x.dtype, (N, D))
+    device = _on_one_gpu(x, stats, grad, weight, out)
+    dx = out if out is not None else x.new_empty((N, D)) if need_dx else None
+    dw = None if weight is None else x.new_empty(D)
+    db = x.new_empty(D) if bias else None
+    nw = 0 if dw is None and db is None else _norm_size(N, D, x.dtype)
+    ws = _workspace(nw, x)
+    _call(device, "tbe_layer_norm_backward", x.data_ptr(), xs, stats.data_ptr(), grad.data_ptr(), gs, _p(weight),
+          _p(dx), ds, _p(dw), _p(db), N, D, _DTYPE[x.dtype], _p(ws), nw)
+    return dx, dw, db
+
+
+# --- the choice of experts ---------------------------------------------------------------------
+
+def _scores(kind):
+    if kind not in _SCORES:
+        _fail(f"scores must be 'softmax' or 'sigmoid', got {kind!r}")
+    return _SCORES[kind]
+
+
+def _finite(v, name):
+    if not abs(v) <= 3.4e38:
+        _fail(f"{name} must be finite, got {v}")
+
+
+def route(logits, k, scores="softmax", bias=None, groups=1, top_groups=1, group_score="max",
+          renormalize=True, scale=1.0):
+    """The k best of a row's experts by score + bias, and their weights.
+
+    logits [N, E]; scores "softmax" (over the row) or "sigmoid"; bias fp32 [E] (None: none) counts
+    in the choice alone.  With groups > 1 the experts lie in that many equal groups of neighbours:
+    the top_groups best by their best expert (group_score "max") or the sum of their best two
+    ("top2") are chosen first.  Returns (ids int32 [N, k], best first, weights fp32 [N, k]): the
+    chosen experts' scores, divided by their sum (renormalize), times scale.
+
+    The choice is that of exact arithmetic, equal scores going to the lower index.  A NaN logit
+    counts as -inf; an expert at -inf has the score 0 and, if chosen for want of others, the
+    weight 0.  E up to 1024, k and groups up to 16.
+    """
+    kind = _scores(scores)
+    if group_score not in _GROUP_SCORE:
+        _fail(f"group_score must be 'max' or 'top2', got {group_score!r}")
+    _finite(scale, "scale")
+    ls = _rows(logits, "logits")
+    N, E = logits.shape
+    if groups < 1 or E < 1 or E % groups:
+        _fail(f"groups must divide the {E} experts, got {groups}")
+    if not 1 <= top_groups <= groups:
+        _fail(f"top_groups must lie in [1, {groups}], got {top_groups}")
+    if not 1 <= k <= E // groups * top_groups:
+        _fail(f"k must lie in [1, {E // groups * top_groups}], got {k}")
+    if bias is not None:
+        _dense(bias, "bias", torch.float32, (E,))
+    device = _on_one_gpu(logits, bias)
+    ids = logits.new_empty((N, k), dtype=torch.int32)
+    weights = logits.new_empty((N, k), dtype=torch.float32)
+    _call(device, "tbe_route", logits.data_ptr(), ls, _p(bias), ids.data_ptr(), weights.data_ptr(), N, E, k, groups,
+          top_groups, _DTYPE[logits.dtype], kind, _GROUP_SCORE[group_score], renormalize, scale)
+    return ids, weights
+
+
+def route_backward(logits, ids, grad, scores="softmax", renormalize=True, scale=1.0, out=None):
+    """The gradient with respect to the logits of route's weights, from theirs, grad fp32 [N, k].
+
+    ids are the forward call's; scores, renormalize and scale must be its too.  (The choice and
+    the bias have no gradient.)  Returns dlogits [N, E] in the logits' type.
+    """
+    kind = _scores(scores)
+    _finite(scale, "scale")
+    ls = _rows(logits, "logits")
+    N, E = logits.shape
+    if ids.dim() != 2 or not 1 <= ids.shape[1] <= E:
+        _fail(f"ids must have the shape ({N}, k), got {tuple(ids.shape)}")
+    k = ids.shape[1]
+    _dense(ids, "ids", torch.int32, (N, k))
+    _dense(grad, "grad", torch.float32, (N, k))
+    ds = E if out is None else _out(out, "out", logits.dtype, (N, E))
+    device = _on_one_gpu(logits, ids, grad, out)
+    if out is None:
+        out = logits.new_empty((N, E))
+    _call(device, "tbe_route_backward", logits.data_ptr(), ls, ids.data_ptr(), grad.data_ptr(), out.data_ptr(), ds,
+          N, E, k, _DTYPE[logits.dtype], kind, renormalize, scale)
+    return out
+
+
+# --- rows to their experts and back ------------------------------------------------------------
+
+class DispatchPlan(typing.NamedTuple):
+    """Where rows go when they are grouped by expert: expert e has the places offsets[e] ..
+    offsets[e + 1] (int64 [experts + 1], as grouped_linear takes them), row n's j-th assignment
+    the place places[n, j] (int32 [N, k]; -1: none)."""
+    offsets: torch.Tensor
+    places: torch.Tensor
+
+
+@functools.lru_cache(maxsize=256)
+def _plan_size(N, k, E):
+    n = ctypes.c_size_t(0)
+    _check(load().tbe_dispatch_plan_size(N, k, E, ctypes.byref(n)), "tbe_dispatch_plan_size")
+    return n.value
+
+
+def dispatch_plan(ids, experts):
+    """The places of each row's assignments, grouped by expert: a DispatchPlan.
+
+    ids [N, k] (int32 or int64).  The assignments of an expert keep their order; an id outside
+    [0, experts) is left out.  It stays on the GPU: nothing is read back.
+    """
+    if ids.dtype not in _INDEX:
+        _fail(f"ids must be int32 or int64, got {ids.dtype}")
+    if ids.dim() != 2 or ids.shape[1] < 1:
+        _fail(f"ids must have the shape (N, k), got {tuple(ids.shape)}")
+    if not ids.is_contiguous():
+        _fail("ids must be contiguous")
+    if experts < 1:
+        _fail(f"experts must be at least 1, got {experts}")
+    device = _on_one_gpu(ids)
+    N, k = ids.shape
+    nw = _plan_size(N, k, experts)
+    offsets = ids.new_empty(experts + 1, dtype=torch.int64)
+    places = ids.new_empty((N, k), dtype=torch.int32)
+    ws = _workspace(nw, ids)
+    _call(device, "tbe_dispatch_plan", ids.data_ptr(), _INDEX[ids.dtype], N, k, experts, offsets.data_ptr(),
+          places.data_ptr(), _p(ws), nw)
+    return DispatchPlan(offsets, places)
+
+
+def _plan(plan):
+    """N, k and the address of the number of places that are taken."""
+    offsets, places = plan
+    if places.dim() != 2 or places.shape[1] < 1:
+        _fail(f"the plan's places must have the shape (N, k), got {tuple(places.shape)}")
+    _dense(places, "the plan's places", torch.int32, places.shape)
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        _fail("the plan's offsets must have one dimension and two entries at least")
+    _dense(offsets, "the plan's offsets", torch.int64, offsets.shape)
+    return (*places.shape, offsets.data_ptr() + 8 * (offsets.shape[0] - 1))
+
+
+def dispatch(x, plan, out=None):
+    """The rows of x [N, D] at their places: [N * k, D], rows that have no assignment zeros."""
+    xs = _rows(x, "x")
+    N, k, total = _plan(plan)
+    D = x.shape[1]
+    if x.shape[0] != N or D < 1:
+        _fail(f"x must have the plan's {N} rows of at least one element, got {tuple(x.shape)}")
+    ys = D if out is None else _out(out, "out", x.dtype, (N * k, D))
+    device = _on_one_gpu(x, *plan, out)
+    if out is None:
+        out = x.new_empty((N * k, D))
+    _call(device, "tbe_dispatch", x.data_ptr(), xs, plan.places.data_ptr(), total, out.data_ptr(), ys, N, k, D,
+          _DTYPE[x.dtype])
+    return out
+
+
+def dispatch_backward(grad, plan, out=None):
+    """The gradient with respect to x of dispatch(x, plan): the sum of a row's places."""
+    return combine(grad, plan, out=out)
+
+
+def combine(y, plan, weights=None, residual=None, out=None):
+    """residual[n] + the sum over j of weights[n, j] * y[places[n, j]].
+
+    y [N * k, D]; weights fp32 [N, k] (None: ones); residual [N, D] (None: zeros).  Returns [N, D]
+    in y's type; out may be the residual itself.
+    """
+    ys = _rows(y, "y")
+    N, k, _ = _plan(plan)
+    D = y.shape[1]
+    if y.shape[0] != N * k or D < 1:
+        _fail(f"y must have the plan's {N * k} rows of at least one element, got {tuple(y.shape)}")
+    if weights is not None:
+        _dense(weights, "weights", torch.float32, (N, k))
+    rs = 0 if residual is None else _rows(residual, "residual", y.dtype, (N, D))
+    os = D if out is None else _out(out, "out", y.dtype, (N, D))
+    device = _on_one_gpu(y, *plan, weights, residual, out)
+    if out is None:
+        out = y.new_empty((N, D))
+    _call(device, "tbe_combine", y.data_ptr(), ys, plan.places.data_ptr(), _p(weights), _p(residual), rs,
+          out.data_ptr(), os, N, k, D, _DTYPE[y.dtype])
+    return out
+
+
+def combine_backward(y, plan, weights, grad, need_dweights=True):
+    """Gradients (dy [N * k, D], dweights fp32 [N, k]) of combine from that of its output, grad
+    [N, D].  Rows of dy that have no assignment are zeros, dweights 0 where the place is -1.
+    (A residual's gradient is grad itself.)"""
+    ys = _rows(y, "y")
+    N, k, total = _plan(plan)
+    D = y.shape[1]
+    if y.shape[0] != N * k or D < 1:
+        _fail(f"y must have the plan's {N * k} rows of at least one element, got {tuple(y.shape)}")
+    _dense(weights, "weights", torch.float32, (N, k))
+    gs = _rows(grad, "grad", y.dtype, (N, D))
+    device = _on_one_gpu(y, *plan, weights, grad)
+    dy = y.new_empty((N * k, D))
+    dw = torch.empty_like(weights) if need_dweights else None
+    _call(device, "tbe_combine_backward", y.data_ptr(), ys, plan.places.data_ptr(), total, weights.data_ptr(),
+          grad.data_ptr(), gs, dy.data_ptr(), D, _p(dw), N, k, D, _DTYPE[y.dtype])
+    return dy, dw
+
+
+# --- softmax loss over a table's rows ----------------------------------------------------------
+
+@functools.lru_cache(maxsize=256)
+def _loss_sizes(N, V, D, dtype):
+    fw, bw = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().tbe_softmax_loss_sizes(N, V, D, _DTYPE[dtype], ctypes.byref(fw), ctypes.byref(bw)),
+           "tbe_softmax_loss_sizes")
+    return fw.value, bw.value
+
+
+def _loss(x, table, targets, scale):
+    xs = _rows(x, "x")
+    ts = _rows(table, "table", x.dtype)
+    N, D = x.shape
+    if table.shape[1] != D or table.shape[0] < 1 or D < 1:
+        _fail(f"table must have rows of {D} elements, at least one, got {tuple(table.shape)}")
+    if targets.dtype not in _INDEX:
+        _fail(f"targets must be int32 or int64, got {targets.dtype}")
+    if targets.shape != (N,):
+        _fail(f"targets must have the shape ({N},), got {tuple(targets.shape)}")
+    if not targets.is_contiguous():
+        _fail("targets must be contiguous")
+    if not 0.0 < scale <= 1e30:
+        _fail(f"scale must lie in (0, 1e30], got {scale}")
+    return (xs, ts, N, table.shape[0], D, *_loss_sizes(N, table.shape[0], D, x.dtype))
+
+
+def softmax_loss(x, table, targets, scale=1.0):
+    """The softmax cross entropy of each row of x [N, D] over the rows of table [V, D].
+
+    With logits z = scale * x @ table.T, which are never kept: returns (loss, lse), fp32 [N],
+    lse[n] = log(sum(exp(z[n]))) and loss[n] = lse[n] - z[n, targets[n]].  targets [N] (int32 or
+    int64); a row whose target is outside [0, V) has none: its loss is 0.
+    """
+    xs, ts, N, V, D, nw, _ = _loss(x, table, targets, scale)
+    device = _on_one_gpu(x, table, targets)
+    loss = x.new_empty(N, dtype=torch.float32)
+    lse = x.new_empty(N, dtype=torch.float32)
+    ws = _workspace(nw, x)
+    _call(device, "tbe_softmax_loss", x.data_ptr(), xs, table.data_ptr(), ts, targets.data_ptr(),
+          _INDEX[targets.dtype], scale, loss.data_ptr(), lse.data_ptr(), N, V, D, _DTYPE[x.dtype], _p(ws), nw)
+    return loss, lse
+
+
+def softmax_loss_backward(x, table, targets, lse, grad, scale=1.0, need_dx=True, need_dtable=True):
+    """Gradients (dx [N, D], dtable [V, D]) of softmax_loss, whose lse this is, from those of its
+    losses, grad fp32 [N].
+
+    Rows without a target have no part in either, whatever they hold.  What is not asked for is None.
+    """
+    xs, ts, N, V, D, _, nw = _loss(x, table, targets, scale)
+    _dense(lse, "lse", torch.float32, (N,))
+    _dense(grad, "grad", torch.float32, (N,))
+    device = _on_one_gpu(x, table, targets, lse, grad)
+    dx = x.new_empty((N, D)) if need_dx else None
+    dt = x.new_empty((V, D)) if need_dtable else None
+    ws = _workspace(nw, x)
+    _call(device, "tbe_softmax_loss_backward", x.data_ptr(), xs, table.data_ptr(), ts, targets.data_ptr(),
+          _INDEX[targets.dtype], scale, lse.data_ptr(), grad.data_ptr(), _p(dx), _p(dt), N, V, D, _DTYPE[x.dtype],
+          _p(ws), nw)
+    return dx, dt
