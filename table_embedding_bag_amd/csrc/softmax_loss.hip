@@ -56,6 +56,15 @@ void carve_backward(LossArgs* a, int32_t dtype, bool dx, bool dtable, Carver* c)
   const int64_t bytes = dtype_bytes(dtype);
   a->factor = static_cast<float*>(c->take(8));
   a->x_width = padded_width(a->K, bytes);
+  if (p.narrow) {
+    a->x_rows = c->take(a->rows * a->x_width * bytes);
+    a->row_info = static_cast<uint32_t*>(c->take(ceil_div(a->rows, 64) * kInfoBlock * 4));
+    if (dx && p.nx.splits > 1)
+      a->dx_parts = static_cast<float*>(c->take(p.nx.splits * a->rows * a->K * 4));
+    if (dtable && p.nw.splits > 1)
+      a->dw_parts = static_cast<float*>(c->take(p.nw.splits * a->vocab * a->K * 4));
+    return;
+  }
   a->x_rows = dtable ? c->take(a->rows * a->x_width * bytes) : nullptr;
   a->dlogits = c->take(a->rows * p.width * bytes);
   a->dx_parts = dx ? static_cast<float*>(c->take(p.x.splits * a->rows * a->K * 4)) : nullptr;
@@ -71,6 +80,10 @@ LossArgs args_of(int64_t rows, int64_t vocab, int64_t K, double scale) {
   a.scale = static_cast<float>(scale);
   a.exponent = static_cast<float>(scale * 1.44269504088896340736);
   return a;
+}
+
+bool takes_narrow(const LossArgs& a, int32_t dtype) {
+  return narrow_rows(a.K, dtype) && a.table_layout == kChunkRows;
 }
 
 // What both calls check of their inputs, with which it completes the arguments.
@@ -111,13 +124,16 @@ tbe_status tbe_softmax_loss_sizes(int64_t rows, int64_t vocab, int64_t dim, int3
   *backward_bytes = 256;
   if (rows == 0) return TBE_OK;
   LossArgs a = args_of(rows, vocab, dim, 1.0);
-  a.forward = plan_loss_forward(rows, vocab, dim, dtype);
-  a.backward = plan_loss_backward(rows, vocab, dim, dtype);
-  Carver f{nullptr}, b{nullptr};
-  carve_forward(&a, &f);
-  carve_backward(&a, dtype, true, true, &b);
-  *forward_bytes = f.used;
-  *backward_bytes = b.used;
+  *backward_bytes = 0;
+  for (int narrow = 0; narrow <= (narrow_rows(dim, dtype) ? 1 : 0); ++narrow) {  // by the alignment
+    a.forward = plan_loss_forward(rows, vocab, dim, narrow, dtype);
+    a.backward = plan_loss_backward(rows, vocab, dim, narrow, dtype);
+    Carver f{nullptr}, b{nullptr};
+    carve_forward(&a, &f);
+    carve_backward(&a, dtype, true, true, &b);
+    *forward_bytes = std::max(*forward_bytes, f.used);
+    *backward_bytes = std::max(*backward_bytes, b.used);
+  }
   return TBE_OK;
 }
 
@@ -133,7 +149,7 @@ tbe_status tbe_softmax_loss(const void* x, int64_t x_stride, const void* table, 
   if (!loss || !lse || !aligned_to(loss, 4) || !aligned_to(lse, 4)) return TBE_ERR_INVALID_ARGUMENT;
   a.loss = loss;
   a.lse = lse;
-  a.forward = plan_loss_forward(rows, vocab, dim, dtype);
+  a.forward = plan_loss_forward(rows, vocab, dim, takes_narrow(a, dtype), dtype);
   Carver c{static_cast<char*>(workspace)};
   carve_forward(&a, &c);
   if (!workspace || !aligned_to(workspace, 256)) return TBE_ERR_INVALID_ARGUMENT;
@@ -164,7 +180,7 @@ tbe_status tbe_softmax_loss_backward(const void* x, int64_t x_stride, const void
   a.dtable = dtable;
   Carver c{static_cast<char*>(workspace)};
   if (rows > 0) {
-    a.backward = plan_loss_backward(rows, vocab, dim, dtype);
+    a.backward = plan_loss_backward(rows, vocab, dim, takes_narrow(a, dtype), dtype);
     carve_backward(&a, dtype, dx, dtable, &c);
   } else {
     a.factor = static_cast<float*>(c.take(8));

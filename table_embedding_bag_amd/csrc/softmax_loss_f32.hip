@@ -1,8 +1,7 @@
 // softmax_loss_f32.hip -- the softmax loss's kernels for fp32 rows.
 #include <hip/hip_runtime.h>
 
-#define TBE_LOSS_KERNELS
-#include "softmax_loss.hpp"
+#include "loss_launch.hpp"
 
 namespace tbe {
 hipError_t launch_loss_f32(const LossArgs& a, bool backward, hipStream_t s) {

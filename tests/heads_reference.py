@@ -211,8 +211,10 @@ def loss(x, table, targets, scale=1.0, g=None, dtype=torch.float32):
         d = torch.where(on, d * g, 0)
         rel = dz + dlse[:, None] + 4 * U32 * (z.abs() + lse.abs()[:, None]) + 8 * U32
         # the machine's power of two gives 0 where it lies below the least normal number, 2^-126:
-        # a probability is off by up to that much
-        dd = torch.where(on, g.abs() * (p * rel + 2.0 ** -126), 0) + 4 * U32 * d.abs()
+        # a probability, or |g| times it, is off by up to that much (fp16's factor takes more than
+        # that off it again: it is 2^14 / max |g| at least)
+        lost = 2.0 ** -126 * g.abs().clamp(min=1)
+        dd = torch.where(on, g.abs() * p * rel + lost, 0) + 4 * U32 * d.abs()
         if dtype != torch.float32:
             dd = dd + half_step(dtype) * (d.abs() + dd)
         if dtype == torch.float16:   # 2^-25 of values that the largest row's 1 makes 2^14 at least

@@ -47,6 +47,36 @@ def test_larger(N, V, D, dtype):
     Problem(N, V, D, DTYPES[dtype], seed=1).check()
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [8, 16, 40, 64, 72, 104, 120, 128])
+@pytest.mark.parametrize("N,V", [(1, 127), (63, 128), (64, 129), (65, 63), (256, 64), (257, 65), (600, 1999)])
+def test_narrow_rows(N, V, D, dtype):
+    """Rows of whole 16-byte chunks, which stay in registers."""
+    Problem(N, V, D, DTYPES[dtype], seed=N + V + D).check()
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128, 200])
+def test_negative_and_zero_gradients(D, dtype):
+    for negative in (0.3, 1.0):
+        p = Problem(300, 500, D, DTYPES[dtype], seed=D)
+        way = torch.rand(300, generator=torch.Generator().manual_seed(1)).cuda()
+        p.grad[way < negative] *= -1
+        p.grad[way > 0.8] = 0
+        p.check()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_logits_that_grow_along_the_table(dtype):
+    """Each tile of the table brings larger logits than all before it, or smaller ones."""
+    for way in (1, -1):
+        p = Problem(70, 2000, 64, DTYPES[dtype], seed=5, left_out=0.0)
+        p.x[:] = 0.5
+        ramp = torch.linspace(-way * 100, way * 100, 2000, device="cuda") / 32
+        p.table[:] = ramp[:, None].to(p.dtype) + 0.01 * p.table
+        p.check()
+
+
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("wide", [3, 4, 8])
 def test_rows_of_wider_buffers(wide, dtype):
