@@ -18,7 +18,9 @@
 namespace tbe {
 namespace {
 
-constexpr int kRing = 4;  // tiles of the ring: one is read, two are in flight, one is filled
+// Tiles of the rings: the forward pass reads one while two are in flight and one is filled;
+// the gradients read two.
+constexpr int kRing = 4, kGradientRing = 5;
 
 // QW of the four waves have rows of Q of their own, the others share them and take other
 // rows of the tile; BL blocks of 32 rows of the tile are a wave's.
@@ -116,51 +118,47 @@ __device__ __forceinline__ void load_rows(const void* p, int64_t stride, int64_t
   }
 }
 
-// The logits of 32 rows of the tile (from row `block` on) and the wave's 64 of Q.
+// Steps of 16 values of the logits of 32 rows of a tile (from row `block` on) and the wave's
+// 64 of Q.
 template <int ST, typename S>
-__device__ __forceinline__ void narrow_logits(const unsigned char* tile, int block, int lane,
-                                              const u32x4 (&q)[2][S::KS], f32x16 (&z)[2]) {
-  const int row = block + (lane & 31), s = narrow_swizzle(lane & 31);
-  z[0] = f32x16{};
-  z[1] = f32x16{};
-#pragma unroll
-  for (int k = 0; k < S::KS; ++k) {
-    const int chunk = (2 * (k & 3) + (lane >> 5)) ^ s;
-    const u32x4 t = *reinterpret_cast<const u32x4*>(tile + ((k >> 2) * S::TR + row) * 128 + chunk * 16);
-    z[0] = multiply<ST>(t, q[0][k], z[0]);
-    z[1] = multiply<ST>(t, q[1][k], z[1]);
-  }
+__device__ __forceinline__ u32x4 tile_chunk(const unsigned char* tile, int block, int k, int lane) {
+  const int row = block + (lane & 31);
+  const int chunk = (2 * (k & 3) + (lane >> 5)) ^ narrow_swizzle(lane & 31);
+  return *reinterpret_cast<const u32x4*>(tile + ((k >> 2) * S::TR + row) * 128 + chunk * 16);
 }
 
-// acc[b][c] += the products of the tile's 32 rows' columns 32 c .. 32 c + 31 and d: the
-// summed index runs over rows in the order in which the logits came out, 4 (lane / 32) + i
-// and 8 more for the two halves of a step.
-template <int ST, typename S>
-__device__ __forceinline__ void narrow_product(const unsigned char* tile, int block, int lane,
-                                               const u32x4 (&d)[2][2], f32x16 (&acc)[2][2 * S::SL]) {
+// Columns 32 c .. 32 c + 31 of half t (16) of the tile's 32 rows from `block` on, an operand
+// whose summed index runs over rows in the order in which the logits come out:
+// 4 (lane / 32) + i, and 8 more for the second four.
+template <typename S>
+__device__ __forceinline__ u32x4 tile_columns(const unsigned char* tile, int block, int t, int c, int lane) {
   const int j = (lane & 15) >> 2, h = lane >> 5;
+  i16x4 half[2];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int c = 0; c < 2 * S::SL; ++c) {
-      i16x4 half[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = block + 16 * t + 8 * e + 4 * h + j;
-        const int chunk = (4 * (c & 1) + 2 * (lane >> 4 & 1) + (lane >> 1 & 1)) ^ ((j >> 1) << 2 | e << 1 | h);
-        const unsigned char* p = tile + ((c >> 1) * S::TR + row) * 128 + chunk * 16 + (lane & 1) * 8;
-        half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(TBE_LDS(i16x4, p));
-      }
-      const u32x4 a =
-          __builtin_bit_cast(u32x4, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
-      acc[0][c] = multiply<ST>(a, d[0][t], acc[0][c]);
-      acc[1][c] = multiply<ST>(a, d[1][t], acc[1][c]);
-    }
+  for (int e = 0; e < 2; ++e) {
+    const int row = block + 16 * t + 8 * e + 4 * h + j;
+    const int chunk = (4 * (c & 1) + 2 * (lane >> 4 & 1) + (lane >> 1 & 1)) ^ ((j >> 1) << 2 | e << 1 | h);
+    const unsigned char* p = tile + ((c >> 1) * S::TR + row) * 128 + chunk * 16 + (lane & 1) * 8;
+    half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(TBE_LDS(i16x4, p));
+  }
+  return __builtin_bit_cast(u32x4, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
+
+// A step is written as matrix instructions one by one, with a few vector instructions and
+// reads of LDS behind each, in its shadow: what is between two of these stays there.  Left to
+// itself the compiler puts all of one kind after all of another, and a matrix instruction
+// right behind another holds up what follows.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+constexpr int kReadAhead = 6;  // matrix instructions between a read and its use
 
 // What follows is done where the branch is taken alone: the compiler would rather do it
 // always and choose afterwards (the forward pass took every power twice).
 __device__ __forceinline__ void rarely() { asm volatile(""); }
+
+// v is computed here: the compiler would move that to where v is used, behind the next
+// branch and out of the matrix instructions' shadow.
+template <typename T>
+__device__ __forceinline__ void settled(T& v) { asm volatile("" : "+v"(v)); }
 
 // Which of the lane's 16 values of a block is row `at` of its 32, or -1.
 __device__ __forceinline__ int32_t element_of(int64_t at, bool real, int lane) {
@@ -173,20 +171,23 @@ __device__ __forceinline__ void subtract_at(f32x16& z, int32_t element, float v)
   for (int e = 0; e < 16; ++e) z[e] -= element == e ? v : 0.0f;
 }
 
-// f(the ring's buffer, the tile's number) for the tiles first .. last, each when it is there.
-template <typename Stream, typename F>
+// f(t, its buffer, the buffer of the tile before) for the tiles first .. last of a ring of
+// R, each when it is there; the LAG tiles before t are still being read.
+template <int R, int LAG, typename Stream, typename F>
 __device__ __forceinline__ void stream_tiles(const Stream& stream, int64_t first, int64_t last, F f) {
+  constexpr int kAhead = R - LAG - 2;  // in flight while t is read
 #pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) stream.load(first + i, i);
-  int at = 0;
+  for (int i = 0; i <= kAhead; ++i) stream.load(first + i, i);
+  int at = 0, before = 0;
   for (int64_t t = first; t < last; ++t) {
-    wait_loads<(kRing - 2) * Stream::loads>();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of the tile before
+    wait_loads<kAhead * Stream::loads>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of the buffer to fill
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    stream.load(t + kRing - 1, (at + kRing - 1) % kRing);  // past the end: zeros
-    f(at, t);
-    at = (at + 1) % kRing;
+    stream.load(t + kAhead + 1, at + kAhead + 1 < R ? at + kAhead + 1 : at + kAhead + 1 - R);
+    f(t, at, before);
+    before = at;
+    at = at + 1 < R ? at + 1 : 0;
   }
   wait_loads<0>();
 }
@@ -208,66 +209,108 @@ __global__ __launch_bounds__(kBlock, 2) void loss_narrow_forward(LossArgs a) {
   stream.init(a.table, a.table_stride, a.vocab, a.K, ring, wave, lane);
   u32x4 q[2][S::KS];
   load_rows<ST, S>(a.x, a.x_stride, n0, a.rows, a.K, lane, q);
-  float m[2] = {kNegInf, kNegInf}, sum[2] = {0.0f, 0.0f};
+  float from[2] = {0.0f, 0.0f}, sum[2] = {0.0f, 0.0f};  // what powers are relative to, their sum
+  bool unset[2] = {true, true};                          // no reference yet
   int64_t target[2];
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const int64_t n = n0 + 32 * b + (lane & 31);
     target[b] = n < a.rows ? target_of(a, n) : -1;
   }
+  // A step takes the logits of a block of the tile while it sums the powers of the block
+  // before: matrix and vector instructions in turn.
+  f32x16 z[2] = {f32x16{}, f32x16{}};
+  float part[2][4];
+  const auto sum_block = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[b][i] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      part[b][e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][e], a.exponent, -from[b]));
+  };
+  // What is done of a block once its powers are summed; v0: its first row.
+  const auto settle = [&](int64_t v0) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int32_t hit = element_of(target[b] - v0, target[b] >= 0, lane);
+      if (__any(hit >= 0)) {
+        rarely();
+        float logit = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) logit = hit == e ? z[b][e] : logit;
+        if (hit >= 0) a.target_logit[n0 + 32 * b + (lane & 31)] = logit;
+      }
+      float now = (part[b][0] + part[b][1]) + (part[b][2] + part[b][3]);
+      const bool again = unset[b] || !(now <= 0x1p80f);  // each lane for itself
+      if (__any(again)) {
+        rarely();
+        float top = z[b][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, z[b][e]);
+        const float next = fmaxf(unset[b] ? kNegInf : from[b], top * a.exponent);
+        const bool still = next == kNegInf;
+        const float keep = from[b], was = sum[b];
+        if (again) from[b] = still ? 0.0f : next;
+        sum_block(b);
+        if (again) {
+          now = (part[b][0] + part[b][1]) + (part[b][2] + part[b][3]);
+          sum[b] = unset[b] ? 0.0f : was * __builtin_amdgcn_exp2f(keep - from[b]);
+          unset[b] = still;
+        }
+      }
+      sum[b] += now;
+    }
+  };
+  const auto mask_end = [&](int64_t v0) {  // nothing past the table's end
+    if (a.vocab - v0 < 32) {
+      rarely();
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (place_of(0, e, lane) >= a.vocab - v0) z[0][e] = z[1][e] = kNegInf;
+    }
+  };
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads are counted from here
-  stream_tiles(stream, first, last, [&](int buffer, int64_t t) {
+  int64_t v_before = -1;  // of the block whose powers are due
+  stream_tiles<kRing, 0>(stream, first, last, [&](int64_t t, int buffer, int) {
     const unsigned char* tile = ring + buffer * S::stage;
 #pragma unroll
     for (int block = 0; block < S::BL; ++block) {
       const int at = 32 * (wave / S::QW * S::BL + block);
-      const int64_t v0 = t * S::TR + at, left = a.vocab - v0;
-      if (left <= 0) continue;
-      f32x16 z[2];
-      narrow_logits<ST, S>(tile, at, lane, q, z);
-      if (left < 32) {  // the last: nothing past the table's end
-        rarely();
+      f32x16 next[2] = {f32x16{}, f32x16{}};
+      u32x4 chunk[S::KS];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (place_of(0, e, lane) >= left) z[0][e] = z[1][e] = kNegInf;
-      }
+      for (int k = 0; k < 3; ++k) chunk[k] = tile_chunk<ST, S>(tile, at, k, lane);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int32_t hit = element_of(target[b] - v0, target[b] >= 0, lane);
-        if (__any(hit >= 0)) {
-          rarely();
-          float logit = 0.0f;
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) logit = hit == e ? z[b][e] : logit;
-          if (hit >= 0) a.target_logit[n0 + 32 * b + (lane & 31)] = logit;
-        }
-        const auto powers = [&](float from) {
-          float part[4] = {};
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            part[e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][e], a.exponent, -from));
-          return (part[0] + part[1]) + (part[2] + part[3]);
-        };
-        const bool unset = m[b] == kNegInf;
-        float part = powers(unset ? 0.0f : m[b]);
-        const bool again = unset || !(part <= 0x1p80f);  // each lane for itself
-        if (__any(again)) {
-          rarely();
-          float top = z[b][0];
-#pragma unroll
-          for (int e = 1; e < 16; ++e) top = fmaxf(top, z[b][e]);
-          const float next = fmaxf(m[b], top * a.exponent), from = next == kNegInf ? 0.0f : next;
-          const float other = powers(from);
-          if (again) {
-            part = other;
-            sum[b] *= __builtin_amdgcn_exp2f(m[b] - from);
-            m[b] = next;
-          }
-        }
-        sum[b] += part;
-      }
+        for (int i = 0; i < 4; ++i) part[b][i] = 0.0f;
+      repeat<0, 2 * S::KS>([&](auto op_) {
+        constexpr int op = op_, k = op / 2, kEach = 16 / S::KS;  // powers behind each
+        in_order();
+        next[op % 2] = multiply<ST>(chunk[k], q[op % 2][k], next[op % 2]);
+        if constexpr (op % 2 == 0 && k + 3 < S::KS) chunk[k + 3] = tile_chunk<ST, S>(tile, at, k + 3, lane);
+        repeat<op * kEach, (op + 1) * kEach>([&](auto i_) {
+          constexpr int b = i_ / 16, e = i_ % 16;
+          part[b][e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][e], a.exponent, -from[b]));
+          settled(part[b][e & 3]);
+        });
+      });
+      in_order();
+      if (v_before >= 0) settle(v_before);
+      z[0] = next[0];
+      z[1] = next[1];
+      v_before = t * S::TR + at;
+      mask_end(v_before);
     }
   });
+  if (v_before >= 0) {
+    sum_block(0);
+    sum_block(1);
+    settle(v_before);
+  }
+  float m[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) m[b] = unset[b] ? kNegInf : from[b];
   // the two halves of a wave, then the waves that share their rows
   __syncthreads();
   float2* joined = reinterpret_cast<float2*>(ring);
@@ -290,11 +333,11 @@ __global__ __launch_bounds__(kBlock, 2) void loss_narrow_forward(LossArgs a) {
 // One gradient, of the table (DTABLE) or of x: of 256 rows of Q, summed over a part of T's
 // tiles.  Sums go to the part, or rounded to the output where there is one.
 template <int ST, typename S, bool DTABLE>
-__global__ __launch_bounds__(kBlock, 2) void loss_narrow_gradient(LossArgs a, int64_t splits, int64_t run,
+__global__ __launch_bounds__(kBlock, 1) void loss_narrow_gradient(LossArgs a, int64_t splits, int64_t run,
                                                                   float* parts, void* out) {
   static_assert(S::QW == 4 && S::BL == 2 && S::TR == 64);
-  __shared__ __align__(1024) unsigned char ring[kRing * S::stage];
-  __shared__ __align__(1024) unsigned char info_ring[DTABLE ? kRing * kInfoBytes : 16];
+  __shared__ __align__(1024) unsigned char ring[kGradientRing * S::stage];
+  __shared__ __align__(1024) unsigned char info_ring[DTABLE ? kGradientRing * kInfoBytes : 16];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t rows_q = DTABLE ? a.vocab : a.rows, rows_t = DTABLE ? a.rows : a.vocab;
   const int64_t nb = (rows_q + S::QR - 1) / S::QR;
@@ -328,79 +371,169 @@ __global__ __launch_bounds__(kBlock, 2) void loss_narrow_gradient(LossArgs a, in
       grad[b] = fabsf(__uint_as_float(info[128]));
     }
   }
-  f32x16 acc[2][2 * S::SL];
+  f32x16 acc[2][2 * S::SL], z[2];
+  u32x4 d[2][2];  // of a block, rounded to the rows' type: operands of the product
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
+  for (int b = 0; b < 2; ++b) {
 #pragma unroll
     for (int c = 0; c < 2 * S::SL; ++c) acc[b][c] = f32x16{};
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads are counted from here
-  stream_tiles(stream, first, last, [&](int buffer, int64_t t) {
-    const unsigned char* tile = ring + buffer * S::stage;
-    const float* bases = reinterpret_cast<const float*>(info_ring + buffer * kInfoBytes);
-    const int32_t* words = reinterpret_cast<const int32_t*>(bases + 64);
-    const float* grads = bases + 128;
 #pragma unroll
-    for (int block = 0; block < S::BL; ++block) {
-      const int64_t t0 = t * S::TR + 32 * block;
-      f32x16 z[2];
-      narrow_logits<ST, S>(tile, 32 * block, lane, q, z);
-      if constexpr (DTABLE) {
+    for (int e = 0; e < 16; ++e) z[b][e] = kNegInf;  // powers of 0 before the first block
+    d[b][0] = d[b][1] = u32x4{};
+  }
+  f32x4 bases[4];  // DTABLE: of the rows of z, lane / 32's share
+#pragma unroll
+  for (int p = 0; p < 4; ++p) bases[p] = f32x4{};
+  const auto read_bases = [&](const unsigned char* info, int at, int p) {
+    if constexpr (DTABLE) bases[p] = *reinterpret_cast<const f32x4*>(info + (at + 8 * p + 4 * (lane >> 5)) * 4);
+  };
+  // The i-th power of z.
+  const auto power = [&](auto i_) {
+    constexpr int i = i_, b = i / 16, e = i % 16;
+    float p = __builtin_amdgcn_exp2f(
+        __builtin_fmaf(z[b][e], a.exponent, DTABLE ? -bases[e / 4][e % 4] : -base[b]));
+    settled(p);
+    z[b][e] = p;
+  };
+  // The gradients of the logits from their powers; t0: the block's first row of T (real:
+  // there is such a block).
+  const auto settle = [&](const unsigned char* info, int at, int64_t t0, bool real) {
+    if constexpr (DTABLE) {
+      // where the wave has a row's target, or a row's gradient is negative
+      const int32_t* words = reinterpret_cast<const int32_t*>(info + 256) + at;
+      const float* grads = reinterpret_cast<const float*>(info + 512) + at;
+      const int32_t word = words[lane & 31];
+      const int64_t hit = (word & ~kNegative) - q0;
+      if (real && __any(word >= 0 && ((hit >= 0 && hit < 64) || (word & kNegative)))) {
+        rarely();
+        const int32_t v = static_cast<int32_t>(q0) + (lane & 31);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const f32x4 four = *reinterpret_cast<const f32x4*>(bases + 32 * block + 8 * p + 4 * (lane >> 5));
+          const u32x4 w4 = *reinterpret_cast<const u32x4*>(words + 8 * p + 4 * (lane >> 5));
+          const f32x4 g4 = *reinterpret_cast<const f32x4*>(grads + 8 * p + 4 * (lane >> 5));
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              z[b][4 * p + e] =
-                  __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][4 * p + e], a.exponent, -four[e]));
-        }
-        // where the wave has a row's target, or a row's gradient is negative
-        const int32_t word = words[32 * block + (lane & 31)];
-        const int64_t hit = (word & ~kNegative) - q0;
-        if (__any(word >= 0 && ((hit >= 0 && hit < 64) || (word & kNegative)))) {
-          rarely();
-          const int32_t v = static_cast<int32_t>(q0) + (lane & 31);
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const int at = 32 * block + 8 * p + 4 * (lane >> 5);
-            const u32x4 w4 = *reinterpret_cast<const u32x4*>(words + at);
-            const f32x4 g4 = *reinterpret_cast<const f32x4*>(grads + at);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int32_t w = static_cast<int32_t>(w4[e]), t = w & ~kNegative;  // none: below 0
-              if (w >= 0 && w != t) z[0][4 * p + e] = -z[0][4 * p + e], z[1][4 * p + e] = -z[1][4 * p + e];
-              z[0][4 * p + e] -= t == v ? g4[e] : 0.0f;
-              z[1][4 * p + e] -= t == v + 32 ? g4[e] : 0.0f;
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            z[b][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][e], a.exponent, -base[b]));
-          const int32_t hit = element_of((target[b] & ~kNegative) - t0, target[b] >= 0, lane);
-          if (__any(hit >= 0)) {
-            rarely();
-            subtract_at(z[b], hit, grad[b]);
+          for (int e = 0; e < 4; ++e) {
+            const int32_t w = static_cast<int32_t>(w4[e]), target_v = w & ~kNegative;  // none: below 0
+            if (w >= 0 && w != target_v)
+              z[0][4 * p + e] = -z[0][4 * p + e], z[1][4 * p + e] = -z[1][4 * p + e];
+            z[0][4 * p + e] -= target_v == v ? g4[e] : 0.0f;
+            z[1][4 * p + e] -= target_v == v + 32 ? g4[e] : 0.0f;
           }
         }
       }
-      u32x4 d[2][2];  // rounded to the rows' type: operands of the product
+    } else {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          StoredVec<ST, 8> v;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = static_cast<typename Stored<ST>::type>(z[b][8 * s + e]);
-          d[b][s] = __builtin_bit_cast(u32x4, v);
+      for (int b = 0; b < 2; ++b) {
+        const int32_t hit = element_of((target[b] & ~kNegative) - t0, target[b] >= 0, lane);
+        if (real && __any(hit >= 0)) {
+          rarely();
+          subtract_at(z[b], hit, grad[b]);
         }
-      narrow_product<ST, S>(tile, 32 * block, lane, d, acc);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        StoredVec<ST, 8> v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = static_cast<typename Stored<ST>::type>(z[b][8 * s + e]);
+        d[b][s] = __builtin_bit_cast(u32x4, v);
+      }
+  };
+  // The i-th of the product's 4 SL parts, and the tile's columns for it.
+  const auto columns_of = [&](const unsigned char* tile, int at, int i) {
+    return tile_columns<S>(tile, at, i / (2 * S::SL), i % (2 * S::SL), lane);
+  };
+  const auto product = [&](const u32x4& columns, int i) {
+    const int t = i / (2 * S::SL), c = i % (2 * S::SL);
+    acc[0][c] = multiply<ST>(columns, d[0][t], acc[0][c]);
+    acc[1][c] = multiply<ST>(columns, d[1][t], acc[1][c]);
+  };
+  u32x4 ahead[4];  // of the next step's first parts, read a step before
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ahead[i] = u32x4{};
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads are counted from here
+  // A step has three blocks in hand, one after the other in T: the logits of one, the powers
+  // of the one before, the product of the one before that (in the tile before): matrix and
+  // vector instructions in turn.
+  const unsigned char *tile_before = ring, *info_before = info_ring;
+  stream_tiles<kGradientRing, 1>(stream, first, last, [&](int64_t t, int buffer, int before) {
+    const unsigned char* tile = ring + buffer * S::stage;
+    const unsigned char* info = info_ring + (DTABLE ? buffer * kInfoBytes : 0);
+    tile_before = ring + before * S::stage;
+    info_before = info_ring + (DTABLE ? before * kInfoBytes : 0);
+#pragma unroll
+    for (int block = 0; block < 2; ++block) {
+      f32x16 next[2] = {f32x16{}, f32x16{}};
+      // The matrix instructions: the product's first four parts, whose columns are there, then
+      // the logits with the other parts between them.  Reads come kReadAhead before their use,
+      // those for the next step's start at the end.
+      constexpr int kOps = 4 * S::KS, kRest = 4 * S::SL - 4;
+      u32x4 chunk[S::KS], rest[kRest ? kRest : 1];
+      const unsigned char* due = block == 0 ? info_before : info;
+      repeat<0, kOps>([&](auto op_) {
+        constexpr int op = op_;
+        in_order();
+        // Behind the first 8 come groups of 6: logits 2 k, logits 2 k + 1, part 4 + k; or, of
+        // short rows, of 2.
+        constexpr int kGroup = kRest ? 6 : 4, at = op - 8;
+        constexpr int pair = at >= 0 ? at / kGroup : 0, in = at >= 0 ? at % kGroup : 0;
+        if constexpr (op < 8) {
+          constexpr int i = op / 2, c = i % (2 * S::SL), s = i / (2 * S::SL);
+          acc[op % 2][c] = multiply<ST>(ahead[i], d[op % 2][s], acc[op % 2][c]);
+        } else if constexpr (in < 4) {
+          constexpr int k = 2 * pair + in / 2;
+          next[in % 2] = multiply<ST>(chunk[k], q[in % 2][k], next[in % 2]);
+        } else {
+          constexpr int i = 4 + pair, c = i % (2 * S::SL), s = i / (2 * S::SL);
+          acc[in % 2][c] = multiply<ST>(rest[pair], d[in % 2][s], acc[in % 2][c]);
+        }
+        constexpr int ahead_at = op + kReadAhead - 8;
+        constexpr int pair_r = ahead_at >= 0 ? ahead_at / kGroup : 0, in_r = ahead_at >= 0 ? ahead_at % kGroup : 1;
+        if constexpr (op + kReadAhead < kOps) {
+          if constexpr (in_r == 0 || in_r == 2) {
+            constexpr int k = 2 * pair_r + in_r / 2;
+            chunk[k] = tile_chunk<ST, S>(tile, 32 * block, k, lane);
+          }
+          if constexpr (in_r == 4) rest[pair_r] = columns_of(tile_before, 32 * block, 4 + pair_r);
+        }
+        if constexpr (kOps - op <= 4) {
+          constexpr int i = 4 - (kOps - op);
+          ahead[i] = block == 0 ? columns_of(tile_before, 32, i) : columns_of(tile, 0, i);
+        }
+        constexpr int kEach = 32 / kOps;  // powers
+        repeat<op * kEach, (op + 1) * kEach>(power);
+      });
+      in_order();
+#pragma unroll
+      for (int p = 0; p < 4; ++p) read_bases(info, 32 * block, p);  // of `next`
+      settle(due, block == 0 ? 32 : 0, t * S::TR - (block == 0 ? 32 : 0),
+             block == 1 || t > first);
+      if constexpr (!DTABLE) {  // rows past the table's end: no powers
+        if (rows_t - t * S::TR - 32 * block < 32) {
+          rarely();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (place_of(0, e, lane) >= rows_t - t * S::TR - 32 * block) next[0][e] = next[1][e] = kNegInf;
+        }
+      }
+      z[0] = next[0];
+      z[1] = next[1];
     }
   });
+  // the last tile's products, its second block's powers
+  {
+    const int buffer = static_cast<int>((last - 1 - first) % kGradientRing);
+    tile_before = ring + buffer * S::stage;
+    info_before = info_ring + (DTABLE ? buffer * kInfoBytes : 0);
+#pragma unroll
+    for (int i = 0; i < 4 * S::SL; ++i) product(columns_of(tile_before, 0, i), i);
+    repeat<0, 32>(power);
+    settle(info_before, 32, (last - 1) * S::TR + 32, true);
+#pragma unroll
+    for (int i = 0; i < 4 * S::SL; ++i) product(columns_of(tile_before, 32, i), i);
+  }
   const float undo = out ? a.factor[1] : 1.0f;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {

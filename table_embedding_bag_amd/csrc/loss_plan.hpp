@@ -72,7 +72,7 @@ struct LossNarrowPlan {
 };
 inline LossNarrowPlan plan_loss_narrow(int64_t out_rows, int64_t other_rows) {
   const int64_t tiles = ceil_div(other_rows, 64);
-  const int64_t want = std::max<int64_t>(1, 512 / ceil_div(out_rows, 256));
+  const int64_t want = std::max<int64_t>(1, 256 / ceil_div(out_rows, 256));
   LossNarrowPlan p{};
   p.run = ceil_div(tiles, std::min(want, tiles));
   p.splits = ceil_div(tiles, p.run);
