@@ -160,11 +160,10 @@ __device__ __forceinline__ void rarely() { asm volatile(""); }
 template <typename T>
 __device__ __forceinline__ void settled(T& v) { asm volatile("" : "+v"(v)); }
 
-// Which of the lane's 16 values of a block is row `at` of its 32, or -1.
-__device__ __forceinline__ int32_t element_of(int64_t at, bool real, int lane) {
-  if (!real || at < 0 || at >= 32 || (at >> 2 & 1) != lane >> 5) return -1;
-  const int32_t r = static_cast<int32_t>(at);
-  return (r >> 3) * 4 + (r & 3);
+// Which of the lane's 16 values of a block is row `at` (where real: in 0 .. 31), or -1.
+__device__ __forceinline__ int32_t element_of(int32_t at, bool real, int lane) {
+  if (!real || (at >> 2 & 1) != lane >> 5) return -1;
+  return (at >> 3) * 4 + (at & 3);
 }
 __device__ __forceinline__ void subtract_at(f32x16& z, int32_t element, float v) {
 #pragma unroll
@@ -211,55 +210,60 @@ __global__ __launch_bounds__(kBlock, 2) void loss_narrow_forward(LossArgs a) {
   load_rows<ST, S>(a.x, a.x_stride, n0, a.rows, a.K, lane, q);
   float from[2] = {0.0f, 0.0f}, sum[2] = {0.0f, 0.0f};  // what powers are relative to, their sum
   bool unset[2] = {true, true};                          // no reference yet
-  int64_t target[2];
+  int32_t target[2];  // tables have at most 2^30 rows
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const int64_t n = n0 + 32 * b + (lane & 31);
-    target[b] = n < a.rows ? target_of(a, n) : -1;
+    target[b] = n < a.rows ? static_cast<int32_t>(target_of(a, n)) : -1;
   }
   // A step takes the logits of a block of the tile while it sums the powers of the block
   // before: matrix and vector instructions in turn.
   f32x16 z[2] = {f32x16{}, f32x16{}};
   float part[2][4];
-  const auto sum_block = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) part[b][i] = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      part[b][e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][e], a.exponent, -from[b]));
+  const auto add_power = [&](int b, int e) {
+    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][e], a.exponent, -from[b]));
+    part[b][e & 3] = e < 4 ? p : part[b][e & 3] + p;
   };
+  const auto block_sum = [&](int b) { return (part[b][0] + part[b][1]) + (part[b][2] + part[b][3]); };
   // What is done of a block once its powers are summed; v0: its first row.
   const auto settle = [&](int64_t v0) {
+    const int32_t first_v = static_cast<int32_t>(v0);
+    const auto near = [&](int b) { return static_cast<uint32_t>(target[b] - first_v) < 32u; };  // none: no
+    if (__any(near(0) || near(1))) {
+      rarely();
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int32_t hit = element_of(target[b] - v0, target[b] >= 0, lane);
-      if (__any(hit >= 0)) {
-        rarely();
+      for (int b = 0; b < 2; ++b) {
+        const int32_t hit = element_of(target[b] - first_v, near(b), lane);
         float logit = 0.0f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) logit = hit == e ? z[b][e] : logit;
         if (hit >= 0) a.target_logit[n0 + 32 * b + (lane & 31)] = logit;
       }
-      float now = (part[b][0] + part[b][1]) + (part[b][2] + part[b][3]);
-      const bool again = unset[b] || !(now <= 0x1p80f);  // each lane for itself
-      if (__any(again)) {
-        rarely();
+    }
+    float now[2] = {block_sum(0), block_sum(1)};
+    const auto again = [&](int b) { return unset[b] || !(now[b] <= 0x1p80f); };  // each lane for itself
+    if (__any(again(0) || again(1))) {
+      rarely();
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
         float top = z[b][0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) top = fmaxf(top, z[b][e]);
         const float next = fmaxf(unset[b] ? kNegInf : from[b], top * a.exponent);
-        const bool still = next == kNegInf;
-        const float keep = from[b], was = sum[b];
-        if (again) from[b] = still ? 0.0f : next;
-        sum_block(b);
-        if (again) {
-          now = (part[b][0] + part[b][1]) + (part[b][2] + part[b][3]);
-          sum[b] = unset[b] ? 0.0f : was * __builtin_amdgcn_exp2f(keep - from[b]);
+        const bool still = next == kNegInf, change = again(b);
+        const float keep = from[b];
+        if (change) from[b] = still ? 0.0f : next;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) add_power(b, e);
+        if (change) {
+          now[b] = block_sum(b);
+          sum[b] = unset[b] ? 0.0f : sum[b] * __builtin_amdgcn_exp2f(keep - from[b]);
           unset[b] = still;
         }
       }
-      sum[b] += now;
     }
+    sum[0] += now[0];
+    sum[1] += now[1];
   };
   const auto mask_end = [&](int64_t v0) {  // nothing past the table's end
     if (a.vocab - v0 < 32) {
@@ -280,10 +284,6 @@ __global__ __launch_bounds__(kBlock, 2) void loss_narrow_forward(LossArgs a) {
       u32x4 chunk[S::KS];
 #pragma unroll
       for (int k = 0; k < 3; ++k) chunk[k] = tile_chunk<ST, S>(tile, at, k, lane);
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[b][i] = 0.0f;
       repeat<0, 2 * S::KS>([&](auto op_) {
         constexpr int op = op_, k = op / 2, kEach = 16 / S::KS;  // powers behind each
         in_order();
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kBlock, 2) void loss_narrow_forward(LossArgs a) {
         if constexpr (op % 2 == 0 && k + 3 < S::KS) chunk[k + 3] = tile_chunk<ST, S>(tile, at, k + 3, lane);
         repeat<op * kEach, (op + 1) * kEach>([&](auto i_) {
           constexpr int b = i_ / 16, e = i_ % 16;
-          part[b][e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][e], a.exponent, -from[b]));
+          add_power(b, e);
           settled(part[b][e & 3]);
         });
       });
@@ -304,8 +304,8 @@ __global__ __launch_bounds__(kBlock, 2) void loss_narrow_forward(LossArgs a) {
     }
   });
   if (v_before >= 0) {
-    sum_block(0);
-    sum_block(1);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) add_power(0, e), add_power(1, e);
     settle(v_before);
   }
   float m[2];
@@ -403,7 +403,7 @@ __global__ __launch_bounds__(kBlock, 1) void loss_narrow_gradient(LossArgs a, in
       const int32_t* words = reinterpret_cast<const int32_t*>(info + 256) + at;
       const float* grads = reinterpret_cast<const float*>(info + 512) + at;
       const int32_t word = words[lane & 31];
-      const int64_t hit = (word & ~kNegative) - q0;
+      const int32_t hit = (word & ~kNegative) - static_cast<int32_t>(q0);
       if (real && __any(word >= 0 && ((hit >= 0 && hit < 64) || (word & kNegative)))) {
         rarely();
         const int32_t v = static_cast<int32_t>(q0) + (lane & 31);
@@ -424,10 +424,11 @@ __global__ __launch_bounds__(kBlock, 1) void loss_narrow_gradient(LossArgs a, in
     } else {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int32_t hit = element_of((target[b] & ~kNegative) - t0, target[b] >= 0, lane);
-        if (real && __any(hit >= 0)) {
+        const int32_t at = (target[b] & ~kNegative) - static_cast<int32_t>(t0);
+        const bool near = target[b] >= 0 && static_cast<uint32_t>(at) < 32u;
+        if (real && __any(near)) {
           rarely();
-          subtract_at(z[b], hit, grad[b]);
+          subtract_at(z[b], element_of(at, near, lane), grad[b]);
         }
       }
     }
