@@ -514,8 +514,8 @@ typedef enum {
  * arithmetic on the given values, down to differences of 64-bit rounding; of
  * equal ones the lower index is better.  ids [rows][k]: the chosen experts, the
  * best first; weights fp32 [rows][k]: their scores without the bias, divided by
- * their sum where `renormalize` is not 0, times scale.  A NaN logit counts as
- * -infinity, +infinity as the largest float; an expert whose logit is
+ * their sum where `renormalize` is not 0, times scale.  A NaN logit or bias counts
+ * as -infinity, +infinity as the largest float; an expert whose logit is
  * -infinity has the score 0 and, where chosen for want of others, the weight 0.
  * experts at most 1024, groups and k at most 16, rows at most 2^25. */
 tbe_status tbe_route(const void* logits, int64_t logits_stride, const float* bias, int32_t* ids,

@@ -110,6 +110,21 @@ def test_masked_experts(dtype, renormalize, scores):
             assert not w[2].any() and not w[6].any() and not d[2].any() and not torch.isnan(w).any()
 
 
+@pytest.mark.parametrize("E,groups,top", [(48, 1, 1), (256, 8, 3), (320, 16, 9)])
+def test_biases_that_close_experts(E, groups, top):
+    """-inf and NaN biases: the expert is chosen for want of others only, the lowest index first."""
+    x = logits_of(50, E, torch.float32, seed=11)
+    for first in (E // 2, 3, 0):
+        bias = bias_of(E)
+        bias[first:] = -torch.inf
+        for scores in ("softmax", "sigmoid"):
+            want = check(x, 6, bias=bias, scores=scores, groups=groups, top_groups=top, group_score="max")
+            other = bias.clone()
+            other[first + 1::2] = float("nan")
+            got = tbe.route(x, 6, bias=other, scores=scores, groups=groups, top_groups=top, group_score="max")
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_strided_rows_and_outputs():
     wide = logits_of(60, 90, torch.bfloat16, seed=4)
     view = wide[:, 3:80]
