@@ -18,8 +18,9 @@ using namespace tbe;
 namespace {
 
 constexpr int kMaxExperts = 2048;
-constexpr int64_t kTile = 4096;      // assignments a workgroup, or more:
+constexpr int64_t kTile = 2048;      // assignments a workgroup, or more:
 constexpr int64_t kMostTiles = 256;  // every workgroup reads all tiles' counts
+constexpr int kAtATime = 8;          // assignments a lane that are on their way together
 
 struct PlanArgs {
   const void* ids;
@@ -39,15 +40,31 @@ __device__ __forceinline__ int expert_of(const PlanArgs& a, int64_t i) {
   return e >= 0 && e < a.experts ? static_cast<int>(e) : -1;
 }
 
+// f(assignment, its expert) for from .. end, `step` lanes side by side; every lane takes part
+// to the end (expert -1 past it).
+template <typename F>
+__device__ __forceinline__ void for_experts(const PlanArgs& a, int64_t from, int64_t end, int lane, int step, F f) {
+  for (int64_t i0 = from; i0 < end; i0 += kAtATime * step) {
+    int e[kAtATime];
+#pragma unroll
+    for (int i = 0; i < kAtATime; ++i) {
+      const int64_t at = i0 + i * step + lane;
+      e[i] = at < end ? expert_of(a, at) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kAtATime; ++i)
+      if (i0 + i * step < end) f(i0 + i * step + lane, e[i]);
+  }
+}
+
 __global__ __launch_bounds__(kBlock) void plan_count(PlanArgs a) {
   __shared__ uint32_t count[kMaxExperts];
   for (int e = threadIdx.x; e < a.experts; e += kBlock) count[e] = 0;
   __syncthreads();
   const int64_t from = blockIdx.x * a.tile, end = std::min(from + a.tile, a.n);
-  for (int64_t i = from + threadIdx.x; i < end; i += kBlock) {
-    const int e = expert_of(a, i);
+  for_experts(a, from, end, threadIdx.x, kBlock, [&](int64_t, int e) {
     if (e >= 0) atomicAdd(&count[e], 1u);
-  }
+  });
   __syncthreads();
   for (int e = threadIdx.x; e < a.experts; e += kBlock)
     a.counts[static_cast<int64_t>(blockIdx.x) * a.experts + e] = count[e];
@@ -58,6 +75,7 @@ __global__ __launch_bounds__(kBlock) void plan_count(PlanArgs a) {
 __global__ __launch_bounds__(kBlock) void plan_place(PlanArgs a) {
   __shared__ uint32_t next[kWavesPerBlock][kMaxExperts];
   __shared__ uint32_t scratch[kWavesPerBlock];
+  __shared__ uint2 slices[kBlock];
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   for (int w = 0; w < kWavesPerBlock; ++w)
     for (int e = threadIdx.x; e < a.experts; e += kBlock) next[w][e] = 0;
@@ -65,33 +83,42 @@ __global__ __launch_bounds__(kBlock) void plan_place(PlanArgs a) {
   const int64_t quarter = a.tile / kWavesPerBlock;
   const int64_t tile_end = std::min((blockIdx.x + int64_t{1}) * a.tile, a.n);
   const int64_t from = blockIdx.x * a.tile + wave * quarter, end = std::min(from + quarter, tile_end);
-  for (int64_t i = from + lane; i < end; i += kWave) {
-    const int e = expert_of(a, i);
+  for_experts(a, from, end, lane, kWave, [&](int64_t, int e) {
     if (e >= 0) atomicAdd(&next[wave][e], 1u);
-  }
+  });
   __syncthreads();
-  // starts: the experts before, the tiles before, the quarters before
+  // Starts: the experts before, the tiles before, the quarters before.  Where there are fewer
+  // experts than threads, several threads go through one's tiles.
+  const int width = a.experts < kBlock ? 1 << a.bits : kBlock;  // experts at a time
+  const int column = threadIdx.x & (width - 1), slice = threadIdx.x / width;
   uint32_t before_all = 0;
-  for (int e0 = 0; e0 < a.experts; e0 += kBlock) {
-    const int e = e0 + threadIdx.x;
-    uint32_t mine = 0, before = 0, total = 0;
-    if (e < a.experts) {
-      for (int w = 0; w < kWavesPerBlock; ++w) mine += next[w][e];
-      total = mine;
-      if (a.counts) {
-        total = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += width) {
+    const int e = e0 + column;
+    const bool is = slice == 0 && e < a.experts;
+    uint32_t before = 0, total = 0;
+    if (a.counts) {
+      if (e < a.experts)
 #pragma unroll 8
-        for (int64_t t = 0; t < a.tiles; ++t) {
+        for (int64_t t = slice; t < a.tiles; t += kBlock / width) {
           const uint32_t c = a.counts[t * a.experts + e];
           total += c;
           before += t < blockIdx.x ? c : 0u;
         }
-      }
+      slices[threadIdx.x] = make_uint2(total, before);
+      __syncthreads();
+      if (is)
+        for (int i = 1; i < kBlock / width; ++i) {
+          total += slices[i * width + column].x;
+          before += slices[i * width + column].y;
+        }
+      __syncthreads();
+    } else if (is) {
+      for (int w = 0; w < kWavesPerBlock; ++w) total += next[w][e];
     }
     uint32_t sum;
-    const uint32_t start = before_all + block_exclusive_sum(total, scratch, &sum);
+    const uint32_t start = before_all + block_exclusive_sum(is ? total : 0u, scratch, &sum);
     before_all += sum;
-    if (e < a.experts) {
+    if (is) {
       uint32_t at = start + before;
       for (int w = 0; w < kWavesPerBlock; ++w) {
         const uint32_t c = next[w][e];
@@ -103,9 +130,7 @@ __global__ __launch_bounds__(kBlock) void plan_place(PlanArgs a) {
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.experts] = before_all;
   __syncthreads();
-  for (int64_t i0 = from; i0 < end; i0 += kWave) {
-    const int64_t i = i0 + lane;
-    const int e = i < end ? expert_of(a, i) : -1;
+  for_experts(a, from, end, lane, kWave, [&](int64_t i, int e) {
     const uint64_t real = __ballot(e >= 0);
     const uint64_t peers = match_low_bits(real, static_cast<uint32_t>(e), a.bits);
     const uint32_t rank = popc_below(peers);
@@ -116,7 +141,7 @@ __global__ __launch_bounds__(kBlock) void plan_place(PlanArgs a) {
     }
     __builtin_amdgcn_wave_barrier();
     if (i < end) a.places[i] = place;
-  }
+  });
 }
 
 struct MoveArgs {
@@ -197,15 +222,24 @@ __global__ __launch_bounds__(kBlock) void combine_rows(MoveArgs a) {
 #pragma unroll
       for (int i = 0; i < E; ++i) sum[i] = static_cast<float>(r.v[i]);
     }
-#pragma unroll 4
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t p = place_of(a, n * a.k + j);
-      if (p < 0) continue;
-      const float w = a.weights ? a.weights[n * a.k + j] : 1.0f;
-      Chunk<ST> v;
-      v.load(a.x, p * a.x_stride, c, a.cols);
+    // Four rows at a time, on their way together: one that is not there is read at place 0 and
+    // left out.
+    for (int j0 = 0; j0 < a.k; j0 += 4) {
+      int64_t p[4];
+      float w[4];
+      Chunk<ST> v[4];
 #pragma unroll
-      for (int i = 0; i < E; ++i) sum[i] += w * static_cast<float>(v.v[i]);
+      for (int j = 0; j < 4; ++j) {
+        p[j] = j0 + j < a.k ? place_of(a, n * a.k + j0 + j) : -1;
+        w[j] = a.weights && j0 + j < a.k ? a.weights[n * a.k + j0 + j] : 1.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j0 + j < a.k) v[j].load(a.x, (p[j] < 0 ? 0 : p[j]) * a.x_stride, c, a.cols);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < E; ++i) sum[i] += p[j] < 0 ? 0.0f : w[j] * static_cast<float>(v[j].v[i]);
     }
     Chunk<ST> out;
 #pragma unroll
