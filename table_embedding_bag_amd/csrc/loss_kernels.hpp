@@ -12,6 +12,17 @@ namespace {
 constexpr float kNegInf = -__builtin_inff();
 constexpr int32_t kNegative = 1 << 30;  // of a row's target: its gradient is negative
 
+// What loss_prepare works out of row n.
+struct RowInfo {
+  float base;
+  int32_t target;
+  float grad;
+};
+__device__ __forceinline__ RowInfo row_info(const LossArgs& a, int64_t n) {
+  const uint32_t* p = a.row_info + n / 64 * kInfoBlock + n % 64;
+  return RowInfo{__uint_as_float(p[0]), static_cast<int32_t>(p[64]), __uint_as_float(p[128])};
+}
+
 // The target of row n, or -1 where it has none (or one outside the table).
 __device__ __forceinline__ int64_t target_of(const LossArgs& a, int64_t n) {
   const int64_t t = a.index64 ? static_cast<const int64_t*>(a.targets)[n]
@@ -157,60 +168,63 @@ __global__ __launch_bounds__(kBlock) void loss_join(LossArgs a) {
   }
 }
 
+// fp16 gradients of the logits are multiplied by 2^14 over the largest row gradient's power
+// of two, so that probabilities down to 2^-28 of it stay normal numbers: that factor, what
+// undoes it times the scale, and its exponent.
+__global__ __launch_bounds__(1024) void loss_factor(LossArgs a) {
+  __shared__ float part[16];
+  float top = 0.0f;
+#pragma unroll 4
+  for (int64_t n = threadIdx.x; n < a.rows; n += 1024)
+    top = fmaxf(top, target_of(a, n) >= 0 ? fabsf(a.grad[n]) : 0.0f);
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if (lane_id() == 0) part[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 0; w < 16; ++w) top = fmaxf(top, part[w]);
+  int e = 0;
+  if (top > 0.0f && top <= 3.0e38f) {
+    frexpf(top, &e);
+    e = 15 - e;  // top 2^e lies in [2^14, 2^15)
+    e = e > 120 ? 120 : e;
+  }
+  a.factor[0] = ldexpf(1.0f, e);
+  a.factor[1] = ldexpf(a.scale, -e);
+  a.factor[2] = static_cast<float>(e);
+}
+
 // x for the gradients' products: rows without a target are zeros, whatever they hold, and
-// so is what follows a row's end.  fp16 gradients of the logits are multiplied by 2^14 over
-// the largest row gradient's power of two, so that probabilities down to 2^-28 of it stay
-// normal numbers; the first workgroup keeps that factor.
-// Narrow rows: info gets what a row's powers are relative to, log2(e^lse / |g factor|),
+// so is what follows a row's end.
+// row_info gets what a row's powers are relative to, log2(e^lse / |g factor|),
 // +infinity where there is no target (powers of 0), its target, -1 for none, with a bit
 // set where g is negative, and g times the factor.
 template <int ST>
 __global__ __launch_bounds__(kBlock) void loss_prepare(LossArgs a) {
   constexpr int E = 16 / StorageTraits<ST>::bytes;
-  int e = 0;
-  if constexpr (ST == kF16) {
-    if (blockIdx.x == 0 || a.row_info) {  // every workgroup looks for itself
-      __shared__ float part[kWavesPerBlock];
-      float top = 0.0f;
-      for (int64_t n = threadIdx.x; n < a.rows; n += kBlock)
-        if (target_of(a, n) >= 0) top = fmaxf(top, fabsf(a.grad[n]));
-      for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-      if (lane_id() == 0) part[threadIdx.x >> 6] = top;
-      __syncthreads();
-      for (int w = 0; w < kWavesPerBlock; ++w) top = fmaxf(top, part[w]);
-      if (top > 0.0f && top <= 3.0e38f) {
-        frexpf(top, &e);
-        e = 15 - e;  // top 2^e lies in [2^14, 2^15)
-        e = e > 120 ? 120 : e;
-      }
+  const int32_t e = ST == kF16 ? static_cast<int32_t>(a.factor[2]) : 0;
+  if (ST != kF16 && blockIdx.x == 0 && threadIdx.x == 0) {
+    a.factor[0] = 1.0f;
+    a.factor[1] = a.scale;
+  }
+  const int64_t padded = (a.rows + 63) / 64 * 64;
+  for (int64_t n = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; n < padded;
+       n += static_cast<int64_t>(gridDim.x) * kBlock) {
+    const int64_t target = n < a.rows ? target_of(a, n) : -1;
+    float base = __builtin_inff(), scaled = 0.0f;
+    int32_t word = -1;
+    if (target >= 0) {
+      const float g = a.grad[n];
+      // in 64 bits: the difference is what powers of two are taken of
+      base = static_cast<float>(static_cast<double>(a.lse_in[n]) * 1.44269504088896340736 -
+                                static_cast<double>(log2f(fabsf(g))) - e);
+      word = static_cast<int32_t>(target) | (g < 0.0f ? kNegative : 0);
+      scaled = ldexpf(g, e);
     }
+    uint32_t* info = a.row_info + n / 64 * kInfoBlock + n % 64;
+    info[0] = __float_as_uint(base);
+    info[64] = static_cast<uint32_t>(word);
+    info[128] = __float_as_uint(scaled);
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    a.factor[0] = ldexpf(1.0f, e);
-    a.factor[1] = ldexpf(a.scale, -e);
-  }
-  if (a.row_info) {
-    const int64_t padded = (a.rows + 63) / 64 * 64;
-    for (int64_t n = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; n < padded;
-         n += static_cast<int64_t>(gridDim.x) * kBlock) {
-      const int64_t target = n < a.rows ? target_of(a, n) : -1;
-      float base = __builtin_inff(), scaled = 0.0f;
-      int32_t word = -1;
-      if (target >= 0) {
-        const float g = a.grad[n];
-        // in 64 bits: the difference is what powers of two are taken of
-        base = static_cast<float>(static_cast<double>(a.lse_in[n]) * 1.44269504088896340736 -
-                                  static_cast<double>(log2f(fabsf(g))) - e);
-        word = static_cast<int32_t>(target) | (g < 0.0f ? kNegative : 0);
-        scaled = ldexpf(g, e);
-      }
-      uint32_t* info = a.row_info + n / 64 * kInfoBlock + n % 64;
-      info[0] = __float_as_uint(base);
-      info[64] = static_cast<uint32_t>(word);
-      info[128] = __float_as_uint(scaled);
-    }
-  }
-  if (!a.x_rows) return;
   const int64_t chunks = a.x_width / E, all = a.rows * chunks;
   for (int64_t q = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; q < all;
        q += static_cast<int64_t>(gridDim.x) * kBlock) {
@@ -241,33 +255,42 @@ __global__ __launch_bounds__(S::threads) void loss_dlogits(LossArgs a, int64_t v
   band_order(xcd_contiguous_block(blockIdx.x, gridDim.x), na, nb, &ta, &tb);
   const int64_t a0 = ta * S::TA, b0 = tb * S::TB, left = piece - a0;
   f32x16 acc[S::WA][S::WB];
-  const void* x = a.x_rows ? a.x_rows : a.x;
-  tile_logits<ST, S, LAYOUT>(a, v0 + a0, left, x, a.x_rows ? a.x_width : a.x_stride, b0, wa, wb, wave,
-                             lane, lds, acc);
-  const float factor = a.factor[0];
+  tile_logits<ST, S, LAYOUT>(a, v0 + a0, left, a.x_rows, a.x_width, b0, wa, wb, wave, lane, lds, acc);
 #pragma unroll
   for (int j = 0; j < S::WB; ++j) {
     const int64_t n = b0 + wb + 32 * j + (lane & 31);
     const bool row = n < a.rows;
-    const int64_t target = row ? target_of(a, n) : -1;
-    const float g = target >= 0 ? a.grad[n] * factor : 0.0f;
-    const float lse2 = target >= 0 ? a.lse_in[n] * 1.44269504088896340736f : 0.0f;
-    const int64_t at = target - v0 - a0 - wa;
-    const bool near = __any(target >= 0 && at >= 0 && at < 32 * S::WA);
+    const RowInfo info = row ? row_info(a, n) : RowInfo{__builtin_inff(), -1, 0.0f};
+    const bool negative = info.target >= 0 && (info.target & kNegative);
+    const int64_t at = (info.target & ~kNegative) - v0 - a0 - wa;
+    const bool near = __any(info.target >= 0 && at >= 0 && at < 32 * S::WA);
+    const bool turned = __any(negative);
+    // 2-byte values: powers times |g| at once.  fp32 would tell that the exponent's rounding
+    // grows with log2 |g|.
+    const float g = fabsf(info.grad);
+    const float base = ST == kF32 ? (info.target >= 0 ? a.lse_in[n] * 1.44269504088896340736f : __builtin_inff())
+                                  : info.base;
     char* p = static_cast<char*>(a.dlogits) +
               (n * a.backward.width + a0 + wa) * StorageTraits<ST>::bytes;
 #pragma unroll
     for (int i = 0; i < S::WA; ++i) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        acc[i][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], a.exponent, -lse2));
+      for (int e = 0; e < 16; ++e) {
+        acc[i][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], a.exponent, -base));
+      }
       if (near) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (target >= 0 && at == place_of(i, e, lane)) acc[i][j][e] -= 1.0f;
+          if (info.target >= 0 && at == place_of(i, e, lane)) acc[i][j][e] -= ST == kF32 ? 1.0f : g;
       }
+      if constexpr (ST == kF32) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = target >= 0 ? acc[i][j][e] * g : 0.0f;
+        for (int e = 0; e < 16; ++e) acc[i][j][e] *= g;
+      }
+      if (turned) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = negative ? -acc[i][j][e] : acc[i][j][e];
+      }
       if (left < S::TA) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)

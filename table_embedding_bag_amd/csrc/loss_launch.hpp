@@ -121,7 +121,12 @@ hipError_t launch_loss_product(const LossArgs& a, int64_t v0, int64_t piece, con
 template <int ST>
 hipError_t launch_loss_backward(const LossArgs& a, hipStream_t s) {
   constexpr int E = 16 / StorageTraits<ST>::bytes;
-  const int64_t chunks = a.x_rows ? a.rows * (a.x_width / E) : 1;
+  if constexpr (ST == kF16) {
+    hipLaunchKernelGGL(loss_factor, dim3(1), dim3(1024), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int64_t chunks = std::max<int64_t>(1, a.rows * (a.x_width / E));
   hipLaunchKernelGGL((loss_prepare<ST>),
                      dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(chunks, kBlock), 4096))),
                      dim3(kBlock), 0, s, a);

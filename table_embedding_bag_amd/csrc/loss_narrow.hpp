@@ -365,10 +365,10 @@ __global__ __launch_bounds__(kBlock, 1) void loss_narrow_gradient(LossArgs a, in
     grad[b] = 0.0f;
     target[b] = -1;
     if (!DTABLE && n < a.rows) {
-      const uint32_t* info = a.row_info + n / 64 * kInfoBlock + n % 64;
-      base[b] = __uint_as_float(info[0]);
-      target[b] = static_cast<int32_t>(info[64]);
-      grad[b] = fabsf(__uint_as_float(info[128]));
+      const RowInfo info = row_info(a, n);
+      base[b] = info.base;
+      target[b] = info.target;
+      grad[b] = fabsf(info.grad);
     }
   }
   f32x16 acc[2][2 * S::SL], z[2];

@@ -54,18 +54,17 @@ void carve_forward(LossArgs* a, Carver* c) {
 void carve_backward(LossArgs* a, int32_t dtype, bool dx, bool dtable, Carver* c) {
   const LossBackwardPlan& p = a->backward;
   const int64_t bytes = dtype_bytes(dtype);
-  a->factor = static_cast<float*>(c->take(8));
+  a->factor = static_cast<float*>(c->take(12));
   a->x_width = padded_width(a->K, bytes);
+  a->x_rows = c->take(a->rows * a->x_width * bytes);
+  a->row_info = static_cast<uint32_t*>(c->take(ceil_div(a->rows, 64) * kInfoBlock * 4));
   if (p.narrow) {
-    a->x_rows = c->take(a->rows * a->x_width * bytes);
-    a->row_info = static_cast<uint32_t*>(c->take(ceil_div(a->rows, 64) * kInfoBlock * 4));
     if (dx && p.nx.splits > 1)
       a->dx_parts = static_cast<float*>(c->take(p.nx.splits * a->rows * a->K * 4));
     if (dtable && p.nw.splits > 1)
       a->dw_parts = static_cast<float*>(c->take(p.nw.splits * a->vocab * a->K * 4));
     return;
   }
-  a->x_rows = dtable ? c->take(a->rows * a->x_width * bytes) : nullptr;
   a->dlogits = c->take(a->rows * p.width * bytes);
   a->dx_parts = dx ? static_cast<float*>(c->take(p.x.splits * a->rows * a->K * 4)) : nullptr;
   a->dw_parts =
@@ -183,7 +182,7 @@ tbe_status tbe_softmax_loss_backward(const void* x, int64_t x_stride, const void
     a.backward = plan_loss_backward(rows, vocab, dim, takes_narrow(a, dtype), dtype);
     carve_backward(&a, dtype, dx, dtable, &c);
   } else {
-    a.factor = static_cast<float*>(c.take(8));
+    a.factor = static_cast<float*>(c.take(12));
   }
   if (!workspace || !aligned_to(workspace, 256)) return TBE_ERR_INVALID_ARGUMENT;
   if (workspace_bytes < c.used) return TBE_ERR_WORKSPACE_TOO_SMALL;

@@ -32,13 +32,14 @@ struct LossArgs {
   LossBackwardPlan backward;
   const float* lse_in;
   const float* grad;      // [rows]
-  void* x_rows;           // [rows][x_width]: x, zeros where a row has no target; or null
+  void* x_rows;           // [rows][x_width]: x, zeros where a row has no target
   int64_t x_width;
   void* dlogits;          // [rows][backward.width]: of one piece
   float* dx_parts;        // [splits][rows][K]; narrow rows: null with one split
   float* dw_parts;        // [splits][piece or vocab][K], or null with one split
-  uint32_t* row_info;     // narrow rows: of every 64 rows their bases, targets and gradients
-  float* factor;          // {what the logits' gradients are multiplied by, what undoes it times scale}
+  uint32_t* row_info;     // of every 64 rows their bases, targets and gradients
+  float* factor;          // what the logits' gradients are multiplied by, what undoes it times
+                          // the scale; fp16: its exponent
   void* dx;               // or null
   void* dtable;           // or null
 };
