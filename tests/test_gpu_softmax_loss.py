@@ -9,6 +9,21 @@ pytestmark = pytest.mark.gpu
 DTYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
 
 
+# Sizes whose tests compare every output with 64 bits; tests/test_loss_plan.py asserts that they reach
+# every kernel.
+SMALL = [(n, v, d) for d in (1, 33, 64, 100, 130, 256)
+         for n, v in ((1, 1), (1, 300), (5, 64), (33, 129), (64, 1000), (130, 257), (300, 2500))]
+NARROW = [(n, v, d) for d in (8, 16, 40, 64, 72, 104, 120, 128)
+          for n, v in ((1, 127), (63, 128), (64, 129), (65, 63), (256, 64), (257, 65), (600, 1999))] + [
+              (8, 70000, 16), (66000, 300, 16)]
+LARGER = [(600, 5000, 128), (40, 30000, 72), (2049, 1030, 520), (5000, 65, 40), (700, 9000, 264), (3000, 4001, 131),
+          (3000, 4001, 130), (3000, 4001, 132), (20, 9000, 301), (20, 9000, 302), (20, 9000, 304),
+          (3000, 6000, 301), (3000, 6000, 302), (3000, 6000, 304)]
+LARGE = [(11000, 12000, 520), (11000, 12000, 521), (11000, 12000, 522)]
+SIZES = [(*s, t) for s in SMALL + LARGER for t in DTYPES] + [(*s, t) for s in NARROW + LARGE for t in ("fp16", "bf16")] + [
+    (70000, 5000, 16, "bf16"), (70000, 5000, 17, "bf16")]
+
+
 class Problem:
     def __init__(self, N, V, D, dtype, seed=0, wide=0, scale=1.0, index=torch.int64, left_out=0.1, spread=2.0):
         g = torch.Generator().manual_seed(seed)
@@ -35,21 +50,37 @@ class Problem:
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("D", [1, 33, 64, 100, 130, 256])
-@pytest.mark.parametrize("N,V", [(1, 1), (1, 300), (5, 64), (33, 129), (64, 1000), (130, 257), (300, 2500)])
+@pytest.mark.parametrize("N,V,D", SMALL)
 def test_forward_and_backward(N, V, D, dtype):
     Problem(N, V, D, DTYPES[dtype], seed=N + V + D).check()
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("N,V,D", [(600, 5000, 128), (40, 30000, 72), (2049, 1030, 520), (5000, 65, 40), (700, 9000, 264)])
+@pytest.mark.parametrize("N,V,D", LARGER)
 def test_larger(N, V, D, dtype):
     Problem(N, V, D, DTYPES[dtype], seed=1).check()
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
-@pytest.mark.parametrize("D", [8, 16, 40, 64, 72, 104, 120, 128])
-@pytest.mark.parametrize("N,V", [(1, 127), (63, 128), (64, 129), (65, 63), (256, 64), (257, 65), (600, 1999)])
+@pytest.mark.parametrize("N,V,D", LARGE)
+def test_large(N, V, D, dtype):
+    Problem(N, V, D, DTYPES[dtype], seed=1).check()
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128, 200])
+def test_logits_far_below_and_above_zero(D, dtype):
+    """Tables that end inside a tile: a row past the end would have the logit 0, which is e^200 times
+    the largest here (or nothing beside the others)."""
+    for sign in (-1, 1):
+        p = Problem(100, 321, D, DTYPES[dtype], seed=6)
+        p.x[:] = 0.05 * p.x + 1
+        p.table[:] = 0.1 * p.table + sign * 200.0 / D
+        p.check()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("N,V,D", NARROW)
 def test_narrow_rows(N, V, D, dtype):
     """Rows of whole 16-byte chunks, which stay in registers."""
     Problem(N, V, D, DTYPES[dtype], seed=N + V + D).check()
@@ -151,9 +182,10 @@ def test_gradients_of_very_different_rows():
     p.check()
 
 
-def test_many_pieces():
-    """More rows than one piece of the logits' gradients has room for, the last piece short."""
-    N, V, D = 70000, 5000, 16
+@pytest.mark.parametrize("D", [16, 17])
+def test_many_rows(D):
+    """More rows than one piece of the logits' gradients has room for, the last piece short (17)."""
+    N, V = 70000, 5000
     p = Problem(N, V, D, torch.bfloat16, seed=9)
     got = p.run()
     z = p.x.float() @ p.table.float().t()
