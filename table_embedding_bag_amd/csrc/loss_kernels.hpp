@@ -30,6 +30,27 @@ __device__ __forceinline__ int64_t target_of(const LossArgs& a, int64_t n) {
   return t >= 0 && t < a.vocab ? t : -1;
 }
 
+// What follows is done where the branch is taken alone: left to itself the compiler may do it
+// always and choose afterwards, and keeps what it needs in registers all the time.
+__device__ __forceinline__ void rarely() { asm volatile(""); }
+
+// A copy of v that the compiler takes for another value: nothing worked out of it is kept from
+// one turn of a loop for the next.
+__device__ __forceinline__ int afresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Which of the lane's 16 values of a block is row `at` (where real: in 0 .. 31), or -1.
+__device__ __forceinline__ int32_t element_of(int32_t at, bool real, int lane) {
+  if (!real || (at >> 2 & 1) != lane >> 5) return -1;
+  return (at >> 3) * 4 + (at & 3);
+}
+__device__ __forceinline__ void subtract_at(f32x16& z, int32_t element, float v) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) z[e] -= element == e ? v : 0.0f;
+}
+
 // Which of a wave's 16 WA logits of a row the lane's i-th fragment's e-th value is.
 __device__ __forceinline__ int place_of(int i, int e, int lane) {
   return 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
@@ -61,8 +82,8 @@ __device__ __forceinline__ float2 join_sums(float2 a, float2 b) {
   return make_float2(top, a.y * __builtin_amdgcn_exp2f(a.x - from) + b.y * __builtin_amdgcn_exp2f(b.x - from));
 }
 
-// Forward: the running largest exponent m and sum s of 2^(exponent - m) of each row over
-// the segment's tiles, lane by lane; joined over lanes and waves once at the end.
+// Forward: each row's sum of 2^(exponent - reference) over the segment's tiles, lane by lane;
+// joined over lanes and waves once at the end.
 template <int ST, typename S, int LAYOUT>
 __global__ __launch_bounds__(S::threads) void loss_forward(LossArgs a) {
   __shared__ __align__(1024) unsigned char lds[kLdsBytes<S, LAYOUT>];
@@ -74,55 +95,79 @@ __global__ __launch_bounds__(S::threads) void loss_forward(LossArgs a) {
   const int64_t b0 = tb * S::TB;
   const int64_t first = segment * a.forward.run;
   const int64_t last = first + a.forward.run < a.forward.tiles ? first + a.forward.run : a.forward.tiles;
-  float m[S::WB], sum[S::WB];
-  int64_t target[S::WB];
+  float from[S::WB], sum[S::WB];  // what a row's powers are relative to, their sum
+  bool unset[S::WB];              // no reference yet
+  int32_t target[S::WB];          // tables have at most 2^30 rows
 #pragma unroll
   for (int j = 0; j < S::WB; ++j) {
-    m[j] = kNegInf;
-    sum[j] = 0.0f;
+    from[j] = sum[j] = 0.0f;
+    unset[j] = true;
     const int64_t n = b0 + wb + 32 * j + (lane & 31);
-    target[j] = n < a.rows ? target_of(a, n) : -1;
+    target[j] = n < a.rows ? static_cast<int32_t>(target_of(a, n)) : -1;
   }
   for (int64_t t = first; t < last; ++t) {
     const int64_t a0 = t * S::TA, left = a.vocab - a0;
     f32x16 acc[S::WA][S::WB];
     if (t > first) __syncthreads();  // the tile before is read
-    tile_logits<ST, S, LAYOUT>(a, a0, left, a.x, a.x_stride, b0, wa, wb, wave, lane, lds, acc);
+    tile_logits<ST, S, LAYOUT>(a, a0, left, a.x, a.x_stride, b0, wa, wb, wave, afresh(lane), lds, acc);
+    const int place = afresh(lane);
     if (left < S::TA) {  // the last: nothing past the table's end
+      rarely();
 #pragma unroll
       for (int i = 0; i < S::WA; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (wa + place_of(i, e, lane) >= left)
+          if (wa + place_of(i, e, place) >= left)
 #pragma unroll
             for (int j = 0; j < S::WB; ++j) acc[i][j][e] = kNegInf;
     }
 #pragma unroll
     for (int j = 0; j < S::WB; ++j) {
-      const int64_t at = target[j] - a0 - wa;
-      if (__any(target[j] >= 0 && at >= 0 && at < 32 * S::WA)) {
+      const int32_t at = target[j] - static_cast<int32_t>(a0) - wa;  // none: below 0
+      const bool near = static_cast<uint32_t>(at) < 32u * S::WA;
+      if (__any(near)) {
+        rarely();
+#pragma unroll
+        for (int i = 0; i < S::WA; ++i) {
+          const int32_t hit = element_of(at - 32 * i, near && at >> 5 == i, place);
+          float logit = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) logit = hit == e ? acc[i][j][e] : logit;
+          if (hit >= 0) a.target_logit[b0 + wb + 32 * j + (place & 31)] = logit;
+        }
+      }
+      // The reference is the largest power of the row's first tile (or of the last one whose
+      // powers grew past 2^80 of it): no maximum is looked for otherwise, as fp32 holds sums
+      // of 2^20 such powers, and what lies far below the reference does not count.
+      const auto powers = [&](float reference) {
+        float part[4] = {};
 #pragma unroll
         for (int i = 0; i < S::WA; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (target[j] >= 0 && at == place_of(i, e, lane))
-              a.target_logit[b0 + wb + 32 * j + (lane & 31)] = acc[i][j][e];
+            part[e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], a.exponent, -reference));
+        return (part[0] + part[1]) + (part[2] + part[3]);
+      };
+      float now = powers(from[j]);
+      const bool again = unset[j] || !(now <= 0x1p80f);  // each lane for itself
+      if (__any(again)) {
+        rarely();
+        float top = kNegInf;
+#pragma unroll
+        for (int i = 0; i < S::WA; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
+        const float next = fmaxf(unset[j] ? kNegInf : from[j], top * a.exponent);
+        const bool still = next == kNegInf;
+        const float reference = still ? 0.0f : next, other = powers(reference);
+        if (again) {
+          now = other;
+          sum[j] = unset[j] ? sum[j] : sum[j] * __builtin_amdgcn_exp2f(from[j] - reference);
+          from[j] = reference;
+          unset[j] = still;
+        }
       }
-      float top = kNegInf;
-#pragma unroll
-      for (int i = 0; i < S::WA; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
-      const float next = fmaxf(m[j], top * a.exponent);
-      const float from = next == kNegInf ? 0.0f : next;
-      float part[4] = {};
-#pragma unroll
-      for (int i = 0; i < S::WA; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          part[e & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], a.exponent, -from));
-      sum[j] = sum[j] * __builtin_amdgcn_exp2f(m[j] - from) + ((part[0] + part[1]) + (part[2] + part[3]));
-      m[j] = next;
+      sum[j] += now;
     }
   }
   // the two halves of a wave, then the waves that have the same rows
@@ -130,8 +175,9 @@ __global__ __launch_bounds__(S::threads) void loss_forward(LossArgs a) {
   float2* joined = reinterpret_cast<float2*>(lds);
 #pragma unroll
   for (int j = 0; j < S::WB; ++j) {
-    const float2 other = make_float2(__shfl_xor(m[j], 32), __shfl_xor(sum[j], 32));
-    const float2 both = join_sums(make_float2(m[j], sum[j]), other);
+    const float2 mine = make_float2(unset[j] ? kNegInf : from[j], sum[j]);
+    const float2 other = make_float2(__shfl_xor(mine.x, 32), __shfl_xor(mine.y, 32));
+    const float2 both = join_sums(mine, other);
     if (lane < 32) joined[(wave % S::NA) * S::TB + wb + 32 * j + lane] = both;
   }
   __syncthreads();
@@ -262,9 +308,9 @@ __global__ __launch_bounds__(S::threads) void loss_dlogits(LossArgs a, int64_t v
     const bool row = n < a.rows;
     const RowInfo info = row ? row_info(a, n) : RowInfo{__builtin_inff(), -1, 0.0f};
     const bool negative = info.target >= 0 && (info.target & kNegative);
-    const int64_t at = (info.target & ~kNegative) - v0 - a0 - wa;
-    const bool near = __any(info.target >= 0 && at >= 0 && at < 32 * S::WA);
-    const bool turned = __any(negative);
+    const int32_t at = (info.target & ~kNegative) - static_cast<int32_t>(v0 + a0) - wa;
+    const bool near = info.target >= 0 && static_cast<uint32_t>(at) < 32u * S::WA;
+    const bool any_near = __any(near), turned = __any(negative);
     // 2-byte values: powers times |g| at once.  fp32 would tell that the exponent's rounding
     // grows with log2 |g|.
     const float g = fabsf(info.grad);
@@ -275,23 +321,23 @@ __global__ __launch_bounds__(S::threads) void loss_dlogits(LossArgs a, int64_t v
 #pragma unroll
     for (int i = 0; i < S::WA; ++i) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < 16; ++e)
         acc[i][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], a.exponent, -base));
-      }
-      if (near) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (info.target >= 0 && at == place_of(i, e, lane)) acc[i][j][e] -= ST == kF32 ? 1.0f : g;
+      if (any_near) {
+        rarely();
+        subtract_at(acc[i][j], element_of(at - 32 * i, near && at >> 5 == i, lane), ST == kF32 ? 1.0f : g);
       }
       if constexpr (ST == kF32) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] *= g;
       }
       if (turned) {
+        rarely();
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = negative ? -acc[i][j][e] : acc[i][j][e];
       }
       if (left < S::TA) {
+        rarely();
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (wa + place_of(i, e, lane) >= left) acc[i][j][e] = 0.0f;

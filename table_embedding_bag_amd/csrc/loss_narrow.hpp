@@ -151,24 +151,10 @@ __device__ __forceinline__ u32x4 tile_columns(const unsigned char* tile, int blo
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 constexpr int kReadAhead = 6;  // matrix instructions between a read and its use
 
-// What follows is done where the branch is taken alone: the compiler would rather do it
-// always and choose afterwards (the forward pass took every power twice).
-__device__ __forceinline__ void rarely() { asm volatile(""); }
-
 // v is computed here: the compiler would move that to where v is used, behind the next
 // branch and out of the matrix instructions' shadow.
 template <typename T>
 __device__ __forceinline__ void settled(T& v) { asm volatile("" : "+v"(v)); }
-
-// Which of the lane's 16 values of a block is row `at` (where real: in 0 .. 31), or -1.
-__device__ __forceinline__ int32_t element_of(int32_t at, bool real, int lane) {
-  if (!real || (at >> 2 & 1) != lane >> 5) return -1;
-  return (at >> 3) * 4 + (at & 3);
-}
-__device__ __forceinline__ void subtract_at(f32x16& z, int32_t element, float v) {
-#pragma unroll
-  for (int e = 0; e < 16; ++e) z[e] -= element == e ? v : 0.0f;
-}
 
 // f(t, its buffer, the buffer of the tile before) for the tiles first .. last of a ring of
 // R, each when it is there; the LAG tiles before t are still being read.
@@ -257,7 +243,7 @@ __global__ __launch_bounds__(kBlock, 2) void loss_narrow_forward(LossArgs a) {
         for (int e = 0; e < 16; ++e) add_power(b, e);
         if (change) {
           now[b] = block_sum(b);
-          sum[b] = unset[b] ? 0.0f : sum[b] * __builtin_amdgcn_exp2f(keep - from[b]);
+          sum[b] = unset[b] ? sum[b] : sum[b] * __builtin_amdgcn_exp2f(keep - from[b]);
           unset[b] = still;
         }
       }

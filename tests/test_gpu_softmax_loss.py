@@ -144,6 +144,17 @@ def test_rows_without_a_target_reach_nothing(dtype):
         assert torch.equal(got[name], clean[name]), name
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("N,V,D", [(300, 1300, 40), (300, 1300, 130), (11000, 12000, 520)])
+def test_rows_of_nan_in_the_table_reach_every_row(N, V, D, dtype):
+    """Whole blocks of the table that hold nothing else, before and behind others."""
+    for first in (0, V // 2):
+        p = Problem(N, V, D, DTYPES[dtype])
+        p.table[first:first + 512] = float("nan")
+        _, lse = tbe.softmax_loss(p.x, p.table, p.targets)
+        assert bool(lse.isnan().all())
+
+
 def test_no_targets_at_all():
     p = Problem(30, 200, 64, torch.float16, seed=6, left_out=2.0)
     got = p.run()
