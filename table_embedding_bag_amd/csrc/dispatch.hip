@@ -6,6 +6,12 @@
 //   combine_backward  drows[places[a]] = w[a] dy[n],  dw[a] = <dy[n], rows[places[a]]>
 // and dispatch's gradient is a combine without weights.  An id outside [0, experts) goes
 // nowhere: place -1.
+//
+// Memory bounds all but the plan, which is a chain of counts, barriers and scattered 4-byte
+// stores.  131072 assignments of 32768 rows to 128 experts, 1024 columns, bf16: plan 17 us (27
+// with its assignments and counts one at a time), dispatch 53 us (6.0 TB/s, as x's lines are read
+// once), combine 90 us (3.6 TB/s: what gathered rows are read at, with a thread for every chunk
+// of the whole matrix too), its gradients 105 us (121 with one of a row's places at a time).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -154,98 +160,143 @@ struct MoveArgs {
   void* out;
   float* dweights;       // or null
   int64_t x_stride, r_stride, g_stride, out_stride;
-  int64_t rows, cols, chunks;  // chunks of 16 bytes in a row
-  int32_t k;
+  int64_t rows, cols;
+  int32_t k, shift;  // 2^shift lanes have a row
 };
 
+// f(WHOLE: whether the thread's chunk at column c ends within the row, known to the compiler)
+template <int ST, typename F>
+__device__ __forceinline__ void with_end(int64_t c, int64_t cols, F f) {
+  if (c + 16 / StorageTraits<ST>::bytes <= cols) f(std::true_type{});
+  else f(std::false_type{});
+}
+
+// A chunk at column c of the row at element `at`.  Loads have no branches, so that several are
+// on their way together: past a row's end the last value is read again, and zeros come of it.
 template <int ST>
 struct Chunk {
   static constexpr int E = 16 / StorageTraits<ST>::bytes;
+  using T = typename Stored<ST>::type;
   StoredVec<ST, E> v = {};
-  // The chunk at column c of the row at element `at`; zeros past its end.
+  template <bool WHOLE>
   __device__ __forceinline__ void load(const void* base, int64_t at, int64_t c, int64_t cols) {
-    if (c + E <= cols) {
+    if constexpr (WHOLE) {
       v = load_vec<ST, E>(base, at + c);
     } else {
+      T one[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (c + i < cols) v[i] = static_cast<const typename Stored<ST>::type*>(base)[at + c + i];
+      for (int i = 0; i < E; ++i) one[i] = static_cast<const T*>(base)[at + (c + i < cols ? c + i : cols - 1)];
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = c + i < cols ? one[i] : static_cast<T>(0.0f);
     }
   }
+  template <bool WHOLE>
   __device__ __forceinline__ void store(void* base, int64_t at, int64_t c, int64_t cols) const {
-    if (c + E <= cols) {
+    if constexpr (WHOLE) {
       store_vec<ST, E>(base, at + c, v);
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (c + i < cols) static_cast<typename Stored<ST>::type*>(base)[at + c + i] = v[i];
+        if (c + i < cols) static_cast<T*>(base)[at + c + i] = v[i];
     }
   }
 };
 
-// The place of assignment i, or -1: a wrong one is none.
-__device__ __forceinline__ int64_t place_of(const MoveArgs& a, int64_t i) {
-  const int32_t p = a.places[i];
-  return p >= 0 && p < a.rows * a.k ? p : -1;
+// f(j0, how many: up to 4, known to the compiler) for a row's k assignments, four at a time.
+template <typename F>
+__device__ __forceinline__ void by_fours(int k, F f) {
+  int j0 = 0;
+  for (; j0 + 4 <= k; j0 += 4) f(j0, std::integral_constant<int, 4>{});
+  if (k - j0 == 3) f(j0, std::integral_constant<int, 3>{});
+  else if (k - j0 == 2) f(j0, std::integral_constant<int, 2>{});
+  else if (k - j0 == 1) f(j0, std::integral_constant<int, 1>{});
 }
 
-// A thread reads a chunk of a row once and writes it to the row's places.
+// The places of C assignments from i on, -1 for none: a wrong one is none.
+template <int C>
+__device__ __forceinline__ void places_of(const MoveArgs& a, int64_t i, int32_t (&p)[C]) {
+#pragma unroll
+  for (int j = 0; j < C; ++j) p[j] = a.places[i + j];
+#pragma unroll
+  for (int j = 0; j < C; ++j) p[j] = p[j] >= 0 && p[j] < a.rows * a.k ? p[j] : -1;
+}
+
+// f(n, c) for the chunks of all rows: 2^shift lanes have a row.
+template <int E, typename F>
+__device__ __forceinline__ void over_chunks(const MoveArgs& a, F f) {
+  const int64_t step = (static_cast<int64_t>(gridDim.x) * kBlock) >> a.shift;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x) >> a.shift;
+  const int lane = static_cast<int>(threadIdx.x) & ((1 << a.shift) - 1);
+  for (int64_t n = first; n < a.rows; n += step)
+    for (int64_t c = lane * E; c < a.cols; c += E << a.shift) f(n, c);
+}
+
+// A thread reads a chunk of a row once and writes it to the row's places (read again for each
+// place the rows would be most of the traffic).
 template <int ST>
 __global__ __launch_bounds__(kBlock) void dispatch_rows(MoveArgs a) {
-  constexpr int E = Chunk<ST>::E;
-  const int64_t all = a.rows * a.chunks, step = static_cast<int64_t>(gridDim.x) * kBlock;
   const int64_t total = *a.total;
-  for (int64_t q = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; q < all; q += step) {
-    const int64_t n = q / a.chunks, c = (q - n * a.chunks) * E;
-    Chunk<ST> v;
-    v.load(a.x, n * a.x_stride, c, a.cols);
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t p = place_of(a, n * a.k + j);
-      if (p >= 0) v.store(a.out, p * a.out_stride, c, a.cols);
-    }
-    // the places that nobody has
-    for (int j = 0; j < a.k; ++j)
-      if (n * a.k + j >= total) Chunk<ST>().store(a.out, (n * a.k + j) * a.out_stride, c, a.cols);
-  }
+  over_chunks<Chunk<ST>::E>(a, [&](int64_t n, int64_t c) {
+    with_end<ST>(c, a.cols, [&](auto whole_) {
+      constexpr bool whole = whole_;
+      Chunk<ST> v;
+      v.template load<whole>(a.x, n * a.x_stride, c, a.cols);
+      by_fours(a.k, [&](int j0, auto some_) {
+        constexpr int some = some_;
+        int32_t p[some];
+        places_of(a, n * a.k + j0, p);
+#pragma unroll
+        for (int j = 0; j < some; ++j)
+          if (p[j] >= 0) v.template store<whole>(a.out, p[j] * a.out_stride, c, a.cols);
+      });
+      // the places that nobody has
+      for (int64_t i = n * a.k > total ? n * a.k : total; i < (n + 1) * a.k; ++i)
+        Chunk<ST>().template store<whole>(a.out, i * a.out_stride, c, a.cols);
+    });
+  });
 }
 
+// A thread has a chunk of a row: four of the experts' rows at a time, on their way together; one
+// that is not there is read at place 0 and left out.
 template <int ST>
 __global__ __launch_bounds__(kBlock) void combine_rows(MoveArgs a) {
   constexpr int E = Chunk<ST>::E;
-  const int64_t all = a.rows * a.chunks, step = static_cast<int64_t>(gridDim.x) * kBlock;
-  for (int64_t q = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; q < all; q += step) {
-    const int64_t n = q / a.chunks, c = (q - n * a.chunks) * E;
-    float sum[E] = {};
-    if (a.residual) {
-      Chunk<ST> r;
-      r.load(a.residual, n * a.r_stride, c, a.cols);
+  over_chunks<E>(a, [&](int64_t n, int64_t c) {
+    with_end<ST>(c, a.cols, [&](auto whole_) {
+      constexpr bool whole = whole_;
+      float sum[E] = {};
+      if (a.residual) {
+        Chunk<ST> r;
+        r.template load<whole>(a.residual, n * a.r_stride, c, a.cols);
 #pragma unroll
-      for (int i = 0; i < E; ++i) sum[i] = static_cast<float>(r.v[i]);
-    }
-    // Four rows at a time, on their way together: one that is not there is read at place 0 and
-    // left out.
-    for (int j0 = 0; j0 < a.k; j0 += 4) {
-      int64_t p[4];
-      float w[4];
-      Chunk<ST> v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        p[j] = j0 + j < a.k ? place_of(a, n * a.k + j0 + j) : -1;
-        w[j] = a.weights && j0 + j < a.k ? a.weights[n * a.k + j0 + j] : 1.0f;
+        for (int i = 0; i < E; ++i) sum[i] = static_cast<float>(r.v[i]);
       }
+      by_fours(a.k, [&](int j0, auto some_) {
+        constexpr int some = some_;
+        int32_t p[some];
+        float w[some];
+        Chunk<ST> v[some];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j0 + j < a.k) v[j].load(a.x, (p[j] < 0 ? 0 : p[j]) * a.x_stride, c, a.cols);
+        for (int j = 0; j < some; ++j) w[j] = 1.0f;
+        if (a.weights) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < some; ++j) w[j] = a.weights[n * a.k + j0 + j];
+        }
+        places_of(a, n * a.k + j0, p);
 #pragma unroll
-        for (int i = 0; i < E; ++i) sum[i] += p[j] < 0 ? 0.0f : w[j] * static_cast<float>(v[j].v[i]);
-    }
-    Chunk<ST> out;
+        for (int j = 0; j < some; ++j)
+          v[j].template load<whole>(a.x, (p[j] < 0 ? 0 : p[j]) * a.x_stride, c, a.cols);
 #pragma unroll
-    for (int i = 0; i < E; ++i) out.v[i] = static_cast<typename Stored<ST>::type>(sum[i]);
-    out.store(a.out, n * a.out_stride, c, a.cols);
-  }
+        for (int j = 0; j < some; ++j)
+#pragma unroll
+          for (int i = 0; i < E; ++i) sum[i] += p[j] < 0 ? 0.0f : w[j] * static_cast<float>(v[j].v[i]);
+      });
+      Chunk<ST> out;
+#pragma unroll
+      for (int i = 0; i < E; ++i) out.v[i] = static_cast<typename Stored<ST>::type>(sum[i]);
+      out.template store<whole>(a.out, n * a.out_stride, c, a.cols);
+    });
+  });
 }
 
 // A wave has a row: its gradient, weighted, to the row's places, and the products with the
@@ -253,36 +304,55 @@ __global__ __launch_bounds__(kBlock) void combine_rows(MoveArgs a) {
 template <int ST>
 __global__ __launch_bounds__(kBlock) void combine_gradients(MoveArgs a) {
   constexpr int E = Chunk<ST>::E;
-  const int lane = lane_id();
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t total = *a.total;
-  for (int64_t n = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + (threadIdx.x >> 6); n < a.rows;
+  for (int64_t n = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + wave; n < a.rows;
        n += static_cast<int64_t>(gridDim.x) * kWavesPerBlock) {
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t i = n * a.k + j, p = place_of(a, i);
-      const bool hole = i >= total;   // a place that nobody has
-      float dot = 0.0f;
-      const float w = p >= 0 ? a.weights[i] : 0.0f;
-      for (int64_t c = lane * E; c < a.cols; c += 64 * E) {
-        if (p >= 0) {
-          Chunk<ST> g, y, out;
-          g.load(a.grad, n * a.g_stride, c, a.cols);
-          if (a.dweights) {
-            y.load(a.x, p * a.x_stride, c, a.cols);
+    by_fours(a.k, [&](int j0, auto some_) {
+      constexpr int some = some_;
+      const int64_t i0 = n * a.k + j0;
+      int32_t p[some];
+      float w[some], dot[some] = {};
+      places_of(a, i0, p);
 #pragma unroll
-            for (int e = 0; e < E; ++e) dot += static_cast<float>(g.v[e]) * static_cast<float>(y.v[e]);
+      for (int j = 0; j < some; ++j) w[j] = a.weights[i0 + j];
+      for (int64_t c = lane * E; c < a.cols; c += 64 * E)
+        with_end<ST>(c, a.cols, [&](auto whole_) {
+          constexpr bool whole = whole_;
+          Chunk<ST> g, y[some], out;
+          g.template load<whole>(a.grad, n * a.g_stride, c, a.cols);
+          if (a.dweights) {
+#pragma unroll
+            for (int j = 0; j < some; ++j)
+              y[j].template load<whole>(a.x, (p[j] < 0 ? 0 : p[j]) * a.x_stride, c, a.cols);
           }
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            out.v[e] = static_cast<typename Stored<ST>::type>(w * static_cast<float>(g.v[e]));
-          out.store(a.out, p * a.out_stride, c, a.cols);
-        }
-        if (hole) Chunk<ST>().store(a.out, i * a.out_stride, c, a.cols);
-      }
+          for (int j = 0; j < some; ++j)
+            if (p[j] >= 0) {
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                out.v[e] = static_cast<typename Stored<ST>::type>(w[j] * static_cast<float>(g.v[e]));
+                dot[j] += static_cast<float>(g.v[e]) * static_cast<float>(y[j].v[e]);
+              }
+              out.template store<whole>(a.out, p[j] * a.out_stride, c, a.cols);
+            }
+        });
       if (a.dweights) {
-        for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
-        if (lane == 0) a.dweights[i] = dot;
+#pragma unroll
+        for (int d = 32; d; d >>= 1)
+#pragma unroll
+          for (int j = 0; j < some; ++j) dot[j] += __shfl_xor(dot[j], d);
+#pragma unroll
+        for (int j = 0; j < some; ++j)
+          if (lane == j) a.dweights[i0 + j] = dot[j];
       }
-    }
+    });
+    // the places that nobody has
+    for (int64_t i = n * a.k > total ? n * a.k : total; i < (n + 1) * a.k; ++i)
+      for (int64_t c = lane * E; c < a.cols; c += 64 * E)
+        with_end<ST>(c, a.cols, [&](auto whole_) {
+          Chunk<ST>().template store<whole_>(a.out, i * a.out_stride, c, a.cols);
+        });
   }
 }
 
@@ -317,7 +387,7 @@ MoveArgs move_args(const int32_t* places, int64_t rows, int64_t k, int64_t cols,
   a.k = static_cast<int32_t>(k);
   a.cols = cols;
   const int64_t e = 16 / dtype_bytes(dtype);
-  a.chunks = (cols + e - 1) / e;
+  while (a.shift < 6 && e << a.shift < cols) ++a.shift;
   return a;
 }
 
@@ -384,7 +454,7 @@ tbe_status tbe_dispatch(const void* x, int64_t x_stride, const int32_t* places, 
   a.out = out;
   a.out_stride = out_stride;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid = grid_of(rows * a.chunks);
+  const dim3 grid = grid_of(rows << a.shift);
   if (dtype == TBE_F32) hipLaunchKernelGGL(dispatch_rows<kF32>, grid, dim3(kBlock), 0, s, a);
   else if (dtype == TBE_F16) hipLaunchKernelGGL(dispatch_rows<kF16>, grid, dim3(kBlock), 0, s, a);
   else hipLaunchKernelGGL(dispatch_rows<kBF16>, grid, dim3(kBlock), 0, s, a);
@@ -411,7 +481,7 @@ tbe_status tbe_combine(const void* y, int64_t y_stride, const int32_t* places, c
   a.out = out;
   a.out_stride = out_stride;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid = grid_of(rows * a.chunks);
+  const dim3 grid = grid_of(rows << a.shift);
   if (dtype == TBE_F32) hipLaunchKernelGGL(combine_rows<kF32>, grid, dim3(kBlock), 0, s, a);
   else if (dtype == TBE_F16) hipLaunchKernelGGL(combine_rows<kF16>, grid, dim3(kBlock), 0, s, a);
   else hipLaunchKernelGGL(combine_rows<kBF16>, grid, dim3(kBlock), 0, s, a);
