@@ -1,4 +1,9 @@
 // loss_kernels.hpp -- the softmax loss's kernels for rows of any width, type and alignment.
+//
+// A tile's product needs all the registers there are, so what follows it is written to keep
+// little across it: targets in 32 bits, rows' information read behind it, branches for what
+// is rare, and nothing worked out of the lane's number kept from tile to tile.  What did not fit
+// went to memory and back: 16384 rows, 131072 outputs of 512, fp16, forward 2.8 ms, 2.2 without.
 #pragma once
 
 #include "products.hpp"

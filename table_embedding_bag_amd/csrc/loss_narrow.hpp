@@ -11,6 +11,10 @@
 //   dx        Q = x, T = table:  dx[q] += sum_t d[q, t] table[t]
 //   dtable    Q = table, T = x:  dtable[q] += sum_t d[t, q] x[t]
 // so the logits' gradients never leave the registers; each pass computes the logits again.
+//
+// 2048 rows, 100000 outputs of 128, bf16: forward 66 us (0.79 PFLOP/s; powers of two take as long
+// as the product), dtable 148 us (two products, 0.71: 391 workgroups take two rounds of the 256
+// places, the second half empty), dx 115 us (0.91).  64 rows: forward 12 us (2.1 TB/s of the table).
 #pragma once
 
 #include "loss_kernels.hpp"

@@ -39,11 +39,9 @@ inline LossForwardPlan plan_loss_forward(int64_t rows, int64_t vocab, int64_t K,
     p.segments = ceil_div(p.tiles, p.run);
     return p;
   }
-  // Large tiles, one to a CU, have nothing to do beside their powers: they pay where rows
-  // are long (16384 x 131072 x 512: 2.84 ms, 2.90 with 128; 4096 x 20000 x 256: 187 us, 93
-  // with 128, 100 with 64).
+  // (16384 rows, 131072 outputs of 512, fp16: 2.20 ms with 256, 2.70 with 128; 3000 rows, 20001
+  // of 513: 103 us, 138.)
   p.tile = rows <= 32 ? 32 : row_tile(vocab, 1, rows, dtype);
-  if (p.tile == 256 && K < 512) p.tile = 128;
   const int64_t along_rows = ceil_div(rows, p.tile);
   p.tiles = ceil_div(vocab, p.tile == 32 ? 128 : p.tile);
   // workgroups for every place of the chip, twice over
@@ -61,8 +59,8 @@ struct LossProductPlan {
 inline LossProductPlan plan_loss_product(int64_t out_rows, int64_t K, int64_t depth, int32_t dtype) {
   const auto tiles = [&](int64_t t) { return ceil_div(out_rows, t) * ceil_div(K, t); };
   LossProductPlan p{};
-  // Few outputs over a short index take small tiles (700 rows over 3000 x 1000 fp16, both
-  // products: 55 us, 65 with 128; 4096 over 20000 x 256: 259, 241 with 128).
+  // Few outputs over a short index take small tiles (the backward pass of 700 rows, 3000
+  // outputs of 1000, fp16: 57 us, 67 with 128; of 4096 rows, 20000 of 256: 249, 225 with 128).
   p.tile = dtype != TBE_F32 && K > 128 && tiles(256) >= 128 ? 256
            : depth * tiles(128) < 512 * 384                 ? 64
                                                             : 128;

@@ -11,6 +11,11 @@
 // equal ones need nothing more; otherwise keys lose their last 4 bits to it, and
 // where two that follow each other lie closer than that and fp32 scores may be off, the
 // wave chooses again in 64 bits.
+//
+// Instructions bound it, not memory (32768 x 256 bf16, 8 of them in 4 of 8 groups by sigmoid +
+// bias: 17 MB, 4 us at a copy's rate): forward 43 us, of which about 20 are the rows that are
+// chosen again and their code's way into the instruction cache, backward 11.4 us.  A row has 16
+// lanes where that leaves a lane 16 experts at most, so that four rows share a wave's steps.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

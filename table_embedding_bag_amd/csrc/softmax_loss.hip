@@ -4,9 +4,15 @@
 // and its gradients, with d_nv = g_n (exp(z_nv - lse_n) - [v = target_n]),
 //   dx = scale d W,   dW = scale d^T x.
 // The logits z are never kept: the forward pass reduces each tile of them to a row's
-// running maximum and sum, the backward pass computes them again, one piece of the
-// vocabulary at a time, and holds that piece's d in the rows' type (the one rounding
-// beside the outputs') for the two products that read it.
+// sum of powers, the backward pass computes them again, one piece of the vocabulary at a
+// time, and holds that piece's d in the rows' type (the one rounding beside the outputs')
+// for the two products that read it.
+//
+// The matrix cores bound it: four products of 2 N V K operations, five for narrow rows
+// (loss_narrow.hpp), whose gradients each compute the logits.  16384 rows, 131072 outputs of 512,
+// fp16: forward 2.2 ms (1.0 PFLOP/s), backward 7.2 ms: 8 pieces of 0.40 ms for the logits'
+// gradients (0.68, with 512 MB to write), 0.26 for the table's (1.08), 0.29 for x's (0.95); pieces
+// of 32 to 256 MB, which the last cache could hold, were slower.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
