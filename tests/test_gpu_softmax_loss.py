@@ -114,6 +114,17 @@ def test_rows_of_wider_buffers(wide, dtype):
     Problem(150, 700, 96, DTYPES[dtype], seed=2, wide=wide).check()
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("N,V,D", [(300, 500, 64), (300, 500, 120), (70, 500, 130)])
+def test_rows_that_start_inside_others(N, V, D, dtype):
+    """x and the table one value into their buffers, each alone and both."""
+    for x_from, table_from in ((1, 0), (0, 1), (1, 1)):
+        p = Problem(N, V, D + 1, DTYPES[dtype], seed=17)
+        p.x = p.x[:, x_from:x_from + D] if x_from else p.x[:, :D].contiguous()
+        p.table = p.table[:, table_from:table_from + D] if table_from else p.table[:, :D].contiguous()
+        p.check()
+
+
 @pytest.mark.parametrize("scale", [0.05, 3.0])
 def test_scale_and_index_types(scale):
     Problem(70, 500, 64, torch.float32, seed=3, scale=scale, index=torch.int32).check()
