@@ -60,7 +60,7 @@ inline LossProductPlan plan_loss_product(int64_t out_rows, int64_t K, int64_t de
   const auto tiles = [&](int64_t t) { return ceil_div(out_rows, t) * ceil_div(K, t); };
   LossProductPlan p{};
   // Few outputs over a short index take small tiles (the backward pass of 700 rows, 3000
-  // outputs of 1000, fp16: 57 us, 67 with 128; of 4096 rows, 20000 of 256: 249, 225 with 128).
+  // outputs of 1000, fp16: 53 us, 67 with 128; of 4096 rows, 20000 of 256: 249, 225 with 128).
   p.tile = dtype != TBE_F32 && K > 128 && tiles(256) >= 128 ? 256
            : depth * tiles(128) < 512 * 384                 ? 64
                                                             : 128;
