@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "layers.hpp"
+#include "route_keys.hpp"
 
 using namespace tbe;
 
@@ -338,13 +339,9 @@ __device__ int choose_exactly(const RouteArgs& a, const float (&l)[V], int lane,
 
 // Keys as whole numbers in the same order, their last `bits` bits an expert's number
 // counted down; 0 for an expert that cannot be chosen.
-__device__ __forceinline__ uint32_t in_order(float f) {
-  const uint32_t u = __float_as_uint(f + 0.0f);  // no -0
-  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
-}
+__device__ __forceinline__ uint32_t in_order(float f) { return key_of_float(__float_as_uint(f + 0.0f)); }  // no -0
 __device__ __forceinline__ float value_of(uint32_t key, uint32_t bits) {
-  const uint32_t u = key & ~bits;
-  return __uint_as_float(u ^ (~static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u));
+  return __uint_as_float(float_of_key(key, bits));
 }
 struct MaxKey {
   __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
@@ -372,7 +369,8 @@ __device__ __forceinline__ int choose_experts(const RouteArgs& a, const float (&
     s[j] = e < a.experts ? (in_order(key[j]) & ~kBits) | (kBits - (NUMBER ? e : j)) : 0u;
   }
   const int first_lane = L == 64 ? 0 : lane_id() & 48;
-  // The lane whose head is the row's best, the lowest of several.
+  // The lane whose head is the row's best, the lowest of several.  There always is one: open
+  // groups and experts of theirs are as many as are taken, at least, and -infinity counts too.
   const auto best_lane = [&](bool is) {
     const uint64_t all = __ballot(is) >> first_lane;
     return __builtin_ctzll(L == 64 ? all | 1ull << 63 : (all & 0xFFFFu) | 0x8000u);  // always one of them
@@ -385,11 +383,11 @@ __device__ __forceinline__ int choose_experts(const RouteArgs& a, const float (&
     if (whole) sort_down<V>(s);
     if (whole) {
       float one = value_of(s[0], kBits), two = V > 1 ? value_of(s[V > 1 ? 1 : 0], kBits) : -__builtin_inff();
-      if (s[0] == 0u) one = kNegInf;
-      if (V > 1 && s[V > 1 ? 1 : 0] == 0u) two = kNegInf;
       best_two<L>(one, two, shift);
       score = a.top2 ? one + two : one;
-      size = over_row<L>(lane >> shift < a.groups ? fabsf(one) + (a.top2 ? fabsf(two) : 0.0f) : 0.0f, Max());
+      // (-infinity is off by nothing)
+      const auto size_of = [](float v) { return v > kNegInf ? fabsf(v) : 0.0f; };
+      size = over_row<L>(lane >> shift < a.groups ? size_of(one) + (a.top2 ? size_of(two) : 0.0f) : 0.0f, Max());
       // one lane for each group
       if (lane >> shift >= a.groups || lane & ((1 << shift) - 1)) score = kDead<float>;
     } else {

@@ -125,6 +125,56 @@ def test_biases_that_close_experts(E, groups, top):
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top,k", [(12, 3, 1, 3), (16, 8, 4, 8), (24, 3, 2, 12), (32, 4, 2, 9), (48, 3, 2, 4), (48, 3, 2, 16),
+                                            (64, 8, 4, 6), (64, 8, 4, 16), (250, 5, 2, 7), (256, 8, 4, 16), (512, 4, 2, 16),
+                                            (1024, 16, 3, 16)])
+def test_groups_without_an_open_expert(E, groups, top, k, scores, dtype):
+    """Rows with fewer open groups than are taken: the rest are the lowest ones, whatever a lane's
+    experts are of a group."""
+    t, per = DTYPES[dtype], E // groups
+    shut = -torch.inf
+    x = torch.full((6 + 3 * groups, E), shut, dtype=t, device="cuda")
+    some = logits_of(x.shape[0], E, t, seed=12)
+    x[1] = float("nan")
+    x[2, ::2] = float("nan")
+    x[3, 0], x[4, E - 1], x[5, E // 2] = some[3, 0], torch.inf, torch.finfo(t).min
+    for g in range(groups):
+        at = slice(g * per, (g + 1) * per)
+        row = 6 + 3 * g
+        x[row, at] = some[row, at]                       # one open group
+        x[row + 1, g * per + per // 2] = some[row + 1, 0]  # one open expert
+        x[row + 2] = some[row + 2]                       # all but one group open
+        x[row + 2, at] = shut
+    for renormalize in (True, False):
+        ids, w, d = check(x, k, scores=scores, groups=groups, top_groups=top, renormalize=renormalize)
+        assert bool(((ids >= 0) & (ids < E)).all()) and not w[:3].any() and not d[:3].any()
+    check(x, k, bias=bias_of(E), scores=scores, groups=groups, top_groups=top, group_score="top2")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top", [(16, 8, 3), (32, 4, 2), (64, 8, 4), (256, 8, 3), (256, 16, 5), (1024, 16, 3), (250, 5, 2)])
+def test_biases_that_close_parts_of_groups(E, groups, top, scores, dtype):
+    """A group's score is the sum of its best two open experts, wherever its closed ones lie."""
+    per = E // groups
+    x = logits_of(60, E, DTYPES[dtype], seed=13)
+    lane = max(1, min(16, E // 16))     # experts side by side in a lane
+    random = torch.rand(E, generator=torch.Generator().manual_seed(14)) < 0.8
+    for name in ("first", "last", "all but one", "all but two", "random"):
+        bias = bias_of(E)
+        for g in range(0, groups, 2):
+            at = torch.arange(g * per, (g + 1) * per)
+            shut = {"first": at[:lane], "last": at[-lane:], "all but one": at[at != g * per + g % per],
+                    "all but two": at[1:-1], "random": at[random[at]]}[name]
+            bias[shut] = -torch.inf
+        want = check(x, min(6, per * top), bias=bias, scores=scores, groups=groups, top_groups=top, group_score="top2")
+        bias[bias == -torch.inf] = float("nan")
+        got = tbe.route(x, min(6, per * top), bias=bias, scores=scores, groups=groups, top_groups=top, group_score="top2")
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), name
+
+
 def test_strided_rows_and_outputs():
     wide = logits_of(60, 90, torch.bfloat16, seed=4)
     view = wide[:, 3:80]
