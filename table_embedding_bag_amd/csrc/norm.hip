@@ -417,10 +417,11 @@ hipError_t launch_backward(const NormArgs& a, hipStream_t s) {
       constexpr int NW = nw, C = c;
       const unsigned blocks = static_cast<unsigned>(a.blocks);
       if constexpr (NW == 0) {
-        if (a.dx)
-          hipLaunchKernelGGL((norm_backward_long<ST>), grid_of(a.rows), dim3(1024), 0, s, a);
+        // the sums first: dx may lie where the gradient does
         if (a.parts)
           hipLaunchKernelGGL((norm_sums_long<ST>), dim3(blocks, columns), dim3(kBlock), 0, s, a);
+        if (a.dx)
+          hipLaunchKernelGGL((norm_backward_long<ST>), grid_of(a.rows), dim3(1024), 0, s, a);
       } else {
         hipLaunchKernelGGL((norm_backward<ST, NW, C>), dim3(blocks), dim3(NW == 1 ? kBlock : NW * 64), 0, s,
                            a);

@@ -127,6 +127,20 @@ def test_in_place():
     assert torch.equal(z, y)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("N,D", [(300, 130), (77, 1000), (60, 4096), (30, 8192), (20, 16384), (9, 20001)])
+def test_every_gradient_in_place(N, D, dtype):
+    """dx into grad itself: the weight's and the bias's gradients are of what grad held before."""
+    x, w, b, grad = inputs(N, D, DTYPES[dtype], seed=14)
+    y, stats = tbe.layer_norm(x, w, b)
+    want = tbe.layer_norm_backward(x, stats, grad, weight=w, bias=True)
+    check(x, w, b, grad, got=(y, stats, *want))
+    got = tbe.layer_norm_backward(x, stats, grad, weight=w, bias=True, out=grad)
+    assert got[0] is grad
+    for name, p, q in zip(("dx", "dweight", "dbias"), got, want):
+        assert torch.equal(p, q), name
+
+
 def test_same_bits_every_time():
     a = inputs(9000, 520, torch.float16, seed=11)
     one = [tbe.layer_norm(*a[:3])]
