@@ -7,7 +7,8 @@
 // outputs, and the next row's are on their way meanwhile.  32768 x 4096 bf16: forward
 // 96 us (5.6 TB/s), backward 163 us (4.9 TB/s; 191 with the weight read for every row, 250
 // without the next row's loads).  The gradients over the rows are summed by each workgroup
-// for its rows, then over the workgroups, in a fixed order.
+// for its rows, at most 512 in a row in fp32, then over the workgroups in 64 bits, in a fixed order:
+// their rounding does not grow with the rows.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -338,24 +339,25 @@ __global__ __launch_bounds__(kBlock) void norm_sums_long(NormArgs a) {
   }
 }
 
-// The workgroups' sums to the gradients, 16 columns a workgroup, 64 of them at a time.
+// The workgroups' sums to the gradients, 16 columns a workgroup, 64 of them at a time; in 64 bits,
+// as there may be many.
 template <int ST>
 __global__ __launch_bounds__(1024) void norm_join(NormArgs a) {
-  __shared__ float part[64][16];
+  __shared__ double part[64][16];
   const int column = threadIdx.x & 15, w = threadIdx.x >> 4, which = blockIdx.y;
   void* out = which == 0 ? a.dweight : a.dbias;
   if (!out) return;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 16 + column;
-  float s = 0.0f;
+  double s = 0.0;
   if (c < a.cols)
 #pragma unroll 8
     for (int64_t b = w; b < a.blocks; b += 64) s += a.parts[(2 * b + which) * a.cols + c];
   part[w][column] = s;
   __syncthreads();
   if (w == 0 && c < a.cols) {
-    s = 0.0f;
+    s = 0.0;
     for (int i = 0; i < 64; ++i) s += part[i][column];
-    store_one<ST>(out, c, s);
+    store_one<ST>(out, c, static_cast<float>(s));
   }
 }
 
@@ -365,13 +367,15 @@ constexpr int64_t kMaxCols = int64_t{1} << 20;
 // with 8192 of them, 108 with 1024, 100 with one a row; the backward pass, which has as many
 // sums to join, 163 with 512, 179 with 1024, 242 with 256.
 constexpr int64_t kMaxGrid = 8192, kBackwardGrid = 512;
+constexpr int64_t kMaxTerms = 512;  // of a workgroup's sums over its rows: beyond, more workgroups
 
 dim3 grid_of(int64_t blocks) { return dim3(static_cast<unsigned>(std::min(blocks, kMaxGrid))); }
 
 int64_t backward_blocks(int64_t rows, int64_t cols, int32_t dtype) {
   const int64_t e = 16 / dtype_bytes(dtype);
   const int64_t each = cols <= 128 * e ? kWavesPerBlock : 1;  // rows of a workgroup at a time
-  return std::max<int64_t>(1, std::min<int64_t>((rows + each - 1) / each, kBackwardGrid));
+  const int64_t steps = (rows + each - 1) / each;
+  return std::max(std::max<int64_t>(1, std::min(steps, kBackwardGrid)), (steps + kMaxTerms - 1) / kMaxTerms);
 }
 
 size_t parts_bytes(int64_t rows, int64_t cols, int32_t dtype) {

@@ -141,6 +141,28 @@ def test_every_gradient_in_place(N, D, dtype):
         assert torch.equal(p, q), name
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("N,D", [(1 << 24, 8), (4000001, 520), (300007, 1100), (200001, 16400)])
+def test_sums_whose_rounding_does_not_grow_with_the_rows(N, D, dtype):
+    """Equal rows (one, N times over), whose terms' roundings all go the same way: whatever N is, a sum
+    is off by at most 512 + 8 half steps of fp32, those of 512 terms and of what joins them."""
+    t = DTYPES[dtype]
+    g = torch.Generator().manual_seed(15)
+    x = torch.randn(1, D, generator=g).to(t).cuda()
+    grad = (torch.rand(1, D, generator=g) + 1 / 3).to(t).cuda()
+    grad *= 2.0 ** -10      # fp16's sums stay below its largest value
+    w = torch.ones(D, dtype=t, device="cuda")
+    _, stats = tbe.layer_norm(x, w, w)
+    _, dw, db = tbe.layer_norm_backward(x.expand(N, D), stats.expand(N, 2).contiguous(), grad.expand(N, D), weight=w,
+                                        bias=True, need_dx=False)
+    # one row's terms, exact for the bias; the weight's as the kernel has them, in fp32: a difference and
+    # two products
+    n = (x.double() - stats[:, :1].double()) * stats[:, 1:].double()
+    for got, one, own in ((dw, grad.double() * n, 3), (db, grad.double(), 0)):
+        want = N * one[0]
+        ref.assert_close(got, want, (520 + own) * ref.U32 * want.abs(), "sum")
+
+
 def test_same_bits_every_time():
     a = inputs(9000, 520, torch.float16, seed=11)
     one = [tbe.layer_norm(*a[:3])]
