@@ -490,7 +490,8 @@ tbe_status tbe_layer_norm_sizes(int64_t rows, int64_t cols, int32_t dtype, size_
 /* Its gradients from that of y, grad [rows, cols]: dx [rows, cols], dweight and
  * dbias [cols], each NULL where not wanted; without the latter two no workspace
  * is needed.  weight: that of the forward call (NULL: ones).  dx may be grad
- * itself (same stride).  No rows: dweight and dbias are zeros. */
+ * itself (same stride).  No rows: dweight and dbias are zeros; else they are
+ * sums of at most 512 terms in fp32, joined in 64 bits. */
 tbe_status tbe_layer_norm_backward(const void* x, int64_t x_stride, const float* stats,
                                    const void* grad, int64_t grad_stride, const void* weight,
                                    void* dx, int64_t dx_stride, void* dweight, void* dbias,
@@ -589,7 +590,12 @@ tbe_status tbe_softmax_loss(const void* x, int64_t x_stride, const void* table,
 
 /* Its gradients from those of the losses, grad fp32 [rows], and the forward
  * call's lse: dx [rows, dim] and dtable [vocab, dim] (contiguous), each NULL
- * where not wanted. */
+ * where not wanted.  Of 2-byte rows the logits' gradients are rounded to the
+ * rows' type (fp16: times one power of two for all rows) before the products
+ * with the table and x, as the matrix cores take operands of that type; sums are
+ * fp32.  That adds about as much error again as the outputs' own rounding (2048
+ * rows, 100000 x 128, bf16: dx off by 0.0024 of its norm, 0.0017 were it rounded
+ * alone).  fp32 rows lose nothing so. */
 tbe_status tbe_softmax_loss_backward(const void* x, int64_t x_stride, const void* table,
                                      int64_t table_stride, const void* targets,
                                      int32_t index_dtype, double scale, const float* lse,

@@ -4,9 +4,10 @@
 // The squares are summed after the mean is subtracted, in fp32.
 //
 // Memory bounds both passes: a row's values stay in registers between its sums and its
-// outputs, and the next row's are on their way meanwhile.  32768 x 4096 bf16: forward
-// 96 us (5.6 TB/s), backward 163 us (4.9 TB/s; 191 with the weight read for every row, 250
-// without the next row's loads).  The gradients over the rows are summed by each workgroup
+// outputs, and the next row's are on their way meanwhile.  32768 x 4096 bf16, one call after
+// the other: forward 96 us (5.6 TB/s), backward 160 us (5.0 TB/s; about 190 with the weight read for
+// every row, 250 without the next row's loads) and its join 8; under the profiler, between other
+// kernels, 86 to 94 and 163 to 195.  The gradients over the rows are summed by each workgroup
 // for its rows, at most 512 in a row in fp32, then over the workgroups in 64 bits, in a fixed order:
 // their rounding does not grow with the rows.
 #include <hip/hip_runtime.h>
@@ -364,8 +365,8 @@ __global__ __launch_bounds__(1024) void norm_join(NormArgs a) {
 constexpr int64_t kMaxRows = int64_t{1} << 30;
 constexpr int64_t kMaxCols = int64_t{1} << 20;
 // Workgroups; each takes every so many-th row.  32768 x 4096 bf16: the forward pass 96 us
-// with 8192 of them, 108 with 1024, 100 with one a row; the backward pass, which has as many
-// sums to join, 163 with 512, 179 with 1024, 242 with 256.
+// with 8192 of them, 105 with 1024, 92 to 100 with one a row; the backward pass, which has as
+// many sums to join, 168 with 512 (and the join), 183 with 1024, 238 with 256.
 constexpr int64_t kMaxGrid = 8192, kBackwardGrid = 512;
 constexpr int64_t kMaxTerms = 512;  // of a workgroup's sums over its rows: beyond, more workgroups
 

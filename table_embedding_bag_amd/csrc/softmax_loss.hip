@@ -6,7 +6,9 @@
 // The logits z are never kept: the forward pass reduces each tile of them to a row's
 // sum of powers, the backward pass computes them again, one piece of the vocabulary at a
 // time, and holds that piece's d in the rows' type (the one rounding beside the outputs')
-// for the two products that read it.
+// for the two products that read it: the matrix cores take 2-byte operands ten times as fast as
+// fp32 ones.  2048 rows, 100000 x 128, bf16: dx is off by 0.0024 of its norm, dtable by 0.0021, where
+// the rounding of the output alone makes 0.0017 of both.
 //
 // The matrix cores bound it: four products of 2 N V K operations, five for narrow rows
 // (loss_narrow.hpp), whose gradients each compute the logits.  16384 rows, 131072 outputs of 512,

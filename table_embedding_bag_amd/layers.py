@@ -435,9 +435,9 @@ def route(logits, k, scores="softmax", bias=None, groups=1, top_groups=1, group_
     ("top2") are chosen first.  Returns (ids int32 [N, k], best first, weights fp32 [N, k]): the
     chosen experts' scores, divided by their sum (renormalize), times scale.
 
-    The choice is that of exact arithmetic, equal scores going to the lower index.  A NaN logit
-    counts as -inf; an expert at -inf has the score 0 and, if chosen for want of others, the
-    weight 0.  E up to 1024, k and groups up to 16.
+    The choice is that of exact arithmetic, down to differences of 64-bit rounding, equal scores
+    going to the lower index.  A NaN logit or bias counts as -inf; an expert whose logit is -inf has
+    the score 0 and, if chosen for want of others, the weight 0.  E up to 1024, k and groups up to 16.
     """
     kind = _scores(scores)
     if group_score not in _GROUP_SCORE:
@@ -651,6 +651,8 @@ def softmax_loss_backward(x, table, targets, lse, grad, scale=1.0, need_dx=True,
     losses, grad fp32 [N].
 
     Rows without a target have no part in either, whatever they hold.  What is not asked for is None.
+    Of fp16 and bf16 rows the logits' gradients are rounded to that type before the products that give
+    dx and dtable (fp32 sums): about as much error again as from the outputs' own rounding.
     """
     xs, ts, N, V, D, _, nw = _loss(x, table, targets, scale)
     _dense(lse, "lse", torch.float32, (N,))
