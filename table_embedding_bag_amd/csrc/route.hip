@@ -14,11 +14,12 @@
 //
 // The second look bounds it, where there is one (32768 x 256 bf16, 8 of them in 4 of 8 groups by
 // sigmoid + bias: 17 MB, 4 us at a copy's rate): 22 us where no row is in doubt (15 by the logits
-// themselves), 43 with biases that differ, where 0.7% of the rows are and a few late waves work on
+// themselves), 43 with biases that differ, where 0.8% of the rows are and a few late waves work on
 // alone, and 76 with biases of 0, where equal logits put a third of the rows in doubt.  By the
-// logits themselves instructions do: 1000 a wave, vector units busy in 58%.  Backward 11 us for 18 MB: the chosen experts' values go
-// through LDS (conflicts in two thirds of its cycles) between two barriers.  A row has 16 lanes
-// where that leaves a lane 16 experts at most, so that four rows share a wave's steps.
+// logits themselves instructions do: 1000 a wave, vector units busy in 58%.  Backward 11 us for
+// 18 MB: the chosen experts' values go through LDS (conflicts in two thirds of its cycles) between
+// two barriers.  A row has 16 lanes where that leaves a lane 16 experts at most, so that four rows
+// share a wave's steps.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
